@@ -1,7 +1,8 @@
 """Orthonormalized optimizer step (Dion power iteration, Muon Newton-Schulz)
 on one NVIDIA GB300.
 
-A thin ctypes binding over libdion.so (C ABI in include/dion.h).  The binding
+A thin ctypes binding over libdion.so (C ABI in include/dion.h and, for the
+8-bit linear layer's operators, include/dion_q8.h).  The binding
 only marshals arguments: every step of the computation runs in libdion's CUDA
 kernels.  PyTorch supplies device memory and the current CUDA stream.  If
 libdion.so is missing the import of a function raises; there is no fallback.
@@ -9,6 +10,11 @@ libdion.so is missing the import of a function raises; there is no fallback.
     from orthonormal_optimizer_step_gb300 import dion_step_batched, muon_ns_batched
     dion_step_batched(X, G, M, Q, mu=0.95, lr=0.01, weight_decay=0.01)
     muon_ns_batched(G, X=X, M=M, head_dim=64)
+
+    from orthonormal_optimizer_step_gb300 import dion_q8_quantize, dion_q8_matmul, dion_rms_norm_q8
+    w8, w8t = dion_q8_quantize(W, form="both", square=True)
+    x8, h, rstd = dion_rms_norm_q8(x, weight, residual=r)
+    y = dion_q8_matmul(x8, w8)
 """
 from __future__ import annotations
 
@@ -23,11 +29,14 @@ LIB_PATH = os.path.join(_PKG, "libdion.so")
 DION_OK, DION_ERR_INVALID_ARG, DION_ERR_UNSUPPORTED, DION_ERR_WORKSPACE, DION_ERR_CUDA, DION_ERR_NUMERIC = range(6)
 DION_F32, DION_BF16 = 0, 1
 
-# The exported symbols of include/dion.h.
+# The exported symbols of include/dion.h and include/dion_q8.h.
 EXPORTS = ("dion_workspace_size", "dion_workspace_panels", "dion_step_batched", "dion_step_batched_dev",
            "dion_step_batched_static", "muon_workspace_size", "muon_ns_batched",
            "dion_get_status", "dion_status_string", "dion_profile_begin", "dion_profile_end",
-           "dion_profile_count", "dion_profile_entry", "dion_profile_dropped")
+           "dion_profile_count", "dion_profile_entry", "dion_profile_dropped",
+           # include/dion_q8.h
+           "dion_q8_quantize", "dion_q8_matmul", "dion_rms_norm_q8", "dion_rms_norm_backward_workspace_size",
+           "dion_rms_norm_backward")
 
 # Muon's published quintic Newton-Schulz coefficients (a, b, c).
 QUINTIC = (3.4445, -4.7750, 2.0315)
@@ -45,6 +54,8 @@ class DionError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libdion.so with argument types declared (raises if not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -70,10 +81,20 @@ def lib() -> ctypes.CDLL:
         L.dion_profile_dropped.argtypes = []
         L.dion_profile_entry.argtypes = [c_int, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(c_int),
                                          ctypes.POINTER(ctypes.c_double)]
+        ll = ctypes.c_longlong
+        L.dion_q8_quantize.argtypes = ([c_int] * 4 + [vp, ll, ll, vp, vp, c_int, c_int, c_int]
+                                       + [vp, ll, ll] * 4 + [vp])
+        L.dion_q8_matmul.argtypes = ([c_int] * 3 + [vp, ll, c_int, vp, ll, c_int] * 2 + [vp, ll, c_int, vp, vp])
+        L.dion_rms_norm_q8.argtypes = ([c_int] * 3 + [vp, ll, vp, ll, vp, c_int, c_float, vp, ll, c_int]
+                                       + [vp, ll, vp, ll, vp, vp])
+        L.dion_rms_norm_backward_workspace_size.argtypes = [c_int, c_int, ctypes.POINTER(c_size)]
+        L.dion_rms_norm_backward.argtypes = ([c_int] * 3 + [vp, ll, vp, ll, vp, vp, c_int, vp, ll, vp, ll]
+                                             + [vp, vp, c_size, vp])
         for f in ("dion_workspace_size", "dion_workspace_panels", "dion_step_batched", "dion_step_batched_dev",
                   "dion_step_batched_static", "muon_workspace_size", "muon_ns_batched",
                   "dion_get_status", "dion_profile_begin", "dion_profile_end", "dion_profile_count",
-                  "dion_profile_entry", "dion_profile_dropped"):
+                  "dion_profile_entry", "dion_profile_dropped", "dion_q8_quantize", "dion_q8_matmul",
+                  "dion_rms_norm_q8", "dion_rms_norm_backward_workspace_size", "dion_rms_norm_backward"):
             getattr(L, f).restype = c_int
         _lib = L
         return L
@@ -267,3 +288,7 @@ class profile:
             out[name.value.decode()] = (launches.value, ms.value)
         self.result = out
         return out
+
+
+from .q8 import (Q8, dion_q8_matmul, dion_q8_quantize, dion_q8_status, dion_rms_norm_backward,  # noqa: E402
+                 dion_rms_norm_backward_workspace_size, dion_rms_norm_q8, new_q8)

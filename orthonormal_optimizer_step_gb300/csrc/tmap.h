@@ -6,7 +6,7 @@
 
 namespace dion {
 
-enum class TmapType { BF16, F32 };
+enum class TmapType { BF16, F32, U8 };
 
 // A [batch][rows][inner] tensor with the given pitches; boxes of
 // box_rows x box_inner elements land in shared memory with the 128-byte

@@ -1,0 +1,340 @@
+"""The 8-bit linear layer's operators (C ABI in include/dion_q8.h).
+
+A quantized matrix is the pair Q8(data, scale): `data` [rows, cols] in
+torch.float8_e4m3fn or torch.float8_e5m2, rows starting on 16-byte boundaries,
+and `scale` [rows, ceil(cols / 128)] in torch.float8_e8m0fnu, one power of two
+for each 1 x 128 block (or [ceil(rows / 128), ceil(cols / 128)], one for each
+128 x 128 block), rows starting on 4-byte boundaries.  `new_q8` allocates one
+that meets this for any size; tensors of a program's own may be passed as well.
+
+    w8, w8t = dion_q8_quantize(W, form="both", square=True)      # weights, both orders
+    x8, h, rstd = dion_rms_norm_q8(x, weight, residual=r)        # layer input
+    y = dion_q8_matmul(x8, w8)                                   # y = x8 w8^T
+    dy8, dy8t = dion_q8_quantize(dy, form="both")
+    _, x8t = dion_q8_quantize(h, form="cols", rstd=rstd, weight=weight)
+    dx = dion_q8_matmul(dy8, w8t)
+    G = dion_q8_matmul(dy8t, x8t)                                # the step's gradient
+    dh, dweight = dion_rms_norm_backward(dx, h, rstd, weight, dh=dh)
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+import orthonormal_optimizer_step_gb300 as _od
+
+_E4M3, _E5M2, _E8M0 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu
+_F32 = torch.float32
+_FORMATS = {_E4M3: 0, _E5M2: 1}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_status = {}
+
+
+class Q8(NamedTuple):
+    """A quantized matrix (or a batch of them): 8-bit values and block scales."""
+    data: torch.Tensor
+    scale: torch.Tensor
+
+
+# ---- checks and layout (the calls below are short: a few microseconds of host time count)
+def _type(dtype, what):
+    code = _TYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {dtype}")
+    return code
+
+
+def _format(dtype):
+    code = _FORMATS.get(dtype)
+    if code is None:
+        raise TypeError(f"8-bit format must be torch.float8_e4m3fn or torch.float8_e5m2, got {dtype}")
+    return code
+
+
+def _cuda(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _pitch(rows, cols, ld, one, what):
+    """Row pitch in elements of a rows x cols matrix with strides (ld, one): its rows are contiguous and apart."""
+    if cols > 1 and one != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    if rows <= 1 or cols == 0:
+        return (cols + 15) // 16 * 16        # no second row: any pitch will do
+    if ld < cols:
+        raise ValueError(f"{what} must not have overlapping rows")
+    return ld
+
+
+def _matrix(t, what):
+    """(matrix of t's rows, row pitch) of a tensor [..., cols], without a copy."""
+    if t.dim() != 2:
+        if t.dim() < 2:
+            raise ValueError(f"{what} must have at least two dimensions")
+        try:
+            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{what} must be viewable as a matrix of rows") from None
+    return t, _pitch(*t.shape, *t.stride(), what)
+
+
+def _vector(t, n, what):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {n}")
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory from the pool of the stream that the call runs on, so that what
+    another stream's work still uses is not written early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def new_q8(rows, cols, *, dtype=_E4M3, square=False, batch=None, device="cuda", stream=None):
+    """An uninitialized quantized matrix (`batch` of them) with aligned rows."""
+    _format(dtype)
+    sr, sc = ((rows + 127) // 128 if square else rows), (cols + 127) // 128
+    ld, lds = (cols + 15) // 16 * 16, (sc + 3) // 4 * 4
+    lead = () if batch is None else (batch,)
+    data = _empty(lead + (rows, ld), dtype, device, stream)
+    scale = _empty(lead + (sr, lds), _E8M0, device, stream)
+    return Q8(data if ld == cols else data[..., :cols], scale if lds == sc else scale[..., :sc])
+
+
+def _q8(q, what):
+    """(rows, cols, format, data pitch, scale pitch, square) of a quantized matrix."""
+    data, scale = q
+    fmt = _format(data.dtype)
+    if scale.dtype is not _E8M0:
+        raise TypeError(f"{what}: scales must be torch.float8_e8m0fnu, got {scale.dtype}")
+    shape, sshape, stride, sstride = data.shape, scale.shape, data.stride(), scale.stride()
+    if len(shape) != len(sshape) or not 2 <= len(shape) <= 3 or shape[:-2] != sshape[:-2]:
+        raise ValueError(f"{what}: {tuple(sshape)} scales do not fit {tuple(shape)} values")
+    rows, cols = shape[-2], shape[-1]
+    sr, sc = sshape[-2], sshape[-1]
+    if sc != (cols + 127) // 128 or (sr != rows and sr != (rows + 127) // 128):
+        raise ValueError(f"{what}: {tuple(sshape)} scales do not fit {tuple(shape)} values")
+    ld = _pitch(rows, cols, stride[-2], stride[-1], what)
+    lds = _pitch(sr, sc, sstride[-2], sstride[-1], what)
+    if ld % 16 or data.data_ptr() % 16:
+        raise ValueError(f"{what}: rows must start on 16-byte boundaries")
+    if lds % 4 or scale.data_ptr() % 4:
+        raise ValueError(f"{what}: scale rows must start on 4-byte boundaries")
+    return rows, cols, fmt, ld, lds, sr != rows
+
+
+def _out_q8(q, rows, cols, dtype, square, batch, what="out"):
+    """(data pitch, scale pitch) of a quantized matrix that a call is to write."""
+    r, c, _, ld, lds, _ = _q8(q, what)
+    shape = (rows, cols) if batch is None else (batch, rows, cols)
+    if tuple(q.data.shape) != shape or q.data.dtype is not dtype or q.scale.shape[-2] != ((rows + 127) // 128 if square else rows):
+        raise ValueError(f"{what} does not have the shape, dtype and scales asked for")
+    return ld, lds
+
+
+# ---- status word of the products
+def _status_word(dev, device):
+    w = _status.get(dev)
+    if w is None:
+        w = _status[dev] = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.current_stream(device).synchronize()   # once: later calls may run on any stream
+    return w.data_ptr()
+
+
+def dion_q8_status(device=None) -> int:
+    """Status word of dion_q8_matmul on a device (synchronize first): 0, or 4
+    once any of its calls gave up waiting (their results are undefined)."""
+    dev = torch.device("cuda" if device is None else device).index
+    w = _status.get(torch.cuda.current_device() if dev is None else dev)
+    return 0 if w is None else int(w.item())
+
+
+# ---- operators
+def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, weight=None, out=None, stream=None):
+    """Quantizes x [rows, cols] or [batch, rows, cols] (float32 or bfloat16).
+
+    form "rows": x with blocks along its rows; "cols": its transpose, with blocks
+    down x's columns; "both": the two from one read.  Returns (rows, cols), each
+    a Q8 or None.  square: one scale for each 128 x 128 block.  With rstd [rows]
+    and weight [cols], x * rstd * weight is quantized instead of x.  out: the
+    pair (rows, cols) to write into."""
+    if form not in ("rows", "cols", "both"):
+        raise ValueError(f"form must be 'rows', 'cols' or 'both', got {form!r}")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 2 and len(shape) != 3:
+        raise ValueError("expected a [rows, cols] or [batch, rows, cols] tensor")
+    dt, fmt, dev = _type(x.dtype, "x"), _format(dtype), _cuda(x, "x")
+    rows, cols = shape[-2], shape[-1]
+    batch = shape[0] if len(shape) == 3 else None
+    wdt, rptr, wptr = 0, None, None
+    if rstd is not None or weight is not None:
+        if rstd is None or weight is None or batch is not None:
+            raise ValueError("rstd and weight go together, with a [rows, cols] tensor")
+        if rstd.dtype is not _F32:
+            raise TypeError(f"rstd must be float32, got {rstd.dtype}")
+        wdt = _type(weight.dtype, "weight")
+        _vector(weight, cols, "weight")
+        _vector(rstd, rows, "rstd")
+        _same_device(dev, rstd=rstd, weight=weight)
+        rptr, wptr = rstd.data_ptr(), weight.data_ptr()
+    ldx = _pitch(rows, cols, stride[-2], stride[-1], "x")
+    pair, args = [None, None], []
+    for i, r, c in ((0, rows, cols), (1, cols, rows)):
+        if form == ("cols", "rows")[i]:
+            args += (None, 0, 0, None, 0, 0)
+            continue
+        if out is None or out[i] is None:
+            q = new_q8(r, c, dtype=dtype, square=square, batch=batch, device=x.device, stream=stream)
+            ld, lds = (c + 15) // 16 * 16, ((c + 127) // 128 + 3) // 4 * 4
+        else:
+            q = out[i]
+            ld, lds = _out_q8(q, r, c, dtype, square, batch)
+            _same_device(dev, out=q.data, out_scale=q.scale)
+        pair[i] = q
+        data, scale = q
+        if batch is None:
+            args += (data.data_ptr(), ld, 0, scale.data_ptr(), lds, 0)
+        else:
+            args += (data.data_ptr(), ld, data.stride(0), scale.data_ptr(), lds, scale.stride(0))
+    if rows == 0 or cols == 0 or batch == 0:
+        return pair[0], pair[1]
+    code = _od.lib().dion_q8_quantize(1 if batch is None else batch, rows, cols, dt, x.data_ptr(), ldx,
+                                      0 if batch is None else stride[0], rptr, wptr, wdt, square, fmt, *args,
+                                      _raw_stream(stream, dev))
+    _od._check(code, "dion_q8_quantize")
+    return pair[0], pair[1]
+
+
+def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
+    """a b^T [m, n] of quantized matrices a [m, k] and b [n, k], in float32 sums
+    rounded once to out_dtype (bfloat16 or float32; that of `out` if given)."""
+    m, k, af, lda, ldsa, a_sq = _q8(a, "a")
+    n, k2, bf, ldb, ldsb, b_sq = _q8(b, "b")
+    if k != k2 or a.data.dim() != 2 or b.data.dim() != 2:
+        raise ValueError(f"expected [m, k] and [n, k], got {tuple(a.data.shape)} and {tuple(b.data.shape)}")
+    dev = _cuda(a.data, "a")
+    if out is None:
+        ct = _type(out_dtype, "out_dtype")
+        out = _empty((m, n), out_dtype, a.data.device, stream)
+        ldc = n
+    else:
+        if out.shape != (m, n):
+            raise ValueError(f"out must be {m} x {n}, got {tuple(out.shape)}")
+        ct, ldc = _type(out.dtype, "out"), _pitch(m, n, *out.stride(), "out")
+    if not dev == a.scale.get_device() == b.data.get_device() == b.scale.get_device() == out.get_device():
+        _same_device(dev, a_scale=a.scale, b=b.data, b_scale=b.scale, out=out)
+    code = _od.lib().dion_q8_matmul(m, n, k, a.data.data_ptr(), lda, af, a.scale.data_ptr(), ldsa, a_sq,
+                                    b.data.data_ptr(), ldb, bf, b.scale.data_ptr(), ldsb, b_sq, out.data_ptr(),
+                                    ldc, ct, _status_word(dev, a.data.device), _raw_stream(stream, dev))
+    _od._check(code, "dion_q8_matmul")
+    return out
+
+
+def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None, out=None, rstd=None, stream=None):
+    """h = x + residual; the rows of h / sqrt(mean(h^2) + eps) * weight, quantized.
+
+    x, residual [..., cols] (float32 or bfloat16), weight [cols].  Returns
+    (y, h, rstd): the Q8 of all rows, the sum in x's type and shape (x itself
+    without a residual; `h` may be given, also as x or residual) and
+    1 / sqrt(mean(h^2) + eps) of each row, which the backward pass reads."""
+    xdt = x.dtype
+    dt, dev, device = _type(xdt, "x"), _cuda(x, "x"), x.device
+    x2, ldx = _matrix(x, "x")
+    rows, cols = x2.shape
+    wdt = _type(weight.dtype, "weight")
+    _vector(weight, cols, "weight")
+    rptr, ldr, hptr, ldh = None, 0, None, 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype is not xdt:
+            raise ValueError("residual must have x's shape and dtype")
+        if h is None:
+            h = _empty(x.shape, xdt, device, stream)
+        elif h.shape != x.shape or h.dtype is not xdt:
+            raise ValueError("h must have x's shape and dtype")
+        r2, ldr = _matrix(residual, "residual")
+        h2, ldh = _matrix(h, "h")
+        rptr, hptr = r2.data_ptr(), h2.data_ptr()
+        _same_device(dev, residual=residual, h=h)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    if out is None:
+        out = new_q8(rows, cols, dtype=dtype, device=device, stream=stream)
+        fmt, ldq, lds = _FORMATS[dtype], (cols + 15) // 16 * 16, ((cols + 127) // 128 + 3) // 4 * 4
+    else:
+        fmt = _format(out.data.dtype)
+        ldq, lds = _out_q8(out, rows, cols, out.data.dtype, False, None)
+        _same_device(dev, out=out.data, out_scale=out.scale)
+    if rstd is None:
+        rstd = _empty((rows,), _F32, device, stream)
+    else:
+        if rstd.dtype is not _F32:
+            raise TypeError(f"rstd must be float32, got {rstd.dtype}")
+        _vector(rstd, rows, "rstd")
+    _same_device(dev, weight=weight, rstd=rstd)
+    if rows and cols:
+        code = _od.lib().dion_rms_norm_q8(rows, cols, dt, x2.data_ptr(), ldx, rptr, ldr, weight.data_ptr(), wdt, eps,
+                                          hptr, ldh, fmt, out.data.data_ptr(), ldq, out.scale.data_ptr(), lds,
+                                          rstd.data_ptr(), _raw_stream(stream, dev))
+        _od._check(code, "dion_rms_norm_q8")
+    return out, (x if residual is None else h), rstd
+
+
+def dion_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _od._check(_od.lib().dion_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)),
+               "dion_rms_norm_backward_workspace_size")
+    return out.value
+
+
+def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients (dx, dweight) of dion_rms_norm_q8 from dy, the gradient of its
+    (unquantized) rows, and dh, that of h along the residual stream, which is
+    added to dx.  dx is the gradient of both x and residual and may be dy or dh
+    itself; dweight is float32."""
+    ydt, shape = dy.dtype, dy.shape
+    dt, dev, device = _type(ydt, "dy"), _cuda(dy, "dy"), dy.device
+    if dx is None:
+        dx = _empty(shape, ydt, device, stream)
+    for name, t in (("h", h), ("dh", dh), ("dx", dx)):
+        if t is not None and (t.shape != shape or t.dtype is not ydt):
+            raise ValueError(f"{name} must have dy's shape and dtype")
+    (y2, ldy), (h2, ldh), (x2, ldx) = _matrix(dy, "dy"), _matrix(h, "h"), _matrix(dx, "dx")
+    dptr, lddh = None, 0
+    if dh is not None:
+        d2, lddh = _matrix(dh, "dh")
+        dptr = d2.data_ptr()
+    rows, cols = y2.shape
+    wdt = _type(weight.dtype, "weight")
+    _vector(weight, cols, "weight")
+    if dweight is None:
+        dweight = _empty((cols,), _F32, device, stream)
+    if rstd.dtype is not _F32 or dweight.dtype is not _F32:
+        raise TypeError("rstd and dweight must be float32")
+    _vector(rstd, rows, "rstd")
+    _vector(dweight, cols, "dweight")
+    if workspace is None:
+        workspace = _empty((max(256, dion_rms_norm_backward_workspace_size(rows, cols)),), torch.uint8, device, stream)
+    _same_device(dev, h=h, rstd=rstd, weight=weight, dh=dh, dx=dx, dweight=dweight, workspace=workspace)
+    if cols:
+        code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh,
+                                                rstd.data_ptr(), weight.data_ptr(), wdt, dptr, lddh, x2.data_ptr(), ldx,
+                                                dweight.data_ptr(), workspace.data_ptr(),
+                                                workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+        _od._check(code, "dion_rms_norm_backward")
+    return dx, dweight
