@@ -78,6 +78,29 @@ cudaError_t launch(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 b
     return e;
 }
 
+// The same with thread-block clusters of `cluster` consecutive CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
+                           cudaStream_t s, Args&&... args)
+{
+    if (grid.x == 0 || grid.y == 0 || grid.z == 0) return cudaSuccess;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int slot = prof_begin(name, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    prof_end(slot, s);
+    return e;
+}
+
 // Raises a kernel's dynamic shared-memory limit on the current device, once
 // per device (the attribute is per device).  `done` is a bit mask of devices
 // already set up; concurrent first calls may both set the attribute, which is

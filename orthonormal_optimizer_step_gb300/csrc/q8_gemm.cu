@@ -47,26 +47,123 @@ __host__ uint32_t idesc_mx(int M, int N, uint32_t fmt_m, uint32_t fmt_n)
 }
 __device__ __forceinline__ uint32_t idesc_sf(uint32_t sel) { return (sel << 4) | (sel << 29); }
 
+// CG = 2: the two CTAs of a pair work on one tile, each with its 128 rows of B
+// and half of the tile's rows of A in its own shared memory; the pair's first
+// CTA issues for both.
+template <int CG>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 
 // 32 rows of 16 bytes from shared memory to 4 columns of tensor memory, in
 // each of the four lane quarters: one scale word of 128 operand rows (row r
-// in lane r % 32 of column r / 32).
+// in lane r % 32 of column r / 32).  CG = 2: in both CTAs, each from its own
+// shared memory.
+template <int CG>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr)
 {
     uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
     d |= (uint64_t)(128u >> 4) << 32;   // eight-row groups are 128 bytes apart
     d |= (uint64_t)1 << 46;             // descriptor version; no swizzle
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    if (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    if (CG == 1)
+        tc::mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(tc::smem_u32(bar)), "h"((uint16_t)3)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols)
+{
+    if (CG == 1) {
+        tc::tmem_alloc(slot, cols);
+        tc::tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(slot)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols)
+{
+    if (CG == 1)
+        tc::tmem_dealloc(taddr, cols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address, in the cluster's shared memory, of this CTA's variable in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
+    return r;
+}
+// Arrives on the first CTA's barrier.
+template <int CG>
+__device__ __forceinline__ void arrive_first(uint64_t* bar)
+{
+    if (CG == 1)
+        tc::mbar_arrive(bar);
+    else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(bar, 0)) : "memory");
+}
+// Orders what the peer wrote before its arrival after this thread's wait.
+template <int CG>
+__device__ __forceinline__ void acquire_peer()
+{
+    if (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+// TMA load into this CTA's shared memory that completes on the first CTA's barrier.
+template <int CG>
+__device__ __forceinline__ void tma_load(void* dst, const void* tmap, uint64_t* bar, uint32_t bar_first, int c0, int c1)
+{
+    if (CG == 1)
+        tc::tma_load_3d(dst, tmap, bar, c0, c1, 0);
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+            ::"r"(tc::smem_u32(dst)), "l"((uint64_t)tmap), "r"(bar_first), "r"(c0), "r"(c1), "r"(0)
+            : "memory");
 }
 
 // A kernel that gave up waiting leaves its last copies and MMAs a millisecond
@@ -80,15 +177,22 @@ __device__ __noinline__ void drain_after_abort()
 
 constexpr int kSfSlots = 4;
 
-template <int BN>
+template <int CG, int BN>
 struct Cfg {
-    static constexpr int BM = 128;                     // rows of B a tile
-    static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = BN * 128, STAGE = P_BYTES + Q_BYTES;
-    static constexpr int STAGES = BN >= 128 ? 6 : 8;
+    static constexpr int BM = 128;                     // rows of B that a CTA holds
+    static constexpr int QROWS = BN / CG;              // rows of A that a CTA holds
+    static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = QROWS * 128, STAGE = P_BYTES + Q_BYTES;
+    static constexpr int STAGES = QROWS >= 128 ? 6 : 8;
     static constexpr int SFQ = (BN + 127) / 128;       // 128-row scale groups of A's side
     static constexpr uint32_t SF_BYTES = 512 * (1 + SFQ);
     static constexpr uint32_t ACC = BN < 32 ? 32 : BN; // accumulator columns
-    static constexpr uint32_t SF_COL = 2 * ACC;        // scales: 4 (B) + 4 SFQ (A) columns a slot
+    // 512 columns hold two accumulators and the scales up to 128 columns wide.
+    // The 256-wide accumulator is single: its eight epilogue warps take it
+    // into registers whole (128 columns each) and release it before they store.
+    static constexpr int BUFS = BN > 128 ? 1 : 2;
+    static constexpr int EW = BN > 128 ? 8 : 4;        // epilogue warps
+    static constexpr int ECOLS = BN / (EW / 4);        // columns of one
+    static constexpr uint32_t SF_COL = BUFS * ACC;     // scales: 4 (B) + 4 SFQ (A) columns a slot
     static constexpr uint32_t SF_COLS = 4 + 4 * SFQ;
     static constexpr uint32_t TMEM = BN <= 32 ? 128 : BN <= 64 ? 256 : 512;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kSfSlots * SF_BYTES + 512;
@@ -111,11 +215,36 @@ __device__ __forceinline__ uint4 scale_words(const uint8_t* s, long long ld, int
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int BN, bool F32>
-__global__ void __launch_bounds__(256, 1)
+// Tile t of the grid: bands of eight row tiles of A, walked row tiles first, so
+// that the tiles in flight share both operands' panels in L2.
+__device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tm, int& tn)
+{
+    const int per_band = 8 * p.tiles_n, band = t / per_band, in = t - band * per_band;
+    const int rows = min(8, p.tiles_m - 8 * band);
+    tm = 8 * band + in % rows;
+    tn = in / rows;
+}
+
+// One accumulator column block of a warp: lane l holds column col of rows
+// row0 .. row0 + N - 1 of C.
+template <bool F32, int N>
+__device__ __forceinline__ void store_cols(const GemmParams& p, int row0, int col, const uint32_t (&v)[N])
+{
+    if (col >= p.n) return;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (row0 + j >= p.m) break;
+        const long long o = (long long)(row0 + j) * p.ldc + col;
+        if (F32) reinterpret_cast<float*>(p.c)[o] = __uint_as_float(v[j]);
+        else reinterpret_cast<bf16*>(p.c)[o] = __float2bfloat16_rn(__uint_as_float(v[j]));
+    }
+}
+
+template <int CG, int BN, bool F32>
+__global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     q8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const GemmParams p)
 {
-    using C = Cfg<BN>;
+    using C = Cfg<CG, BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sf = smem + C::STAGES * C::STAGE;
@@ -128,6 +257,7 @@ __global__ void __launch_bounds__(256, 1)
     uint32_t* tmem_slot = (uint32_t*)(acc_empty + 2);
     volatile int* abrt = (volatile int*)(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -135,26 +265,25 @@ __global__ void __launch_bounds__(256, 1)
             tc::mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < kSfSlots; ++s) {
-            tc::mbar_init(&sf_full[s], 1);
+            tc::mbar_init(&sf_full[s], CG);
             tc::mbar_init(&sf_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&acc_full[b], 1);
-            tc::mbar_init(&acc_empty[b], 4);
+            tc::mbar_init(&acc_empty[b], CG * C::EW);
         }
         *abrt = 0;
         tc::fence_mbar_init();
     }
-    if (warp == 1) {
-        tc::tmem_alloc(tmem_slot, C::TMEM);
-        tc::tmem_relinquish();
-    }
+    if (warp == 1) tmem_alloc<CG>(tmem_slot, C::TMEM);
     tc::tc_fence_before();
-    __syncthreads();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int tiles = p.tiles_m * p.tiles_n;
     const int kblocks = (p.k + 127) / 128;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -163,37 +292,40 @@ __global__ void __launch_bounds__(256, 1)
             int stage = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int tn = t % p.tiles_n, tm = t / p.tiles_n;
+            for (int t = first; t < tiles && ok; t += step) {
+                int tm, tn;
+                tile_of(p, t, tm, tn);
+                const int prow = (tn * CG + rank) * C::BM, qrow = tm * BN + rank * C::QROWS;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!(ok = tc::mbar_wait(&empty[stage], ph ^ 1, abrt, p.status))) break;
                     uint8_t* s = smem + stage * C::STAGE;
-                    tc::mbar_arrive_expect_tx(&full[stage], C::STAGE);
-                    tc::tma_load_3d(s, &tmP, &full[stage], kb * 128, tn * C::BM, 0);
-                    tc::tma_load_3d(s + C::P_BYTES, &tmQ, &full[stage], kb * 128, tm * BN, 0);
+                    const uint32_t bar = CG == 2 ? map_rank(&full[stage], 0) : 0;
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], CG * C::STAGE);
+                    tma_load<CG>(s, &tmP, &full[stage], bar, kb * 128, prow);
+                    tma_load<CG>(s + C::P_BYTES, &tmQ, &full[stage], bar, kb * 128, qrow);
                     if (++stage == C::STAGES) { stage = 0; ph ^= 1; }
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0, slot = 0, it = 0;
-            uint32_t ph = 0, sph = 0;
+        if (lane == 0 && rank == 0) {
+            int stage = 0, slot = 0, buf = 0;
+            uint32_t ph = 0, sph = 0, aph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
-                const int buf = it & 1;
-                if (!(ok = tc::mbar_wait(&acc_empty[buf], ((it >> 1) & 1) ^ 1, abrt, p.status))) break;
+            for (int t = first; t < tiles && ok; t += step) {
+                if (!(ok = tc::mbar_wait(&acc_empty[buf], aph ^ 1, abrt, p.status))) break;
                 tc::tc_fence_after();
                 const uint32_t d = tmem + buf * C::ACC;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     const uint32_t sfp = tmem + C::SF_COL + slot * C::SF_COLS, sfq = sfp + 4;
                     if ((kb & 3) == 0) {
                         if (!(ok = tc::mbar_wait(&sf_full[slot], sph, abrt, p.status))) break;
+                        acquire_peer<CG>();
                         tc::tc_fence_after();
                         const uint32_t src = tc::smem_u32(sf + slot * C::SF_BYTES);
-                        tmem_cp_scales(sfp, src);
+                        tmem_cp_scales<CG>(sfp, src);
 #pragma unroll
-                        for (int i = 0; i < C::SFQ; ++i) tmem_cp_scales(sfq + 4 * i, src + 512 * (1 + i));
+                        for (int i = 0; i < C::SFQ; ++i) tmem_cp_scales<CG>(sfq + 4 * i, src + 512 * (1 + i));
                     }
                     if (!(ok = tc::mbar_wait(&full[stage], ph, abrt, p.status))) break;
                     tc::tc_fence_after();
@@ -201,27 +333,29 @@ __global__ void __launch_bounds__(256, 1)
                     const uint32_t idesc = p.idesc | idesc_sf(kb & 3);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_mx(d, tc::make_sdesc(a0 + 32 * j, 16, 1024), tc::make_sdesc(b0 + 32 * j, 16, 1024), idesc,
-                               sfp, sfq, (kb | j) != 0);
-                    tc::mma_commit(&empty[stage]);
+                        mma_mx<CG>(d, tc::make_sdesc(a0 + 32 * j, 16, 1024), tc::make_sdesc(b0 + 32 * j, 16, 1024), idesc,
+                                   sfp, sfq, (kb | j) != 0);
+                    commit<CG>(&empty[stage]);
                     if (++stage == C::STAGES) { stage = 0; ph ^= 1; }
                     if ((kb & 3) == 3 || kb == kblocks - 1) {
-                        tc::mma_commit(&sf_empty[slot]);
+                        commit<CG>(&sf_empty[slot]);
                         if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
                     }
                 }
-                if (ok) tc::mma_commit(&acc_full[buf]);
+                if (ok) commit<CG>(&acc_full[buf]);
+                if (++buf == C::BUFS) { buf = 0; aph ^= 1; }
             }
         }
     } else if (warp == 2) {
         int slot = 0;
         uint32_t sph = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int tn = t % p.tiles_n, tm = t / p.tiles_n;
+        for (int t = first; t < tiles && ok; t += step) {
+            int tm, tn;
+            tile_of(p, t, tm, tn);
             for (int g = 0; 4 * g < kblocks; ++g) {
                 uint4 w[1 + C::SFQ];
-                w[0] = scale_words(p.sb, p.ldsb, p.sb_shift, p.sb_rows, tn * C::BM, C::BM, g, lane);
+                w[0] = scale_words(p.sb, p.ldsb, p.sb_shift, p.sb_rows, (tn * CG + rank) * C::BM, C::BM, g, lane);
 #pragma unroll
                 for (int i = 0; i < C::SFQ; ++i)
                     w[1 + i] = scale_words(p.sa, p.ldsa, p.sa_shift, p.sa_rows, tm * BN + 128 * i, BN - 128 * i, g, lane);
@@ -232,80 +366,92 @@ __global__ void __launch_bounds__(256, 1)
                 for (int i = 0; i < 1 + C::SFQ; ++i) dst[32 * i + lane] = w[i];
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sf_full[slot]);
+                if (lane == 0) arrive_first<CG>(&sf_full[slot]);
                 if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
             }
         }
     } else if (warp >= 4) {
         const int q = warp & 3;          // the lane quarter of tensor memory that this warp reads
-        int it = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
-            const int tn = t % p.tiles_n, tm = t / p.tiles_n;
-            const int buf = it & 1;
-            if (!tc::mbar_wait(&acc_full[buf], (it >> 1) & 1, abrt, p.status)) break;
+        const int c0 = (warp - 4) / 4 * C::ECOLS;
+        int buf = 0;
+        uint32_t aph = 0;
+        for (int t = first; t < tiles; t += step) {
+            int tm, tn;
+            tile_of(p, t, tm, tn);
+            if (!tc::mbar_wait(&acc_full[buf], aph, abrt, p.status)) break;
             tc::tc_fence_after();
-            const int col = tn * C::BM + q * 32 + lane;
-#pragma unroll 1
-            for (int j0 = 0; j0 < BN; j0 += 16) {
-                uint32_t v[16];
-                tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * C::ACC + j0, v);
-                tc::tmem_ld_wait();
-                const int row0 = tm * BN + j0;
-                if (col < p.n) {
+            const int col = (tn * CG + rank) * C::BM + q * 32 + lane;
+            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + buf * C::ACC + c0;
+            if constexpr (C::BUFS == 1) {
+                uint32_t v[C::ECOLS / 32][32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (row0 + j >= p.m) break;
-                        const long long o = (long long)(row0 + j) * p.ldc + col;
-                        if (F32) reinterpret_cast<float*>(p.c)[o] = __uint_as_float(v[j]);
-                        else reinterpret_cast<bf16*>(p.c)[o] = __float2bfloat16_rn(__uint_as_float(v[j]));
-                    }
+                for (int j = 0; j < C::ECOLS / 32; ++j) tc::tmem_ld32(src + 32 * j, v[j]);
+                tc::tmem_ld_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
+#pragma unroll
+                for (int j = 0; j < C::ECOLS / 32; ++j) store_cols<F32>(p, tm * BN + c0 + 32 * j, col, v[j]);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < C::ECOLS; j += 16) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(src + j, v);
+                    tc::tmem_ld_wait();
+                    store_cols<F32>(p, tm * BN + c0 + j, col, v);
                 }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
             }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
+            if (++buf == C::BUFS) { buf = 0; aph ^= 1; }
         }
     }
     __syncthreads();
     if (*abrt) drain_after_abort();
+    if (CG == 2) cluster_sync();         // the pair's barriers and tensor memory are both CTAs' until here
     if (warp == 1) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, C::TMEM);
+        tmem_dealloc<CG>(tmem, C::TMEM);
     }
 }
 
-template <int BN, bool F32>
+template <int CG, int BN, bool F32>
 cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
 {
-    using C = Cfg<BN>;
+    using C = Cfg<CG, BN>;
     static std::atomic<unsigned long long> attr{0};
-    cudaError_t e = smem_attr_once((const void*)q8_gemm_kernel<BN, F32>, (int)C::SMEM, attr);
+    cudaError_t e = smem_attr_once((const void*)q8_gemm_kernel<CG, BN, F32>, (int)C::SMEM, attr);
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmQ;
     if (!make_tmap_3d(&tmP, a.b, TmapType::U8, a.k, a.n, 1, a.ldb, a.ldb, 128, C::BM) ||
-        !make_tmap_3d(&tmQ, a.a, TmapType::U8, a.k, a.m, 1, a.lda, a.lda, 128, BN))
+        !make_tmap_3d(&tmQ, a.a, TmapType::U8, a.k, a.m, 1, a.lda, a.lda, 128, C::QROWS))
         return cudaErrorInvalidValue;
     GemmParams p{};
     p.m = a.m; p.n = a.n; p.k = a.k;
     p.tiles_m = (int)cdiv(a.m, BN);
-    p.tiles_n = (int)cdiv(a.n, C::BM);
+    p.tiles_n = (int)cdiv(a.n, C::BM * CG);
     p.sa = a.sa; p.ldsa = a.ldsa; p.sa_shift = a.a_square ? 7 : 0; p.sa_rows = a.a_square ? (int)cdiv(a.m, 128) : a.m;
     p.sb = a.sb; p.ldsb = a.ldsb; p.sb_shift = a.b_square ? 7 : 0; p.sb_rows = a.b_square ? (int)cdiv(a.n, 128) : a.n;
     p.c = a.c; p.ldc = a.ldc;
-    p.idesc = idesc_mx(C::BM, BN, (uint32_t)a.bfmt, (uint32_t)a.afmt);
+    p.idesc = idesc_mx(C::BM * CG, BN, (uint32_t)a.bfmt, (uint32_t)a.afmt);
     p.status = a.status;
     const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    return launch("q8_matmul", q8_gemm_kernel<BN, F32>, dim3((unsigned)std::min<long long>(tiles, num_sms())), dim3(256),
-                  C::SMEM, st, tmP, tmQ, p);
+    const unsigned grid = (unsigned)(CG * std::min<long long>(tiles, num_sms() / CG));
+    const dim3 block(128 + 32 * C::EW);
+    if (CG == 1)
+        return launch("q8_matmul", q8_gemm_kernel<CG, BN, F32>, dim3(grid), block, C::SMEM, st, tmP, tmQ, p);
+    return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, p);
 }
 
 template <bool F32>
 cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
 {
-    if (a.m <= 16) return gemm_go<16, F32>(a, st);
-    if (a.m <= 32) return gemm_go<32, F32>(a, st);
-    if (a.m <= 64) return gemm_go<64, F32>(a, st);
-    return gemm_go<128, F32>(a, st);
+    if (a.m <= 16) return gemm_go<1, 16, F32>(a, st);
+    if (a.m <= 32) return gemm_go<1, 32, F32>(a, st);
+    if (a.m <= 64) return gemm_go<1, 64, F32>(a, st);
+    if (a.m <= 128) return gemm_go<1, 128, F32>(a, st);
+    return gemm_go<2, 256, F32>(a, st);
 }
 
 }  // namespace
