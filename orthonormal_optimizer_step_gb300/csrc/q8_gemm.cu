@@ -121,6 +121,21 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
+// One lane of a converged warp.  The branch on it tells the compiler that one
+// thread runs: a branch on the lane number does not, and each tcgen05
+// instruction behind it then costs about 200 cycles of issue (a pair of MMAs of
+// 128 or of 256 columns alike took 205; measured at 4864 x 4096 x 32768).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -147,11 +162,22 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar)
     else
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(bar, 0)) : "memory");
 }
-// Orders what the peer wrote before its arrival after this thread's wait.
+// Waits like tc::mbar_wait for arrivals that may come from the peer CTA.
 template <int CG>
-__device__ __forceinline__ void acquire_peer()
+__device__ __forceinline__ bool wait_peer(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status)
 {
-    if (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    if (!tc::mbar_wait(bar, parity, abort_flag, status)) return false;
+    if (CG == 2) {                       // complete: acquires at cluster scope without waiting again
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(tc::smem_u32(bar)), "r"(parity)
+            : "memory");
+    }
+    return true;
 }
 // TMA load into this CTA's shared memory that completes on the first CTA's barrier.
 template <int CG>
@@ -175,7 +201,8 @@ __device__ __noinline__ void drain_after_abort()
     __syncthreads();
 }
 
-constexpr int kSfSlots = 4;
+constexpr int kSfSlots = 4;      // scale groups (four blocks of the contraction) in flight
+constexpr int kSfBatch = 4;      // groups whose words are loaded together
 
 template <int CG, int BN>
 struct Cfg {
@@ -256,7 +283,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = (uint32_t*)(acc_empty + 2);
     volatile int* abrt = (volatile int*)(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             tc::tma_prefetch_desc(&tmP);
             tc::tma_prefetch_desc(&tmQ);
             int stage = 0;
@@ -308,19 +335,18 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
             int stage = 0, slot = 0, buf = 0;
             uint32_t ph = 0, sph = 0, aph = 0;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                if (!(ok = tc::mbar_wait(&acc_empty[buf], aph ^ 1, abrt, p.status))) break;
+                if (!(ok = wait_peer<CG>(&acc_empty[buf], aph ^ 1, abrt, p.status))) break;
                 tc::tc_fence_after();
                 const uint32_t d = tmem + buf * C::ACC;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     const uint32_t sfp = tmem + C::SF_COL + slot * C::SF_COLS, sfq = sfp + 4;
                     if ((kb & 3) == 0) {
-                        if (!(ok = tc::mbar_wait(&sf_full[slot], sph, abrt, p.status))) break;
-                        acquire_peer<CG>();
+                        if (!(ok = wait_peer<CG>(&sf_full[slot], sph, abrt, p.status))) break;
                         tc::tc_fence_after();
                         const uint32_t src = tc::smem_u32(sf + slot * C::SF_BYTES);
                         tmem_cp_scales<CG>(sfp, src);
@@ -353,21 +379,34 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
         for (int t = first; t < tiles && ok; t += step) {
             int tm, tn;
             tile_of(p, t, tm, tn);
-            for (int g = 0; 4 * g < kblocks; ++g) {
-                uint4 w[1 + C::SFQ];
-                w[0] = scale_words(p.sb, p.ldsb, p.sb_shift, p.sb_rows, (tn * CG + rank) * C::BM, C::BM, g, lane);
+            // the words of kSfBatch groups are loaded together: one group at a
+            // time, the loads' latency (more than the 2048 cycles of a
+            // group's MMAs) set the pace
+            const int groups = (kblocks + 3) / 4;
+            for (int g0 = 0; g0 < groups && ok; g0 += kSfBatch) {
+                uint4 w[kSfBatch][1 + C::SFQ];
 #pragma unroll
-                for (int i = 0; i < C::SFQ; ++i)
-                    w[1 + i] = scale_words(p.sa, p.ldsa, p.sa_shift, p.sa_rows, tm * BN + 128 * i, BN - 128 * i, g, lane);
-                ok = tc::mbar_wait(&sf_empty[slot], sph ^ 1, abrt, p.status);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                uint4* dst = reinterpret_cast<uint4*>(sf + slot * C::SF_BYTES);
+                for (int j = 0; j < kSfBatch; ++j) {
+                    if (g0 + j >= groups) break;
+                    w[j][0] = scale_words(p.sb, p.ldsb, p.sb_shift, p.sb_rows, (tn * CG + rank) * C::BM, C::BM, g0 + j, lane);
 #pragma unroll
-                for (int i = 0; i < 1 + C::SFQ; ++i) dst[32 * i + lane] = w[i];
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_first<CG>(&sf_full[slot]);
-                if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
+                    for (int i = 0; i < C::SFQ; ++i)
+                        w[j][1 + i] = scale_words(p.sa, p.ldsa, p.sa_shift, p.sa_rows, tm * BN + 128 * i, BN - 128 * i,
+                                                  g0 + j, lane);
+                }
+#pragma unroll
+                for (int j = 0; j < kSfBatch; ++j) {
+                    if (g0 + j >= groups) break;
+                    ok = tc::mbar_wait(&sf_empty[slot], sph ^ 1, abrt, p.status);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    uint4* dst = reinterpret_cast<uint4*>(sf + slot * C::SF_BYTES);
+#pragma unroll
+                    for (int i = 0; i < 1 + C::SFQ; ++i) dst[32 * i + lane] = w[j][i];
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_first<CG>(&sf_full[slot]);
+                    if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
+                }
             }
         }
     } else if (warp >= 4) {
