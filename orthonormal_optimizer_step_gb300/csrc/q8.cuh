@@ -191,12 +191,15 @@ struct NormBwdArgs {
 size_t norm_backward_workspace(int rows, int cols);
 cudaError_t rms_norm_backward(const NormBwdArgs& a, dion_dtype dt, cudaStream_t stream);
 
+// One operand of the product: rows of 8-bit values, their format and scales.
+struct Q8Side {
+    int rows;
+    const uint8_t* q; long long ld; dion_q8_format fmt;
+    const uint8_t* s; long long lds; int square;
+};
 struct Q8MatArgs {
-    int m, n, k;
-    const uint8_t* a; long long lda; dion_q8_format afmt;
-    const uint8_t* sa; long long ldsa; int a_square;
-    const uint8_t* b; long long ldb; dion_q8_format bfmt;
-    const uint8_t* sb; long long ldsb; int b_square;
+    int k;
+    Q8Side a, b;
     void* c; long long ldc; dion_dtype cdt;
     int* status;
 };

@@ -79,9 +79,9 @@ extern "C" dion_status dion_q8_matmul(int m, int n, int k, const void* a, long l
     if (m > 0x7fffff00 || n > 0x7fffff00 || k > 0x7fffff00 || !tiles_fit(m, n) || lda >> 40 || ldb >> 40)
         return DION_ERR_UNSUPPORTED;
     Q8MatArgs g{};
-    g.m = m; g.n = n; g.k = k;
-    g.a = (const uint8_t*)a; g.lda = lda; g.afmt = afmt; g.sa = (const uint8_t*)sa; g.ldsa = ldsa; g.a_square = a_square;
-    g.b = (const uint8_t*)b; g.ldb = ldb; g.bfmt = bfmt; g.sb = (const uint8_t*)sb; g.ldsb = ldsb; g.b_square = b_square;
+    g.k = k;
+    g.a = Q8Side{m, (const uint8_t*)a, lda, afmt, (const uint8_t*)sa, ldsa, a_square};
+    g.b = Q8Side{n, (const uint8_t*)b, ldb, bfmt, (const uint8_t*)sb, ldsb, b_square};
     g.c = c; g.ldc = ldc; g.cdt = cdt;
     g.status = status;
     return done(q8_matmul(g, (cudaStream_t)cuda_stream));

@@ -8,10 +8,18 @@
 // scale byte (the instruction descriptor selects it), and one 32-bit word per
 // operand row carries the scales of four consecutive blocks.
 //
-// B's rows (the output's columns) are the instruction's M side and A's rows
-// its N side, so an accumulator column is a run of consecutive elements of one
-// row of C: a warp stores 32 neighbours at once whatever the shapes, and few
-// rows of A (single tokens) make the narrow side of the instruction.
+// Either operand can take the instruction's M side (its rows are then the
+// accumulator's lanes), the other its N side (the accumulator's columns):
+//   A on the M side (rows of C in the lanes): a thread holds consecutive
+//     elements of one row of C and stores 32 bytes at a time, if C's rows
+//     start on 16-byte boundaries.
+//   B on the M side (columns of C in the lanes): the lanes of a warp hold 32
+//     consecutive elements of one row of C and store them together, whatever
+//     C's alignment; and few rows of A (single tokens) make the narrow side
+//     of the instruction.
+// The first form's stores are an eighth as many: 4864 x 4096 x 512 (four
+// blocks of contraction a tile, so the stores set the pace) takes @@ us
+// against @@ us.
 //
 // Warps of a CTA: 0 loads operand tiles by TMA (128 bytes of the contraction
 // a stage, 128-byte swizzle), 1 issues the MMAs and the copies of the scales
@@ -29,12 +37,14 @@ int num_sms();
 
 namespace {
 
+// The operand on the instruction's M side is P, the other Q.
 struct GemmParams {
-    int m, n, k;
-    int tiles_m, tiles_n;             // of BN rows of A, 128 rows of B
-    const uint8_t* sa; long long ldsa; int sa_shift, sa_rows;   // scale row = row >> shift, rows in the table
-    const uint8_t* sb; long long ldsb; int sb_shift, sb_rows;
+    int np, nq, k;                    // rows of P and of Q, contraction
+    int tiles_p, tiles_q;
+    const uint8_t* sp; long long ldsp; int sp_shift, sp_rows;   // scale row = row >> shift, rows in the table
+    const uint8_t* sq; long long ldsq; int sq_shift, sq_rows;
     void* c; long long ldc;
+    int wide;                         // rows of C start on 32-byte boundaries
     uint32_t idesc;
     int* status;
 };
@@ -242,32 +252,74 @@ __device__ __forceinline__ uint4 scale_words(const uint8_t* s, long long ld, int
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Tile t of the grid: bands of eight row tiles of A, walked row tiles first, so
-// that the tiles in flight share both operands' panels in L2.
-__device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tm, int& tn)
+// Tile t of the grid: bands of eight tiles of Q, walked along Q first, so that
+// the tiles in flight share both operands' panels in L2.
+__device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tq, int& tp)
 {
-    const int per_band = 8 * p.tiles_n, band = t / per_band, in = t - band * per_band;
-    const int rows = min(8, p.tiles_m - 8 * band);
-    tm = 8 * band + in % rows;
-    tn = in / rows;
+    const int per_band = 8 * p.tiles_p, band = t / per_band, in = t - band * per_band;
+    const int rows = min(8, p.tiles_q - 8 * band);
+    tq = 8 * band + in % rows;
+    tp = in / rows;
 }
 
-// One accumulator column block of a warp: lane l holds column col of rows
-// row0 .. row0 + N - 1 of C.
+// N accumulator columns of a warp, B on the M side: lane l holds column col of
+// rows row0 .. row0 + N - 1 of C.
 template <bool F32, int N>
 __device__ __forceinline__ void store_cols(const GemmParams& p, int row0, int col, const uint32_t (&v)[N])
 {
-    if (col >= p.n) return;
+    if (col >= p.np) return;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        if (row0 + j >= p.m) break;
+        if (row0 + j >= p.nq) break;
         const long long o = (long long)(row0 + j) * p.ldc + col;
         if (F32) reinterpret_cast<float*>(p.c)[o] = __uint_as_float(v[j]);
         else reinterpret_cast<bf16*>(p.c)[o] = __float2bfloat16_rn(__uint_as_float(v[j]));
     }
 }
 
-template <int CG, int BN, bool F32>
+// 32 bytes to a 16-byte aligned address (one instruction if it is 32-byte aligned).
+__device__ __forceinline__ void store32(void* o, const uint32_t (&w)[8], int wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// A on the M side: this lane holds columns col0 .. col0 + 31 of row `row` of C,
+// whose rows start on 16-byte boundaries.
+template <bool F32>
+__device__ __forceinline__ void store_row(const GemmParams& p, int row, int col0, const uint32_t (&v)[32])
+{
+    if (row >= p.np || col0 >= p.nq) return;
+    constexpr int PER = F32 ? 8 : 16;    // elements of 32 bytes
+    char* o = reinterpret_cast<char*>(p.c) + ((long long)row * p.ldc + col0) * (F32 ? 4 : 2);
+    if (col0 + 32 <= p.nq) {
+#pragma unroll
+        for (int j = 0; j < 32; j += PER) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = F32 ? v[j + i]
+                           : tc::pack_bf16x2(__uint_as_float(v[j + 2 * i & 31]), __uint_as_float(v[j + 2 * i + 1 & 31]));
+            store32(o + 32 * (j / PER), w, p.wide);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (col0 + j >= p.nq) break;
+            if (F32) reinterpret_cast<float*>(o)[j] = __uint_as_float(v[j]);
+            else reinterpret_cast<bf16*>(o)[j] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        }
+    }
+}
+
+// ROWS: A is on the M side (P), else B is.
+template <int CG, int BN, bool F32, bool ROWS>
 __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     q8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const GemmParams p)
 {
@@ -308,7 +360,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     else __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int tiles = p.tiles_m * p.tiles_n;
+    const int tiles = p.tiles_p * p.tiles_q;
     const int kblocks = (p.k + 127) / 128;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
@@ -320,9 +372,9 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             uint32_t ph = 0;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                int tm, tn;
-                tile_of(p, t, tm, tn);
-                const int prow = (tn * CG + rank) * C::BM, qrow = tm * BN + rank * C::QROWS;
+                int tq, tp;
+                tile_of(p, t, tq, tp);
+                const int prow = (tp * CG + rank) * C::BM, qrow = tq * BN + rank * C::QROWS;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!(ok = tc::mbar_wait(&empty[stage], ph ^ 1, abrt, p.status))) break;
                     uint8_t* s = smem + stage * C::STAGE;
@@ -377,8 +429,8 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
         uint32_t sph = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
-            int tm, tn;
-            tile_of(p, t, tm, tn);
+            int tq, tp;
+            tile_of(p, t, tq, tp);
             // the words of kSfBatch groups are loaded together: one group at a
             // time, the loads' latency (more than the 2048 cycles of a
             // group's MMAs) set the pace
@@ -388,10 +440,10 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
 #pragma unroll
                 for (int j = 0; j < kSfBatch; ++j) {
                     if (g0 + j >= groups) break;
-                    w[j][0] = scale_words(p.sb, p.ldsb, p.sb_shift, p.sb_rows, (tn * CG + rank) * C::BM, C::BM, g0 + j, lane);
+                    w[j][0] = scale_words(p.sp, p.ldsp, p.sp_shift, p.sp_rows, (tp * CG + rank) * C::BM, C::BM, g0 + j, lane);
 #pragma unroll
                     for (int i = 0; i < C::SFQ; ++i)
-                        w[j][1 + i] = scale_words(p.sa, p.ldsa, p.sa_shift, p.sa_rows, tm * BN + 128 * i, BN - 128 * i,
+                        w[j][1 + i] = scale_words(p.sq, p.ldsq, p.sq_shift, p.sq_rows, tq * BN + 128 * i, BN - 128 * i,
                                                   g0 + j, lane);
                 }
 #pragma unroll
@@ -415,11 +467,11 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
         int buf = 0;
         uint32_t aph = 0;
         for (int t = first; t < tiles; t += step) {
-            int tm, tn;
-            tile_of(p, t, tm, tn);
+            int tq, tp;
+            tile_of(p, t, tq, tp);
             if (!tc::mbar_wait(&acc_full[buf], aph, abrt, p.status)) break;
             tc::tc_fence_after();
-            const int col = (tn * CG + rank) * C::BM + q * 32 + lane;
+            const int lrow = (tp * CG + rank) * C::BM + q * 32 + lane;
             const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + buf * C::ACC + c0;
             if constexpr (C::BUFS == 1) {
                 uint32_t v[C::ECOLS / 32][32];
@@ -430,14 +482,17 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
                 __syncwarp();
                 if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
 #pragma unroll
-                for (int j = 0; j < C::ECOLS / 32; ++j) store_cols<F32>(p, tm * BN + c0 + 32 * j, col, v[j]);
+                for (int j = 0; j < C::ECOLS / 32; ++j) {
+                    if (ROWS) store_row<F32>(p, lrow, tq * BN + c0 + 32 * j, v[j]);
+                    else store_cols<F32>(p, tq * BN + c0 + 32 * j, lrow, v[j]);
+                }
             } else {
 #pragma unroll 1
                 for (int j = 0; j < C::ECOLS; j += 16) {
                     uint32_t v[16];
                     tc::tmem_ld16(src + j, v);
                     tc::tmem_ld_wait();
-                    store_cols<F32>(p, tm * BN + c0 + j, col, v);
+                    store_cols<F32>(p, tq * BN + c0 + j, lrow, v);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -455,52 +510,56 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     }
 }
 
-template <int CG, int BN, bool F32>
+template <int CG, int BN, bool F32, bool ROWS>
 cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
 {
     using C = Cfg<CG, BN>;
     static std::atomic<unsigned long long> attr{0};
-    cudaError_t e = smem_attr_once((const void*)q8_gemm_kernel<CG, BN, F32>, (int)C::SMEM, attr);
+    cudaError_t e = smem_attr_once((const void*)q8_gemm_kernel<CG, BN, F32, ROWS>, (int)C::SMEM, attr);
     if (e != cudaSuccess) return e;
+    const Q8Side P = ROWS ? a.a : a.b, Q = ROWS ? a.b : a.a;
     CUtensorMap tmP, tmQ;
-    if (!make_tmap_3d(&tmP, a.b, TmapType::U8, a.k, a.n, 1, a.ldb, a.ldb, 128, C::BM) ||
-        !make_tmap_3d(&tmQ, a.a, TmapType::U8, a.k, a.m, 1, a.lda, a.lda, 128, C::QROWS))
+    if (!make_tmap_3d(&tmP, P.q, TmapType::U8, a.k, P.rows, 1, P.ld, P.ld, 128, C::BM) ||
+        !make_tmap_3d(&tmQ, Q.q, TmapType::U8, a.k, Q.rows, 1, Q.ld, Q.ld, 128, C::QROWS))
         return cudaErrorInvalidValue;
     GemmParams p{};
-    p.m = a.m; p.n = a.n; p.k = a.k;
-    p.tiles_m = (int)cdiv(a.m, BN);
-    p.tiles_n = (int)cdiv(a.n, C::BM * CG);
-    p.sa = a.sa; p.ldsa = a.ldsa; p.sa_shift = a.a_square ? 7 : 0; p.sa_rows = a.a_square ? (int)cdiv(a.m, 128) : a.m;
-    p.sb = a.sb; p.ldsb = a.ldsb; p.sb_shift = a.b_square ? 7 : 0; p.sb_rows = a.b_square ? (int)cdiv(a.n, 128) : a.n;
+    p.np = P.rows; p.nq = Q.rows; p.k = a.k;
+    p.tiles_p = (int)cdiv(P.rows, C::BM * CG);
+    p.tiles_q = (int)cdiv(Q.rows, BN);
+    p.sp = P.s; p.ldsp = P.lds; p.sp_shift = P.square ? 7 : 0; p.sp_rows = P.square ? (int)cdiv(P.rows, 128) : P.rows;
+    p.sq = Q.s; p.ldsq = Q.lds; p.sq_shift = Q.square ? 7 : 0; p.sq_rows = Q.square ? (int)cdiv(Q.rows, 128) : Q.rows;
     p.c = a.c; p.ldc = a.ldc;
-    p.idesc = idesc_mx(C::BM * CG, BN, (uint32_t)a.bfmt, (uint32_t)a.afmt);
+    p.wide = (uintptr_t)a.c % 32 == 0 && (a.ldc * (F32 ? 4 : 2)) % 32 == 0;
+    p.idesc = idesc_mx(C::BM * CG, BN, (uint32_t)P.fmt, (uint32_t)Q.fmt);
     p.status = a.status;
-    const long long tiles = (long long)p.tiles_m * p.tiles_n;
+    const long long tiles = (long long)p.tiles_p * p.tiles_q;
     const unsigned grid = (unsigned)(CG * std::min<long long>(tiles, num_sms() / CG));
     const dim3 block(128 + 32 * C::EW);
     if (CG == 1)
-        return launch("q8_matmul", q8_gemm_kernel<CG, BN, F32>, dim3(grid), block, C::SMEM, st, tmP, tmQ, p);
-    return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, p);
+        return launch("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, C::SMEM, st, tmP, tmQ, p);
+    return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, p);
 }
 
 template <bool F32>
 cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
 {
-    if (a.m <= 16) return gemm_go<1, 16, F32>(a, st);
-    if (a.m <= 32) return gemm_go<1, 32, F32>(a, st);
-    if (a.m <= 64) return gemm_go<1, 64, F32>(a, st);
-    if (a.m <= 128) return gemm_go<1, 128, F32>(a, st);
-    return gemm_go<2, 256, F32>(a, st);
+    const int m = a.a.rows;
+    if (m <= 16) return gemm_go<1, 16, F32, false>(a, st);
+    if (m <= 32) return gemm_go<1, 32, F32, false>(a, st);
+    if (m <= 64) return gemm_go<1, 64, F32, false>(a, st);
+    if (m <= 128) return gemm_go<1, 128, F32, false>(a, st);
+    const bool aligned = (uintptr_t)a.c % 16 == 0 && (a.ldc * (F32 ? 4 : 2)) % 16 == 0;
+    return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t q8_matmul(const Q8MatArgs& a, cudaStream_t st)
 {
-    if (a.m == 0 || a.n == 0) return cudaSuccess;
+    if (a.a.rows == 0 || a.b.rows == 0) return cudaSuccess;
     if (a.k == 0) {
         const size_t e = a.cdt == DION_F32 ? 4 : 2;
-        return cudaMemset2DAsync(a.c, (size_t)a.ldc * e, 0, (size_t)a.n * e, (size_t)a.m, st);
+        return cudaMemset2DAsync(a.c, (size_t)a.ldc * e, 0, (size_t)a.b.rows * e, (size_t)a.a.rows, st);
     }
     return a.cdt == DION_F32 ? gemm_pick<true>(a, st) : gemm_pick<false>(a, st);
 }
