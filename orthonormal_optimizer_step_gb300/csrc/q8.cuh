@@ -42,6 +42,43 @@ __device__ __forceinline__ uint32_t cvt2(float a, float b)
     return r;
 }
 
+// Pairs of float32 in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+          "l"(*reinterpret_cast<const uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+// Two bfloat16 in a word (the first in the low half) to float32.
+__device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float2 v)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Magnitude for a block's maximum: infinities and NaN do not count.
@@ -77,55 +114,67 @@ __device__ __forceinline__ int elem(int l, int i)
 
 
 
+// Eight values as four pairs; raw: as stored (one or two 16-byte words).
+template <typename T> struct Raw8 { uint4 u[sizeof(T) / 2]; };
+__device__ __forceinline__ void unpack8(const Raw8<bf16>& r, float2 (&f)[4])
+{
+    f[0] = unpack2(r.u[0].x);
+    f[1] = unpack2(r.u[0].y);
+    f[2] = unpack2(r.u[0].z);
+    f[3] = unpack2(r.u[0].w);
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float2 (&f)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        f[2 * i] = make_float2(__uint_as_float(r.u[i].x), __uint_as_float(r.u[i].y));
+        f[2 * i + 1] = make_float2(__uint_as_float(r.u[i].z), __uint_as_float(r.u[i].w));
+    }
+}
+__device__ __forceinline__ void pack8(Raw8<bf16>& r, const float2 (&f)[4])
+{
+    r.u[0] = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+__device__ __forceinline__ void pack8(Raw8<float>& r, const float2 (&f)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r.u[i] = make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y), __float_as_uint(f[2 * i + 1].x),
+                            __float_as_uint(f[2 * i + 1].y));
+}
+
+// A lane's eight values of the block at column c0 of a row; zeros past the row.
 template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, int c0, int cols, int l, float (&f)[8])
+__device__ __forceinline__ void load8(const T* row, int c0, int cols, int l, float2 (&f)[4])
 {
     if (VEC && c0 + 8 * l + 8 <= cols) {
-        const T* p = row + c0 + 8 * l;
-        if (sizeof(T) == 2) {
-            const uint4 u = *reinterpret_cast<const uint4*>(p);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        Raw8<T> r;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-        }
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = reinterpret_cast<const uint4*>(row + c0 + 8 * l)[i];
+        unpack8(r, f);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + elem<VEC>(l, i);
-            f[i] = c < cols ? to_f(row[c]) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const int a = c0 + elem<VEC>(l, 2 * i), b = c0 + elem<VEC>(l, 2 * i + 1);
+            f[i] = make_float2(a < cols ? to_f(row[a]) : 0.f, b < cols ? to_f(row[b]) : 0.f);
         }
     }
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, int c0, int cols, int l, const float (&f)[8])
+__device__ __forceinline__ void store8(T* row, int c0, int cols, int l, const float2 (&f)[4])
 {
     if (VEC && c0 + 8 * l + 8 <= cols) {
-        T* p = row + c0 + 8 * l;
-        if (sizeof(T) == 2) {
-            uint32_t w[4];
+        Raw8<T> r;
+        pack8(r, f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        }
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(row + c0 + 8 * l)[i] = r.u[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + elem<VEC>(l, i);
-            if (c < cols) row[c] = from_f<T>(f[i]);
+        for (int i = 0; i < 4; ++i) {
+            const int a = c0 + elem<VEC>(l, 2 * i), b = c0 + elem<VEC>(l, 2 * i + 1);
+            if (a < cols) row[a] = from_f<T>(f[i].x);
+            if (b < cols) row[b] = from_f<T>(f[i].y);
         }
     }
 }
@@ -133,11 +182,14 @@ __device__ __forceinline__ void store8(T* row, int c0, int cols, int l, const fl
 // Eight values of a lane, scaled and converted, to a row of 8-bit values
 // (16-byte aligned rows, so a lane's eight bytes are 8-byte aligned).
 template <bool VEC, int FMT>
-__device__ __forceinline__ void store_q8(uint8_t* row, int c0, int cols, int l, const float (&f)[8], float inv)
+__device__ __forceinline__ void store_q8(uint8_t* row, int c0, int cols, int l, const float2 (&f)[4], float inv)
 {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cvt2<FMT>(f[2 * i] * inv, f[2 * i + 1] * inv);
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = mul2(f[i], make_float2(inv, inv));
+        w[i] = cvt2<FMT>(v.x, v.y);
+    }
     if (VEC && c0 + 8 * l + 8 <= cols) {
         *reinterpret_cast<uint2*>(row + c0 + 8 * l) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     } else {
