@@ -78,7 +78,11 @@ def _pitch(rows, cols, ld, one, what):
 
 def _matrix(t, what):
     """(matrix of t's rows, row pitch) of a tensor [..., cols], without a copy."""
-    if t.dim() != 2:
+    if t.dim() == 2:
+        (rows, cols), (ld, one) = t.shape, t.stride()
+        if one == 1 and ld >= cols:
+            return t, ld
+    else:
         if t.dim() < 2:
             raise ValueError(f"{what} must have at least two dimensions")
         try:
@@ -109,17 +113,28 @@ def _empty(shape, dtype, device, stream):
 def new_q8(rows, cols, *, dtype=_E4M3, square=False, batch=None, device="cuda", stream=None):
     """An uninitialized quantized matrix (`batch` of them) with aligned rows."""
     _format(dtype)
+    return _new_q8(rows, cols, dtype, square, batch, device, stream)
+
+
+def _new_q8(rows, cols, dtype, square, batch, device, stream):
     sr, sc = ((rows + 127) // 128 if square else rows), (cols + 127) // 128
     ld, lds = (cols + 15) // 16 * 16, (sc + 3) // 4 * 4
-    lead = () if batch is None else (batch,)
-    data = _empty(lead + (rows, ld), dtype, device, stream)
-    scale = _empty(lead + (sr, lds), _E8M0, device, stream)
+    if batch is None:
+        data, scale = _empty((rows, ld), dtype, device, stream), _empty((sr, lds), _E8M0, device, stream)
+    else:
+        data, scale = _empty((batch, rows, ld), dtype, device, stream), _empty((batch, sr, lds), _E8M0, device, stream)
     return Q8(data if ld == cols else data[..., :cols], scale if lds == sc else scale[..., :sc])
 
 
 def _q8(q, what):
-    """(rows, cols, format, data pitch, scale pitch, square) of a quantized matrix."""
+    """(rows, cols, format, data pitch, scale pitch, square, pointers) of a quantized matrix."""
     data, scale = q
+    fmt, dptr, sptr = _FORMATS.get(data.dtype), data.data_ptr(), scale.data_ptr()
+    if data.dim() == 2 == scale.dim():       # all at once; what fails is found out below
+        (rows, cols), (sr, sc), (ld, one), (lds, sone) = data.shape, scale.shape, data.stride(), scale.stride()
+        if (fmt is not None and scale.dtype is _E8M0 and sc == (cols + 127) >> 7 and (sr == rows or sr == (rows + 127) >> 7)
+                and one == 1 == sone and ld >= cols and lds >= sc and not (ld | dptr) & 15 and not (lds | sptr) & 3):
+            return rows, cols, fmt, ld, lds, sr != rows, dptr, sptr
     fmt = _format(data.dtype)
     if scale.dtype is not _E8M0:
         raise TypeError(f"{what}: scales must be torch.float8_e8m0fnu, got {scale.dtype}")
@@ -132,16 +147,16 @@ def _q8(q, what):
         raise ValueError(f"{what}: {tuple(sshape)} scales do not fit {tuple(shape)} values")
     ld = _pitch(rows, cols, stride[-2], stride[-1], what)
     lds = _pitch(sr, sc, sstride[-2], sstride[-1], what)
-    if ld % 16 or data.data_ptr() % 16:
+    if ld % 16 or dptr % 16:
         raise ValueError(f"{what}: rows must start on 16-byte boundaries")
-    if lds % 4 or scale.data_ptr() % 4:
+    if lds % 4 or sptr % 4:
         raise ValueError(f"{what}: scale rows must start on 4-byte boundaries")
-    return rows, cols, fmt, ld, lds, sr != rows
+    return rows, cols, fmt, ld, lds, sr != rows, dptr, sptr
 
 
 def _out_q8(q, rows, cols, dtype, square, batch, what="out"):
     """(data pitch, scale pitch) of a quantized matrix that a call is to write."""
-    r, c, _, ld, lds, _ = _q8(q, what)
+    _, _, _, ld, lds, _, _, _ = _q8(q, what)
     shape = (rows, cols) if batch is None else (batch, rows, cols)
     if tuple(q.data.shape) != shape or q.data.dtype is not dtype or q.scale.shape[-2] != ((rows + 127) // 128 if square else rows):
         raise ValueError(f"{what} does not have the shape, dtype and scales asked for")
@@ -152,9 +167,10 @@ def _out_q8(q, rows, cols, dtype, square, batch, what="out"):
 def _status_word(dev, device):
     w = _status.get(dev)
     if w is None:
-        w = _status[dev] = torch.zeros(1, dtype=torch.int32, device=device)
+        t = torch.zeros(1, dtype=torch.int32, device=device)
         torch.cuda.current_stream(device).synchronize()   # once: later calls may run on any stream
-    return w.data_ptr()
+        w = _status[dev] = (t.data_ptr(), t)
+    return w[0]
 
 
 def dion_q8_status(device=None) -> int:
@@ -162,7 +178,7 @@ def dion_q8_status(device=None) -> int:
     once any of its calls gave up waiting (their results are undefined)."""
     dev = torch.device("cuda" if device is None else device).index
     w = _status.get(torch.cuda.current_device() if dev is None else dev)
-    return 0 if w is None else int(w.item())
+    return 0 if w is None else int(w[1].item())
 
 
 # ---- operators
@@ -200,7 +216,7 @@ def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, we
             args += (None, 0, 0, None, 0, 0)
             continue
         if out is None or out[i] is None:
-            q = new_q8(r, c, dtype=dtype, square=square, batch=batch, device=x.device, stream=stream)
+            q = _new_q8(r, c, dtype, square, batch, x.device, stream)
             ld, lds = (c + 15) // 16 * 16, ((c + 127) // 128 + 3) // 4 * 4
         else:
             q = out[i]
@@ -217,32 +233,36 @@ def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, we
     code = _od.lib().dion_q8_quantize(1 if batch is None else batch, rows, cols, dt, x.data_ptr(), ldx,
                                       0 if batch is None else stride[0], rptr, wptr, wdt, square, fmt, *args,
                                       _raw_stream(stream, dev))
-    _od._check(code, "dion_q8_quantize")
+    if code:
+        _od._check(code, "dion_q8_quantize")
     return pair[0], pair[1]
 
 
 def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
     """a b^T [m, n] of quantized matrices a [m, k] and b [n, k], in float32 sums
     rounded once to out_dtype (bfloat16 or float32; that of `out` if given)."""
-    m, k, af, lda, ldsa, a_sq = _q8(a, "a")
-    n, k2, bf, ldb, ldsb, b_sq = _q8(b, "b")
-    if k != k2 or a.data.dim() != 2 or b.data.dim() != 2:
-        raise ValueError(f"expected [m, k] and [n, k], got {tuple(a.data.shape)} and {tuple(b.data.shape)}")
-    dev = _cuda(a.data, "a")
+    m, k, af, lda, ldsa, a_sq, aptr, saptr = _q8(a, "a")
+    n, k2, bf, ldb, ldsb, b_sq, bptr, sbptr = _q8(b, "b")
+    ad, asc = a
+    bd, bsc = b
+    if k != k2 or ad.dim() != 2 or bd.dim() != 2:
+        raise ValueError(f"expected [m, k] and [n, k], got {tuple(ad.shape)} and {tuple(bd.shape)}")
+    dev = ad.get_device()
+    if dev < 0:
+        raise ValueError("a must be a CUDA tensor")
     if out is None:
-        ct = _type(out_dtype, "out_dtype")
-        out = _empty((m, n), out_dtype, a.data.device, stream)
-        ldc = n
+        ct, ldc = _type(out_dtype, "out_dtype"), n
+        out = _empty((m, n), out_dtype, ad.device, stream)
     else:
         if out.shape != (m, n):
             raise ValueError(f"out must be {m} x {n}, got {tuple(out.shape)}")
         ct, ldc = _type(out.dtype, "out"), _pitch(m, n, *out.stride(), "out")
-    if not dev == a.scale.get_device() == b.data.get_device() == b.scale.get_device() == out.get_device():
-        _same_device(dev, a_scale=a.scale, b=b.data, b_scale=b.scale, out=out)
-    code = _od.lib().dion_q8_matmul(m, n, k, a.data.data_ptr(), lda, af, a.scale.data_ptr(), ldsa, a_sq,
-                                    b.data.data_ptr(), ldb, bf, b.scale.data_ptr(), ldsb, b_sq, out.data_ptr(),
-                                    ldc, ct, _status_word(dev, a.data.device), _raw_stream(stream, dev))
-    _od._check(code, "dion_q8_matmul")
+    if not dev == asc.get_device() == bd.get_device() == bsc.get_device() == out.get_device():
+        _same_device(dev, a_scale=asc, b=bd, b_scale=bsc, out=out)
+    code = _od.lib().dion_q8_matmul(m, n, k, aptr, lda, af, saptr, ldsa, a_sq, bptr, ldb, bf, sbptr, ldsb, b_sq,
+                                    out.data_ptr(), ldc, ct, _status_word(dev, ad.device), _raw_stream(stream, dev))
+    if code:
+        _od._check(code, "dion_q8_matmul")
     return out
 
 
@@ -253,11 +273,10 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
     (y, h, rstd): the Q8 of all rows, the sum in x's type and shape (x itself
     without a residual; `h` may be given, also as x or residual) and
     1 / sqrt(mean(h^2) + eps) of each row, which the backward pass reads."""
-    xdt = x.dtype
-    dt, dev, device = _type(xdt, "x"), _cuda(x, "x"), x.device
+    xdt, device = x.dtype, x.device
+    dt, wdt, dev = _type(xdt, "x"), _type(weight.dtype, "weight"), _cuda(x, "x")
     x2, ldx = _matrix(x, "x")
     rows, cols = x2.shape
-    wdt = _type(weight.dtype, "weight")
     _vector(weight, cols, "weight")
     rptr, ldr, hptr, ldh = None, 0, None, 0
     if residual is not None:
@@ -270,12 +289,13 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
         r2, ldr = _matrix(residual, "residual")
         h2, ldh = _matrix(h, "h")
         rptr, hptr = r2.data_ptr(), h2.data_ptr()
-        _same_device(dev, residual=residual, h=h)
+        if not dev == residual.get_device() == h.get_device():
+            _same_device(dev, residual=residual, h=h)
     elif h is not None:
         raise ValueError("h is written only with a residual")
     if out is None:
-        out = new_q8(rows, cols, dtype=dtype, device=device, stream=stream)
-        fmt, ldq, lds = _FORMATS[dtype], (cols + 15) // 16 * 16, ((cols + 127) // 128 + 3) // 4 * 4
+        fmt, ldq, lds = _format(dtype), (cols + 15) // 16 * 16, ((cols + 127) // 128 + 3) // 4 * 4
+        out = _new_q8(rows, cols, dtype, False, None, device, stream)
     else:
         fmt = _format(out.data.dtype)
         ldq, lds = _out_q8(out, rows, cols, out.data.dtype, False, None)
@@ -286,12 +306,14 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
         if rstd.dtype is not _F32:
             raise TypeError(f"rstd must be float32, got {rstd.dtype}")
         _vector(rstd, rows, "rstd")
-    _same_device(dev, weight=weight, rstd=rstd)
+    if not dev == weight.get_device() == rstd.get_device():
+        _same_device(dev, weight=weight, rstd=rstd)
     if rows and cols:
         code = _od.lib().dion_rms_norm_q8(rows, cols, dt, x2.data_ptr(), ldx, rptr, ldr, weight.data_ptr(), wdt, eps,
-                                          hptr, ldh, fmt, out.data.data_ptr(), ldq, out.scale.data_ptr(), lds,
+                                          hptr, ldh, fmt, out[0].data_ptr(), ldq, out[1].data_ptr(), lds,
                                           rstd.data_ptr(), _raw_stream(stream, dev))
-        _od._check(code, "dion_rms_norm_q8")
+        if code:
+            _od._check(code, "dion_rms_norm_q8")
     return out, (x if residual is None else h), rstd
 
 
@@ -311,14 +333,15 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     dt, dev, device = _type(ydt, "dy"), _cuda(dy, "dy"), dy.device
     if dx is None:
         dx = _empty(shape, ydt, device, stream)
-    for name, t in (("h", h), ("dh", dh), ("dx", dx)):
-        if t is not None and (t.shape != shape or t.dtype is not ydt):
-            raise ValueError(f"{name} must have dy's shape and dtype")
+    for t in (h, dx) if dh is None else (h, dx, dh):
+        if t.shape != shape or t.dtype is not ydt:
+            raise ValueError(f"{'h' if t is h else 'dx' if t is dx else 'dh'} must have dy's shape and dtype")
     (y2, ldy), (h2, ldh), (x2, ldx) = _matrix(dy, "dy"), _matrix(h, "h"), _matrix(dx, "dx")
     dptr, lddh = None, 0
     if dh is not None:
         d2, lddh = _matrix(dh, "dh")
         dptr = d2.data_ptr()
+        _same_device(dev, dh=dh)
     rows, cols = y2.shape
     wdt = _type(weight.dtype, "weight")
     _vector(weight, cols, "weight")
@@ -330,11 +353,13 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     _vector(dweight, cols, "dweight")
     if workspace is None:
         workspace = _empty((max(256, dion_rms_norm_backward_workspace_size(rows, cols)),), torch.uint8, device, stream)
-    _same_device(dev, h=h, rstd=rstd, weight=weight, dh=dh, dx=dx, dweight=dweight, workspace=workspace)
+    if not dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device() == workspace.get_device():
+        _same_device(dev, h=h, rstd=rstd, weight=weight, dx=dx, dweight=dweight, workspace=workspace)
     if cols:
         code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh,
                                                 rstd.data_ptr(), weight.data_ptr(), wdt, dptr, lddh, x2.data_ptr(), ldx,
                                                 dweight.data_ptr(), workspace.data_ptr(),
                                                 workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
-        _od._check(code, "dion_rms_norm_backward")
+        if code:
+            _od._check(code, "dion_rms_norm_backward")
     return dx, dweight
