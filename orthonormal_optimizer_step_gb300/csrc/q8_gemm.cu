@@ -18,8 +18,8 @@
 //     C's alignment; and few rows of A (single tokens) make the narrow side
 //     of the instruction.
 // The first form's stores are an eighth as many: 4864 x 4096 x 512 (four
-// blocks of contraction a tile, so the stores set the pace) takes @@ us
-// against @@ us.
+// blocks of contraction a tile, so the stores set the pace) takes 20.1 us
+// against 24.9 us.
 //
 // Warps of a CTA: 0 loads operand tiles by TMA (128 bytes of the contraction
 // a stage, 128-byte swizzle), 1 issues the MMAs and the copies of the scales
@@ -44,7 +44,7 @@ struct GemmParams {
     const uint8_t* sp; long long ldsp; int sp_shift, sp_rows;   // scale row = row >> shift, rows in the table
     const uint8_t* sq; long long ldsq; int sq_shift, sq_rows;
     void* c; long long ldc;
-    int wide;                         // rows of C start on 32-byte boundaries
+    int wide, vec4;                   // rows of C start on 32-byte boundaries; on those of four elements
     uint32_t idesc;
     int* status;
 };
@@ -156,6 +156,15 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+__device__ __forceinline__ float4 load_remote(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 // The address, in the cluster's shared memory, of this CTA's variable in CTA `rank`.
 __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank)
 {
@@ -163,7 +172,7 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
     return r;
 }
-// Arrives on the first CTA's barrier.
+// Arrives on the barrier of the pair's first CTA.
 template <int CG>
 __device__ __forceinline__ void arrive_first(uint64_t* bar)
 {
@@ -487,12 +496,15 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
                     else store_cols<F32>(p, tq * BN + c0 + 32 * j, lrow, v[j]);
                 }
             } else {
+                constexpr int N = BN < 32 ? 16 : 32;
 #pragma unroll 1
-                for (int j = 0; j < C::ECOLS; j += 16) {
-                    uint32_t v[16];
-                    tc::tmem_ld16(src + j, v);
+                for (int j = 0; j < C::ECOLS; j += N) {
+                    uint32_t v[N];
+                    if constexpr (N == 16) tc::tmem_ld16(src + j, v);
+                    else tc::tmem_ld32(src + j, v);
                     tc::tmem_ld_wait();
-                    store_cols<F32>(p, tq * BN + c0 + j, lrow, v);
+                    if constexpr (ROWS && N == 32) store_row<F32>(p, lrow, tq * BN + c0 + j, v);
+                    else store_cols<F32>(p, tq * BN + c0 + j, lrow, v);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -510,6 +522,238 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     }
 }
 
+// -------------------------------------------- few tiles: the contraction split
+// One tile a cluster of `splits` CTAs, B on the M side.  Each contracts its share of the blocks and leaves its sums in its
+// shared memory; then every CTA finishes BN / splits columns of its rows: it
+// reads them from all CTAs that hold the same rows (16 bytes a lane through
+// distributed shared memory; 4-byte remote stores of the sums took several
+// times as long) and adds them in the order of the shares, so the bits are the
+// same every time.
+template <int BN>
+struct SplitCfg {
+    static constexpr int BM = 128;
+    static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = BN * 128, STAGE = P_BYTES + Q_BYTES;
+    static constexpr int STAGES = BN >= 128 ? 6 : 8;
+    static constexpr uint32_t SF_BYTES = 1024;           // scale words of 128 rows of each operand
+    static constexpr uint32_t ACC = BN < 32 ? 32 : BN;
+    static constexpr uint32_t SF_COL = ACC, SF_COLS = 8;
+    static constexpr uint32_t TMEM = BN <= 32 ? 64 : BN == 64 ? 128 : 256;
+    // Sums [column][128 rows] float, in the place of the stages, which the MMAs have all read by then.
+    static constexpr uint32_t SUMS = BN * 512;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kSfSlots * SF_BYTES + 512;
+    static_assert(SF_COL + kSfSlots * SF_COLS <= TMEM, "tensor memory columns");
+    static_assert(SUMS <= STAGES * STAGE, "sums in the stages' place");
+    static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+template <int BN, bool F32>
+__global__ void __launch_bounds__(256, 1)
+    q8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                         const GemmParams p, const int splits)
+{
+    using C = SplitCfg<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sf = smem + C::STAGES * C::STAGE;
+    float* sums = (float*)smem;
+    uint64_t* full = (uint64_t*)(sf + kSfSlots * C::SF_BYTES);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* sf_full = empty + C::STAGES;
+    uint64_t* sf_empty = sf_full + kSfSlots;
+    uint64_t* acc_full = sf_empty + kSfSlots;
+    uint32_t* tmem_slot = (uint32_t*)(acc_full + 1);
+    volatile int* abrt = (volatile int*)(tmem_slot + 1);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int share = (int)cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kSfSlots; ++s) {
+            tc::mbar_init(&sf_full[s], 1);
+            tc::mbar_init(&sf_empty[s], 1);
+        }
+        tc::mbar_init(acc_full, 1);
+        *abrt = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc<1>(tmem_slot, C::TMEM);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tile = blockIdx.x / splits, tq = tile % p.tiles_q, tp = tile / p.tiles_q;
+    const int kblocks = (p.k + 127) / 128, per = (kblocks + splits - 1) / splits;
+    const int kb0 = min(share * per, kblocks), kb1 = min(kb0 + per, kblocks);
+    const int prow = tp * C::BM, qrow = tq * BN;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            int stage = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!tc::mbar_wait(&empty[stage], ph ^ 1, abrt, p.status)) break;
+                uint8_t* s = smem + stage * C::STAGE;
+                tc::mbar_arrive_expect_tx(&full[stage], C::STAGE);
+                tc::tma_load_3d(s, &tmP, &full[stage], kb * 128, prow, 0);
+                tc::tma_load_3d(s + C::P_BYTES, &tmQ, &full[stage], kb * 128, qrow, 0);
+                if (++stage == C::STAGES) { stage = 0; ph ^= 1; }
+            }
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            int stage = 0, slot = 0;
+            uint32_t ph = 0, sph = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const uint32_t sfp = tmem + C::SF_COL + slot * C::SF_COLS, sfq = sfp + 4;
+                if ((kb & 3) == 0 || kb == kb0) {
+                    if (!(ok = tc::mbar_wait(&sf_full[slot], sph, abrt, p.status))) break;
+                    tc::tc_fence_after();
+                    const uint32_t src = tc::smem_u32(sf + slot * C::SF_BYTES);
+                    tmem_cp_scales<1>(sfp, src);
+                    tmem_cp_scales<1>(sfq, src + 512);
+                }
+                if (!(ok = tc::mbar_wait(&full[stage], ph, abrt, p.status))) break;
+                tc::tc_fence_after();
+                const uint32_t a0 = tc::smem_u32(smem + stage * C::STAGE), b0 = a0 + C::P_BYTES;
+                const uint32_t idesc = p.idesc | idesc_sf(kb & 3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_mx<1>(tmem, tc::make_sdesc(a0 + 32 * j, 16, 1024), tc::make_sdesc(b0 + 32 * j, 16, 1024), idesc,
+                               sfp, sfq, (kb != kb0) | (j != 0));
+                commit<1>(&empty[stage]);
+                if (++stage == C::STAGES) { stage = 0; ph ^= 1; }
+                if ((kb & 3) == 3) {
+                    commit<1>(&sf_empty[slot]);
+                    if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
+                }
+            }
+            if (ok && kb1 > kb0) commit<1>(acc_full);
+        }
+    } else if (warp == 2) {
+        int slot = 0;
+        uint32_t sph = 0;
+        bool ok = true;
+        const int g1 = kb1 > kb0 ? (kb1 + 3) / 4 : 0;
+        for (int g0 = kb0 / 4; g0 < g1 && ok; g0 += kSfBatch) {
+            uint4 w[kSfBatch][2];
+#pragma unroll
+            for (int j = 0; j < kSfBatch; ++j) {
+                if (g0 + j >= g1) break;
+                w[j][0] = scale_words(p.sp, p.ldsp, p.sp_shift, p.sp_rows, prow, C::BM, g0 + j, lane);
+                w[j][1] = scale_words(p.sq, p.ldsq, p.sq_shift, p.sq_rows, qrow, BN, g0 + j, lane);
+            }
+#pragma unroll
+            for (int j = 0; j < kSfBatch; ++j) {
+                if (g0 + j >= g1) break;
+                ok = tc::mbar_wait(&sf_empty[slot], sph ^ 1, abrt, p.status);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                uint4* dst = reinterpret_cast<uint4*>(sf + slot * C::SF_BYTES);
+                dst[lane] = w[j][0];
+                dst[32 + lane] = w[j][1];
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sf_full[slot]);
+                if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
+            }
+        }
+    }
+    if (warp >= 4) {
+        const int q = warp & 3;          // the lane quarter of tensor memory that this warp reads
+        float* dst = sums + q * 32 + lane;
+        const bool some = kb1 > kb0;
+        if (some) tc::mbar_wait(acc_full, 0, abrt, p.status);
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int j0 = 0; j0 < BN; j0 += 16) {
+            uint32_t v[16];
+            if (some) {
+                tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + j0, v);
+                tc::tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dst[(j0 + j) * 128] = __uint_as_float(v[j]);
+        }
+        tc::tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    // a warp takes one column at a time, a lane four rows of it
+    const int mine = (BN + splits - 1) / splits, c1 = min(BN, (share + 1) * mine);
+    const int n = prow + 4 * lane;
+    for (int c = share * mine + warp; c < c1; c += 8) {
+        const int m = qrow + c;
+        if (m >= p.nq) break;
+        const uint32_t at = tc::smem_u32(sums) + 512 * c + 16 * lane;
+        float4 t[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (s >= splits) break;
+            uint32_t addr;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(at), "r"(s));
+            t[s] = load_remote(addr);
+        }
+#pragma unroll
+        for (int s = 1; s < 8; ++s) {
+            if (s >= splits) break;
+            t[0].x += t[s].x;
+            t[0].y += t[s].y;
+            t[0].z += t[s].z;
+            t[0].w += t[s].w;
+        }
+        const float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
+        const long long o = (long long)m * p.ldc + n;
+        if (n + 4 <= p.np && p.vec4) {
+            if (F32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.c) + o) = t[0];
+            else *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(p.c) + o) =
+                make_uint2(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (n + i >= p.np) break;
+                if (F32) reinterpret_cast<float*>(p.c)[o + i] = v[i];
+                else reinterpret_cast<bf16*>(p.c)[o + i] = __float2bfloat16_rn(v[i]);
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();                      // the others have read this CTA's sums
+    __syncthreads();
+    if (*abrt) drain_after_abort();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tmem_dealloc<1>(tmem, C::TMEM);
+    }
+}
+
+// Tensor maps and parameters of a launch with tiles of prows rows of P (boxes
+// of 128) and qrows rows of Q (boxes of qbox); false if a map cannot be made.
+template <bool F32, bool ROWS>
+bool make_params(const Q8MatArgs& a, int prows, int qrows, int qbox, GemmParams& p, CUtensorMap& tmP, CUtensorMap& tmQ)
+{
+    const Q8Side P = ROWS ? a.a : a.b, Q = ROWS ? a.b : a.a;
+    if (!make_tmap_3d(&tmP, P.q, TmapType::U8, a.k, P.rows, 1, P.ld, P.ld, 128, 128) ||
+        !make_tmap_3d(&tmQ, Q.q, TmapType::U8, a.k, Q.rows, 1, Q.ld, Q.ld, 128, qbox))
+        return false;
+    p.np = P.rows; p.nq = Q.rows; p.k = a.k;
+    p.tiles_p = (int)cdiv(P.rows, prows);
+    p.tiles_q = (int)cdiv(Q.rows, qrows);
+    p.sp = P.s; p.ldsp = P.lds; p.sp_shift = P.square ? 7 : 0; p.sp_rows = P.square ? (int)cdiv(P.rows, 128) : P.rows;
+    p.sq = Q.s; p.ldsq = Q.lds; p.sq_shift = Q.square ? 7 : 0; p.sq_rows = Q.square ? (int)cdiv(Q.rows, 128) : Q.rows;
+    p.c = a.c; p.ldc = a.ldc;
+    p.wide = (uintptr_t)a.c % 32 == 0 && (a.ldc * (F32 ? 4 : 2)) % 32 == 0;
+    p.vec4 = (uintptr_t)a.c % (F32 ? 16 : 8) == 0 && a.ldc % 4 == 0;
+    p.idesc = idesc_mx(prows, qrows, (uint32_t)P.fmt, (uint32_t)Q.fmt);
+    p.status = a.status;
+    return true;
+}
+
 template <int CG, int BN, bool F32, bool ROWS>
 cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
 {
@@ -517,21 +761,9 @@ cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
     static std::atomic<unsigned long long> attr{0};
     cudaError_t e = smem_attr_once((const void*)q8_gemm_kernel<CG, BN, F32, ROWS>, (int)C::SMEM, attr);
     if (e != cudaSuccess) return e;
-    const Q8Side P = ROWS ? a.a : a.b, Q = ROWS ? a.b : a.a;
-    CUtensorMap tmP, tmQ;
-    if (!make_tmap_3d(&tmP, P.q, TmapType::U8, a.k, P.rows, 1, P.ld, P.ld, 128, C::BM) ||
-        !make_tmap_3d(&tmQ, Q.q, TmapType::U8, a.k, Q.rows, 1, Q.ld, Q.ld, 128, C::QROWS))
-        return cudaErrorInvalidValue;
     GemmParams p{};
-    p.np = P.rows; p.nq = Q.rows; p.k = a.k;
-    p.tiles_p = (int)cdiv(P.rows, C::BM * CG);
-    p.tiles_q = (int)cdiv(Q.rows, BN);
-    p.sp = P.s; p.ldsp = P.lds; p.sp_shift = P.square ? 7 : 0; p.sp_rows = P.square ? (int)cdiv(P.rows, 128) : P.rows;
-    p.sq = Q.s; p.ldsq = Q.lds; p.sq_shift = Q.square ? 7 : 0; p.sq_rows = Q.square ? (int)cdiv(Q.rows, 128) : Q.rows;
-    p.c = a.c; p.ldc = a.ldc;
-    p.wide = (uintptr_t)a.c % 32 == 0 && (a.ldc * (F32 ? 4 : 2)) % 32 == 0;
-    p.idesc = idesc_mx(C::BM * CG, BN, (uint32_t)P.fmt, (uint32_t)Q.fmt);
-    p.status = a.status;
+    CUtensorMap tmP, tmQ;
+    if (!make_params<F32, ROWS>(a, C::BM * CG, BN, C::QROWS, p, tmP, tmQ)) return cudaErrorInvalidValue;
     const long long tiles = (long long)p.tiles_p * p.tiles_q;
     const unsigned grid = (unsigned)(CG * std::min<long long>(tiles, num_sms() / CG));
     const dim3 block(128 + 32 * C::EW);
@@ -540,16 +772,65 @@ cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
     return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, p);
 }
 
+template <int BN, bool F32>
+cudaError_t gemm_split(const Q8MatArgs& a, int splits, cudaStream_t st)
+{
+    using C = SplitCfg<BN>;
+    static std::atomic<unsigned long long> attr{0};
+    cudaError_t e = smem_attr_once((const void*)q8_gemm_split_kernel<BN, F32>, (int)C::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    GemmParams p{};
+    CUtensorMap tmP, tmQ;
+    if (!make_params<F32, false>(a, C::BM, BN, BN, p, tmP, tmQ)) return cudaErrorInvalidValue;
+    return launch_cluster("q8_matmul_split", q8_gemm_split_kernel<BN, F32>,
+                          dim3((unsigned)(p.tiles_p * p.tiles_q * splits)), dim3(256), splits, C::SMEM, st, tmP, tmQ, p, splits);
+}
+
+// Shares of the contraction for `tiles` tiles of 128 rows of B: as many as the
+// clusters that run at once allow (an SM group holds whole clusters only: 152
+// SMs take 46 clusters of 3, 36 of 4, 28, 23, 15, 15 of 8), three blocks each
+// at least, and none for short contractions.  Measured, split / whole:
+// 1x4096x14336 13.6 / 24.9 us, 64x4096x4096 9.2 / 11.3, 768x768x16384 20.9 / 30.0;
+// 16x1024x1024 (8 blocks) 5.0 / 4.6; two shares gain nothing over one
+// (1024x1024x8192 17.8 / 17.4).
+int shares(long long tiles, int kblocks)
+{
+    constexpr int at_once[9] = {0, 0, 0, 46, 36, 28, 23, 15, 15};
+    if (kblocks < 16) return 1;
+    for (int s = 8; s > 2; --s)
+        if (3 * s <= kblocks && tiles <= at_once[s]) return s;
+    return 1;
+}
+
+template <int BN, bool F32>
+cudaError_t gemm_narrow(const Q8MatArgs& a, cudaStream_t st)
+{
+    const int s = shares(cdiv(a.b.rows, 128) * cdiv(a.a.rows, BN), (int)cdiv(a.k, 128));
+    return s > 1 ? gemm_split<BN, F32>(a, s, st) : gemm_go<1, BN, F32, false>(a, st);
+}
+
 template <bool F32>
 cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
 {
-    const int m = a.a.rows;
-    if (m <= 16) return gemm_go<1, 16, F32, false>(a, st);
-    if (m <= 32) return gemm_go<1, 32, F32, false>(a, st);
-    if (m <= 64) return gemm_go<1, 64, F32, false>(a, st);
-    if (m <= 128) return gemm_go<1, 128, F32, false>(a, st);
+    const int m = a.a.rows, n = a.b.rows, kb = (int)cdiv(a.k, 128);
+    if (m <= 16) return gemm_narrow<16, F32>(a, st);
+    if (m <= 32) return gemm_narrow<32, F32>(a, st);
+    if (m <= 64) return gemm_narrow<64, F32>(a, st);
     const bool aligned = (uintptr_t)a.c % 16 == 0 && (a.ldc * (F32 ? 4 : 2)) % 16 == 0;
-    return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
+    // 128 x 128 tiles of one CTA against 256 x 256 tiles of a pair, by what
+    // they were measured to take (us; 152 SMs): a CTA's stage is bound by the
+    // 32 KB that its SM reads from L2, a pair's by the tensor cores, at twice
+    // the products a byte, but a pair starts and ends later and does not
+    // overlap a tile's end with the next one's start.  512x4096x4096 11.8
+    // against 17.1, 8192x2304x768 17.3 against 19.9; 4096x4096x4096 53.4
+    // against 50.1, 2048x14336x4096 89 against 75.
+    const long long t1 = cdiv(m, 128) * cdiv(n, 128), t2 = cdiv(m, 256) * cdiv(n, 256);
+    const float one = 3.5f + (float)cdiv(t1, 152) * (0.24f * kb + 0.3f);
+    const float pair = 6.5f + (float)cdiv(t2, 76) * (0.31f * kb + 0.9f);
+    if (pair < one) return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
+    const int s = shares(t1, kb);
+    if (s > 1) return gemm_split<128, F32>(a, s, st);
+    return aligned ? gemm_go<1, 128, F32, true>(a, st) : gemm_go<1, 128, F32, false>(a, st);
 }
 
 }  // namespace
