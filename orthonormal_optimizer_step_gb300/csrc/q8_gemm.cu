@@ -11,13 +11,13 @@
 // Either operand can take the instruction's M side (its rows are then the
 // accumulator's lanes), the other its N side (the accumulator's columns):
 //   A on the M side (rows of C in the lanes): a thread holds consecutive
-//     elements of one row of C and stores 32 bytes at a time, if C's rows
-//     start on 16-byte boundaries.
+//     elements of one row of C and packs them into 16-byte words, if C's rows
+//     start and end on 16-byte boundaries.
 //   B on the M side (columns of C in the lanes): the lanes of a warp hold 32
 //     consecutive elements of one row of C and store them together, whatever
 //     C's alignment; and few rows of A (single tokens) make the narrow side
 //     of the instruction.
-// The first form's stores are an eighth as many: 4864 x 4096 x 512 (four
+// The first form's stores are fewer and wider: 4864 x 4096 x 512 (four
 // blocks of contraction a tile, so the stores set the pace) takes 20.1 us
 // against 24.9 us.
 //
@@ -44,7 +44,8 @@ struct GemmParams {
     const uint8_t* sp; long long ldsp; int sp_shift, sp_rows;   // scale row = row >> shift, rows in the table
     const uint8_t* sq; long long ldsq; int sq_shift, sq_rows;
     void* c; long long ldc;
-    int wide, vec4;                   // rows of C start on 32-byte boundaries; on those of four elements
+    int vec4;                         // rows of C start on boundaries of four elements
+    int sf16;                         // scale rows start on 16-byte boundaries
     uint32_t idesc;
     int* status;
 };
@@ -220,28 +221,34 @@ __device__ __noinline__ void drain_after_abort()
     __syncthreads();
 }
 
+constexpr int kOutBytes = 2048;  // a block of C on its way out: 32 rows of 64 bytes
 constexpr int kSfSlots = 4;      // scale groups (four blocks of the contraction) in flight
 constexpr int kSfBatch = 4;      // groups whose words are loaded together
+static_assert(kSfBatch == 4, "scale_words4 loads four");
 
 template <int CG, int BN>
 struct Cfg {
     static constexpr int BM = 128;                     // rows of B that a CTA holds
     static constexpr int QROWS = BN / CG;              // rows of A that a CTA holds
     static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = QROWS * 128, STAGE = P_BYTES + Q_BYTES;
-    static constexpr int STAGES = QROWS >= 128 ? 6 : 8;
+    static constexpr int STAGES = QROWS >= 96 ? 6 : 8;
     static constexpr int SFQ = (BN + 127) / 128;       // 128-row scale groups of A's side
     static constexpr uint32_t SF_BYTES = 512 * (1 + SFQ);
     static constexpr uint32_t ACC = BN < 32 ? 32 : BN; // accumulator columns
-    // 512 columns hold two accumulators and the scales up to 128 columns wide.
+    // 512 columns hold two accumulators and the scales up to 224 columns wide.
     // The 256-wide accumulator is single: its eight epilogue warps take it
     // into registers whole (128 columns each) and release it before they store.
-    static constexpr int BUFS = BN > 128 ? 1 : 2;
-    static constexpr int EW = BN > 128 ? 8 : 4;        // epilogue warps
-    static constexpr int ECOLS = BN / (EW / 4);        // columns of one
+    static constexpr int BUFS = BN > 224 ? 1 : 2;
+    static constexpr int EW = CG == 2 ? 8 : 4;         // epilogue warps
+    static constexpr int EGROUPS = EW / 4;             // warps on each lane quarter, and the columns of one
+    static constexpr int ECOLS = EGROUPS == 1 ? BN : (BN / 2 + 31) / 32 * 32;
     static constexpr uint32_t SF_COL = BUFS * ACC;     // scales: 4 (B) + 4 SFQ (A) columns a slot
     static constexpr uint32_t SF_COLS = 4 + 4 * SFQ;
     static constexpr uint32_t TMEM = BN <= 32 ? 128 : BN <= 64 ? 256 : 512;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kSfSlots * SF_BYTES + 512;
+    static constexpr int OUTS = BN < 32 ? 0 : BN > 224 ? 1 : 2;   // such blocks of an epilogue warp
+    static constexpr uint32_t OUT = EW * OUTS * kOutBytes;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + OUT + kSfSlots * SF_BYTES + 512;
+    static_assert(kSfSlots * SF_BYTES % 512 == 0, "the swizzle of C's blocks repeats every 512 bytes");
     static_assert(SF_COL + kSfSlots * SF_COLS <= TMEM, "tensor memory columns");
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
@@ -259,6 +266,24 @@ __device__ __forceinline__ uint4 scale_words(const uint8_t* s, long long ld, int
         w[i] = r < nrows && sr < rows ? *reinterpret_cast<const uint32_t*>(s + sr * ld + 4ll * g) : 0x7f7f7f7fu;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same for groups g0 .. g0 + 3 at once, of rows whose 16 bytes at 4 g0 are
+// aligned: a quarter as many loads.
+__device__ __forceinline__ void scale_words4(const uint8_t* s, long long ld, int shift, int rows, int row0, int nrows,
+                                             int g0, int lane, uint4& w0, uint4& w1, uint4& w2, uint4& w3)
+{
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 32 * i + lane, sr = (row0 + r) >> shift;
+        u[i] = r < nrows && sr < rows ? *reinterpret_cast<const uint4*>(s + sr * ld + 4ll * g0)
+                                      : make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+    }
+    w0 = make_uint4(u[0].x, u[1].x, u[2].x, u[3].x);
+    w1 = make_uint4(u[0].y, u[1].y, u[2].y, u[3].y);
+    w2 = make_uint4(u[0].z, u[1].z, u[2].z, u[3].z);
+    w3 = make_uint4(u[0].w, u[1].w, u[2].w, u[3].w);
 }
 
 // Tile t of the grid: bands of eight tiles of Q, walked along Q first, so that
@@ -286,57 +311,61 @@ __device__ __forceinline__ void store_cols(const GemmParams& p, int row0, int co
     }
 }
 
-// 32 bytes to a 16-byte aligned address (one instruction if it is 32-byte aligned).
-__device__ __forceinline__ void store32(void* o, const uint32_t (&w)[8], int wide)
+// A on the M side: this lane holds columns col0 .. col0 + 31 of row row0 + lane
+// of C, whose rows start and end on 16-byte boundaries.  The warp's block leaves as TMA
+// stores of 32 rows x 64 bytes from shared memory (16-byte word c of row r at
+// c ^ (r / 2 % 4), the 64-byte swizzle, so that the lanes' writes meet no bank
+// twice); what lies outside C is not written.  Shared memory's bandwidth
+// bounds the main loop (@@), so the epilogue's use of it counts: without any
+// stores 8192 x 14336 x 4096 takes 254 us; with them as now @@, through
+// shared memory and back through registers 297, 32 bytes a lane straight from
+// registers 299.
+template <bool F32, int OUTS>
+__device__ __forceinline__ void store_rows(const GemmParams& p, const CUtensorMap* tmC, int row0, int col0,
+                                           const uint32_t (&v)[32], uint8_t* buf, int& turn, int lane)
 {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-
-// A on the M side: this lane holds columns col0 .. col0 + 31 of row `row` of C,
-// whose rows start on 16-byte boundaries.
-template <bool F32>
-__device__ __forceinline__ void store_row(const GemmParams& p, int row, int col0, const uint32_t (&v)[32])
-{
-    if (row >= p.np || col0 >= p.nq) return;
-    constexpr int PER = F32 ? 8 : 16;    // elements of 32 bytes
-    char* o = reinterpret_cast<char*>(p.c) + ((long long)row * p.ldc + col0) * (F32 ? 4 : 2);
-    if (col0 + 32 <= p.nq) {
+    if (row0 >= p.np || col0 >= p.nq) return;
+    constexpr int COLS = F32 ? 16 : 32;
 #pragma unroll
-        for (int j = 0; j < 32; j += PER) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = F32 ? v[j + i]
-                           : tc::pack_bf16x2(__uint_as_float(v[j + 2 * i & 31]), __uint_as_float(v[j + 2 * i + 1 & 31]));
-            store32(o + 32 * (j / PER), w, p.wide);
+    for (int h = 0; h < 32 / COLS; ++h) {
+        if (col0 + h * COLS >= p.nq) break;
+        uint8_t* b = buf + (OUTS == 2 ? turn * kOutBytes : 0);
+        if (lane == 0) {                 // the block's last store has been read
+            if (OUTS == 2) tc::tma_store_wait_read1();
+            else tc::tma_store_wait_read();
         }
-    } else {
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (col0 + j >= p.nq) break;
-            if (F32) reinterpret_cast<float*>(o)[j] = __uint_as_float(v[j]);
-            else reinterpret_cast<bf16*>(o)[j] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = F32 ? v[(h * COLS + 4 * c + i) % 32]
+                           : tc::pack_bf16x2(__uint_as_float(v[(8 * c + 2 * i) % 32]), __uint_as_float(v[(8 * c + 2 * i + 1) % 32]));
+            *reinterpret_cast<uint4*>(b + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::tma_store_3d(tmC, b, col0 + h * COLS, row0, 0);
+            tc::tma_store_commit();
+        }
+        turn ^= 1;
     }
 }
 
 // ROWS: A is on the M side (P), else B is.
 template <int CG, int BN, bool F32, bool ROWS>
 __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
-    q8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const GemmParams p)
+    q8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                   const __grid_constant__ CUtensorMap tmC, const GemmParams p)
 {
     using C = Cfg<CG, BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sf = smem + C::STAGES * C::STAGE;
-    uint64_t* full = (uint64_t*)(sf + kSfSlots * C::SF_BYTES);
+    uint8_t* out = sf + kSfSlots * C::SF_BYTES;
+    uint64_t* full = (uint64_t*)(out + C::OUT);
     uint64_t* empty = full + C::STAGES;
     uint64_t* sf_full = empty + C::STAGES;
     uint64_t* sf_empty = sf_full + kSfSlots;
@@ -446,14 +475,23 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             const int groups = (kblocks + 3) / 4;
             for (int g0 = 0; g0 < groups && ok; g0 += kSfBatch) {
                 uint4 w[kSfBatch][1 + C::SFQ];
-#pragma unroll
-                for (int j = 0; j < kSfBatch; ++j) {
-                    if (g0 + j >= groups) break;
-                    w[j][0] = scale_words(p.sp, p.ldsp, p.sp_shift, p.sp_rows, (tp * CG + rank) * C::BM, C::BM, g0 + j, lane);
+                if (p.sf16 && g0 + 4 <= groups) {
+                    scale_words4(p.sp, p.ldsp, p.sp_shift, p.sp_rows, (tp * CG + rank) * C::BM, C::BM, g0, lane, w[0][0],
+                                 w[1][0], w[2][0], w[3][0]);
 #pragma unroll
                     for (int i = 0; i < C::SFQ; ++i)
-                        w[j][1 + i] = scale_words(p.sq, p.ldsq, p.sq_shift, p.sq_rows, tq * BN + 128 * i, BN - 128 * i,
-                                                  g0 + j, lane);
+                        scale_words4(p.sq, p.ldsq, p.sq_shift, p.sq_rows, tq * BN + 128 * i, BN - 128 * i, g0, lane,
+                                     w[0][1 + i], w[1][1 + i], w[2][1 + i], w[3][1 + i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kSfBatch; ++j) {
+                        if (g0 + j >= groups) break;
+                        w[j][0] = scale_words(p.sp, p.ldsp, p.sp_shift, p.sp_rows, (tp * CG + rank) * C::BM, C::BM, g0 + j, lane);
+#pragma unroll
+                        for (int i = 0; i < C::SFQ; ++i)
+                            w[j][1 + i] = scale_words(p.sq, p.ldsq, p.sq_shift, p.sq_rows, tq * BN + 128 * i, BN - 128 * i,
+                                                      g0 + j, lane);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < kSfBatch; ++j) {
@@ -473,6 +511,8 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     } else if (warp >= 4) {
         const int q = warp & 3;          // the lane quarter of tensor memory that this warp reads
         const int c0 = (warp - 4) / 4 * C::ECOLS;
+        uint8_t* outs = out + (warp - 4) * C::OUTS * kOutBytes;
+        int turn = 0;
         int buf = 0;
         uint32_t aph = 0;
         for (int t = first; t < tiles; t += step) {
@@ -480,7 +520,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             tile_of(p, t, tq, tp);
             if (!tc::mbar_wait(&acc_full[buf], aph, abrt, p.status)) break;
             tc::tc_fence_after();
-            const int lrow = (tp * CG + rank) * C::BM + q * 32 + lane;
+            const int lrow = (tp * CG + rank) * C::BM + q * 32;
             const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + buf * C::ACC + c0;
             if constexpr (C::BUFS == 1) {
                 uint32_t v[C::ECOLS / 32][32];
@@ -492,19 +532,20 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
                 if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
 #pragma unroll
                 for (int j = 0; j < C::ECOLS / 32; ++j) {
-                    if (ROWS) store_row<F32>(p, lrow, tq * BN + c0 + 32 * j, v[j]);
-                    else store_cols<F32>(p, tq * BN + c0 + 32 * j, lrow, v[j]);
+                    if constexpr (ROWS) store_rows<F32, C::OUTS>(p, &tmC, lrow, tq * BN + c0 + 32 * j, v[j], outs, turn, lane);
+                    else store_cols<F32>(p, tq * BN + c0 + 32 * j, lrow + lane, v[j]);
                 }
             } else {
                 constexpr int N = BN < 32 ? 16 : 32;
+                const int cols = min(C::ECOLS, BN - c0);
 #pragma unroll 1
-                for (int j = 0; j < C::ECOLS; j += N) {
+                for (int j = 0; j < cols; j += N) {
                     uint32_t v[N];
                     if constexpr (N == 16) tc::tmem_ld16(src + j, v);
                     else tc::tmem_ld32(src + j, v);
                     tc::tmem_ld_wait();
-                    if constexpr (ROWS && N == 32) store_row<F32>(p, lrow, tq * BN + c0 + j, v);
-                    else store_cols<F32>(p, tq * BN + c0 + j, lrow, v);
+                    if constexpr (ROWS) store_rows<F32, C::OUTS>(p, &tmC, lrow, tq * BN + c0 + j, v, outs, turn, lane);
+                    else store_cols<F32>(p, tq * BN + c0 + j, lrow + lane, v);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -512,6 +553,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             }
             if (++buf == C::BUFS) { buf = 0; aph ^= 1; }
         }
+        if (ROWS && lane == 0) tc::tma_store_wait_all();
     }
     __syncthreads();
     if (*abrt) drain_after_abort();
@@ -746,8 +788,8 @@ bool make_params(const Q8MatArgs& a, int prows, int qrows, int qbox, GemmParams&
     p.tiles_q = (int)cdiv(Q.rows, qrows);
     p.sp = P.s; p.ldsp = P.lds; p.sp_shift = P.square ? 7 : 0; p.sp_rows = P.square ? (int)cdiv(P.rows, 128) : P.rows;
     p.sq = Q.s; p.ldsq = Q.lds; p.sq_shift = Q.square ? 7 : 0; p.sq_rows = Q.square ? (int)cdiv(Q.rows, 128) : Q.rows;
+    p.sf16 = (uintptr_t)P.s % 16 == 0 && (uintptr_t)Q.s % 16 == 0 && P.lds % 16 == 0 && Q.lds % 16 == 0;
     p.c = a.c; p.ldc = a.ldc;
-    p.wide = (uintptr_t)a.c % 32 == 0 && (a.ldc * (F32 ? 4 : 2)) % 32 == 0;
     p.vec4 = (uintptr_t)a.c % (F32 ? 16 : 8) == 0 && a.ldc % 4 == 0;
     p.idesc = idesc_mx(prows, qrows, (uint32_t)P.fmt, (uint32_t)Q.fmt);
     p.status = a.status;
@@ -764,12 +806,17 @@ cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
     GemmParams p{};
     CUtensorMap tmP, tmQ;
     if (!make_params<F32, ROWS>(a, C::BM * CG, BN, C::QROWS, p, tmP, tmQ)) return cudaErrorInvalidValue;
+    CUtensorMap tmC = tmP;               // used with ROWS only
+    if (ROWS && !make_tmap_3d_sw64(&tmC, a.c, F32 ? TmapType::F32 : TmapType::BF16, a.b.rows, a.a.rows, 1,
+                                   (uint64_t)a.ldc * (F32 ? 4 : 2), (uint64_t)a.ldc * (F32 ? 4 : 2), F32 ? 16 : 32, 32))
+        return cudaErrorInvalidValue;
     const long long tiles = (long long)p.tiles_p * p.tiles_q;
     const unsigned grid = (unsigned)(CG * std::min<long long>(tiles, num_sms() / CG));
     const dim3 block(128 + 32 * C::EW);
     if (CG == 1)
-        return launch("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, C::SMEM, st, tmP, tmQ, p);
-    return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, p);
+        return launch("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, C::SMEM, st, tmP, tmQ, tmC,
+                      p);
+    return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, tmC, p);
 }
 
 template <int BN, bool F32>
@@ -816,7 +863,8 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     if (m <= 16) return gemm_narrow<16, F32>(a, st);
     if (m <= 32) return gemm_narrow<32, F32>(a, st);
     if (m <= 64) return gemm_narrow<64, F32>(a, st);
-    const bool aligned = (uintptr_t)a.c % 16 == 0 && (a.ldc * (F32 ? 4 : 2)) % 16 == 0;
+    // TMA stores move whole 16-byte words: C's rows start and end on such boundaries
+    const bool aligned = (uintptr_t)a.c % 16 == 0 && (a.ldc * (F32 ? 4 : 2)) % 16 == 0 && n % (F32 ? 4 : 8) == 0;
     // 128 x 128 tiles of one CTA against 256 x 256 tiles of a pair, by what
     // they were measured to take (us; 152 SMs): a CTA's stage is bound by the
     // 32 KB that its SM reads from L2, a pair's by the tensor cores, at twice
@@ -824,10 +872,20 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     // overlap a tile's end with the next one's start.  512x4096x4096 11.8
     // against 17.1, 8192x2304x768 17.3 against 19.9; 4096x4096x4096 53.4
     // against 50.1, 2048x14336x4096 89 against 75.
-    const long long t1 = cdiv(m, 128) * cdiv(n, 128), t2 = cdiv(m, 256) * cdiv(n, 256);
+    const long long t1 = cdiv(m, 128) * cdiv(n, 128);
     const float one = 3.5f + (float)cdiv(t1, 152) * (0.24f * kb + 0.3f);
-    const float pair = 6.5f + (float)cdiv(t2, 76) * (0.31f * kb + 0.9f);
-    if (pair < one) return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
+    const int q = aligned ? n : m, other = aligned ? m : n;      // rows of the operand on the N side
+    int bn = 0;
+    float best = one;
+    const int widths[3] = {256, 224, 192};
+    const float kbs[3] = {0.30f, 0.275f, 0.245f}, ends[3] = {0.9f, 0.2f, 0.2f};
+    for (int i = 0; i < 3; ++i) {
+        const float t = 6.f + (float)cdiv(cdiv(q, widths[i]) * cdiv(other, 256), 76) * (kbs[i] * kb + ends[i]);
+        if (t < best) { best = t; bn = widths[i]; }
+    }
+    if (bn == 256) return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
+    if (bn == 224) return aligned ? gemm_go<2, 224, F32, true>(a, st) : gemm_go<2, 224, F32, false>(a, st);
+    if (bn == 192) return aligned ? gemm_go<2, 192, F32, true>(a, st) : gemm_go<2, 192, F32, false>(a, st);
     const int s = shares(t1, kb);
     if (s > 1) return gemm_split<128, F32>(a, s, st);
     return aligned ? gemm_go<1, 128, F32, true>(a, st) : gemm_go<1, 128, F32, false>(a, st);
