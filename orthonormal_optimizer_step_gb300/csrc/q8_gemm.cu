@@ -316,10 +316,10 @@ __device__ __forceinline__ void store_cols(const GemmParams& p, int row0, int co
 // stores of 32 rows x 64 bytes from shared memory (16-byte word c of row r at
 // c ^ (r / 2 % 4), the 64-byte swizzle, so that the lanes' writes meet no bank
 // twice); what lies outside C is not written.  Shared memory's bandwidth
-// bounds the main loop (@@), so the epilogue's use of it counts: without any
-// stores 8192 x 14336 x 4096 takes 254 us; with them as now @@, through
-// shared memory and back through registers 297, 32 bytes a lane straight from
-// registers 299.
+// bounds the main loop (a block of a 256 x 224 tile moves 30 KB in by TMA and
+// about 30 KB out to the MMAs, at 128 bytes a cycle 470 of its 490 cycles), so
+// the epilogue's use of it counts: 8192 x 14336 x 4096 takes 254 us without
+// stores, 293 as here, 298 through shared memory and back through registers.
 template <bool F32, int OUTS>
 __device__ __forceinline__ void store_rows(const GemmParams& p, const CUtensorMap* tmC, int row0, int col0,
                                            const uint32_t (&v)[32], uint8_t* buf, int& turn, int lane)
@@ -865,27 +865,26 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     if (m <= 64) return gemm_narrow<64, F32>(a, st);
     // TMA stores move whole 16-byte words: C's rows start and end on such boundaries
     const bool aligned = (uintptr_t)a.c % 16 == 0 && (a.ldc * (F32 ? 4 : 2)) % 16 == 0 && n % (F32 ? 4 : 8) == 0;
-    // 128 x 128 tiles of one CTA against 256 x 256 tiles of a pair, by what
-    // they were measured to take (us; 152 SMs): a CTA's stage is bound by the
-    // 32 KB that its SM reads from L2, a pair's by the tensor cores, at twice
-    // the products a byte, but a pair starts and ends later and does not
-    // overlap a tile's end with the next one's start.  512x4096x4096 11.8
-    // against 17.1, 8192x2304x768 17.3 against 19.9; 4096x4096x4096 53.4
-    // against 50.1, 2048x14336x4096 89 against 75.
+    // 128 x 128 tiles of one CTA against tiles of a pair, 256 x 256 or 256 x 224
+    // (which double the accumulator), by a model of what they were measured to
+    // take: start + waves * (time a block * blocks + a tile's end), in us on 152
+    // SMs.  A pair reads half as much a product but starts and ends later.
+    // Measured, us:                  128     224     256
+    //    512 x  4096 x  4096        11.8            17.1
+    //   8192 x  2304 x   768        17.1    19.4    19.2
+    //   4096 x  4096 x  4096        52.6    45.0    47.9
+    //   8192 x  1024 x  4096        35.4    36.4    27.2    (the last wave of 224 is nearly empty)
+    //   8192 x 14336 x  4096         368     293     328
+    //   4096 x 14336 x  8192         362     318     304
+    // Without alignment for TMA stores a 224-wide tile's stores take longer
+    // than its share of the main loop is worth (4096 x 4097 x 4096: 58.1, 256: 53.6).
     const long long t1 = cdiv(m, 128) * cdiv(n, 128);
-    const float one = 3.5f + (float)cdiv(t1, 152) * (0.24f * kb + 0.3f);
     const int q = aligned ? n : m, other = aligned ? m : n;      // rows of the operand on the N side
-    int bn = 0;
-    float best = one;
-    const int widths[3] = {256, 224, 192};
-    const float kbs[3] = {0.30f, 0.275f, 0.245f}, ends[3] = {0.9f, 0.2f, 0.2f};
-    for (int i = 0; i < 3; ++i) {
-        const float t = 6.f + (float)cdiv(cdiv(q, widths[i]) * cdiv(other, 256), 76) * (kbs[i] * kb + ends[i]);
-        if (t < best) { best = t; bn = widths[i]; }
-    }
-    if (bn == 256) return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
-    if (bn == 224) return aligned ? gemm_go<2, 224, F32, true>(a, st) : gemm_go<2, 224, F32, false>(a, st);
-    if (bn == 192) return aligned ? gemm_go<2, 192, F32, true>(a, st) : gemm_go<2, 192, F32, false>(a, st);
+    const float one = 3.5f + (float)cdiv(t1, 152) * (0.215f * kb + 0.4f);
+    const float w256 = 5.f + (float)cdiv(cdiv(q, 256) * cdiv(other, 256), 76) * (0.335f * kb + 1.8f);
+    const float w224 = 5.f + (float)cdiv(cdiv(q, 224) * cdiv(other, 256), 76) * (0.30f * kb + 0.9f);
+    if (aligned && w224 < one && w224 < w256) return gemm_go<2, 224, F32, true>(a, st);
+    if (w256 < one) return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
     const int s = shares(t1, kb);
     if (s > 1) return gemm_split<128, F32>(a, s, st);
     return aligned ? gemm_go<1, 128, F32, true>(a, st) : gemm_go<1, 128, F32, false>(a, st);
