@@ -31,8 +31,8 @@ struct QuantParams {
 __device__ __forceinline__ int t_granule(int c, int g) { return c * 16 + (g ^ ((c >> 3) & 15)); }
 
 // A thread's 8 x 8 values, pairs (2 i, 2 i + 1) of a row together.
-template <bool PACKED> struct Frag;
-template <> struct Frag<true> {          // bfloat16 as stored
+template <bool PACKED, bool NORM> struct Frag;
+template <> struct Frag<true, false> {   // bfloat16 as stored
     uint32_t v[8][4];
     __device__ __forceinline__ float2 get(int j, int i) const { return unpack2(v[j][i]); }
     __device__ __forceinline__ void set(int j, int i, float2 f) { v[j][i] = pack2(f); }   // f holds bfloat16 values
@@ -53,16 +53,13 @@ template <> struct Frag<true> {          // bfloat16 as stored
         return *reinterpret_cast<const uint32_t*>(&r);
     }
 };
-template <> struct Frag<false> {
-    float2 v[8][4];
-    __device__ __forceinline__ float2 get(int j, int i) const { return v[j][i]; }
-    __device__ __forceinline__ void set(int j, int i, float2 f) { v[j][i] = f; }
+struct PairMax {                         // of float32 values
     typedef float2 Max;
     __device__ __forceinline__ static Max zero() { return make_float2(0.f, 0.f); }
-    __device__ __forceinline__ void take(Max& m, int j, int i) const
+    __device__ __forceinline__ static void larger(Max& m, float2 v)
     {
-        m.x = fmaxf(m.x, fabsf(v[j][i].x));
-        m.y = fmaxf(m.y, fabsf(v[j][i].y));
+        m.x = fmaxf(m.x, fabsf(v.x));
+        m.y = fmaxf(m.y, fabsf(v.y));
     }
     __device__ __forceinline__ static uint2 bits(Max m) { return make_uint2(__float_as_uint(m.x), __float_as_uint(m.y)); }
     __device__ __forceinline__ static Max of_bits(uint32_t a, uint32_t b)
@@ -72,6 +69,45 @@ template <> struct Frag<false> {
     __device__ __forceinline__ static Max max16(Max m)
     {
         return make_float2(fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, 16)), fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, 16)));
+    }
+};
+template <bool NORM> struct Frag<false, NORM> : PairMax {
+    float2 v[8][4];
+    __device__ __forceinline__ float2 get(int j, int i) const { return v[j][i]; }
+    __device__ __forceinline__ void set(int j, int i, float2 f) { v[j][i] = f; }
+    __device__ __forceinline__ void take(Max& m, int j, int i) const { larger(m, v[j][i]); }
+    __device__ __forceinline__ void norm(int j, float rs, const float2 (&w)[4])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = mul2(mul2(v[j][i], make_float2(rs, rs)), w[i]);
+    }
+};
+// bfloat16 as stored, times the row's and the columns' factors wherever it is
+// read: two products each time cost less than the occupancy of 64 registers
+// (again() keeps the compiler from holding on to the products).
+template <> struct Frag<true, true> : PairMax {
+    uint32_t v[8][4];
+    float rs[8];
+    float2 w[4];
+    __device__ __forceinline__ float2 get(int j, int i) const
+    {
+        return mul2(mul2(unpack2(v[j][i]), make_float2(rs[j], rs[j])), w[i]);
+    }
+    // the value as read from memory; later only to make products NaN
+    __device__ __forceinline__ void set(int j, int i, float2 f) { v[j][i] = pack2(f); }
+    __device__ __forceinline__ void take(Max& m, int j, int i) const { larger(m, get(j, i)); }
+    __device__ __forceinline__ void norm(int j, float r, const float2 (&f)[4])
+    {
+        rs[j] = r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = f[i];
+    }
+    __device__ __forceinline__ void again()
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(v[j][i]));
     }
 };
 
@@ -91,10 +127,10 @@ __device__ __forceinline__ uint32_t max16_of8(const uint32_t (&v)[8], int l)
 }
 
 template <typename T, int FMT, bool ROWS, bool COLS, bool SQUARE, bool VEC, bool NORM>
-__global__ void __launch_bounds__(kThreads) q8_quant_kernel(const QuantParams p)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS && COLS ? 3 : 4) q8_quant_kernel(const QuantParams p)
 {
-    constexpr bool PACKED = sizeof(T) == 2 && !NORM;
-    typedef Frag<PACKED> F;
+    constexpr bool PACKED = sizeof(T) == 2;
+    typedef Frag<PACKED, NORM> F;
     __shared__ uint2 tile[COLS ? kTile * 16 : 1];
     __shared__ typename F::Max colmax[(COLS || SQUARE) ? kThreads / 32 : 1][kTile / 2];
     __shared__ float colinv[kTile];
@@ -146,20 +182,11 @@ __global__ void __launch_bounds__(kThreads) q8_quant_kernel(const QuantParams p)
         }
     }
     if constexpr (NORM) {
-        float w[8];
+        float2 w[4];
+        if (p.wf32) load8<VEC>(reinterpret_cast<const float*>(a.weight), c0, a.cols, l, w);
+        else load8<VEC>(reinterpret_cast<const bf16*>(a.weight), c0, a.cols, l, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + elem<VEC>(l, i);
-            w[i] = c >= a.cols ? 0.f : p.wf32 ? reinterpret_cast<const float*>(a.weight)[c]
-                                              : to_f(reinterpret_cast<const bf16*>(a.weight)[c]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float rs = r0 + j < a.rows ? a.rstd[r0 + j] : 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f.set(j, i, mul2(mul2(f.get(j, i), make_float2(rs, rs)), make_float2(w[2 * i], w[2 * i + 1])));
-        }
+        for (int j = 0; j < 8; ++j) f.norm(j, r0 + j < a.rows ? a.rstd[r0 + j] : 0.f, w);
     }
     // largest magnitudes along this thread's rows and columns
     uint32_t rm[8], all = 0;
@@ -178,6 +205,7 @@ __global__ void __launch_bounds__(kThreads) q8_quant_kernel(const QuantParams p)
         rm[j] = max(mb.x, mb.y);
         all = max(all, rm[j]);
     }
+    if constexpr (PACKED && NORM) f.again();
     if (all >= kInfBits) {                            // rare: infinities become NaN; neither counts
         all = 0;
         uint32_t c8[8];
@@ -193,13 +221,20 @@ __global__ void __launch_bounds__(kThreads) q8_quant_kernel(const QuantParams p)
                 rm[j] = max(rm[j], max(u, w));
                 c8[2 * i] = max(c8[2 * i], u);
                 c8[2 * i + 1] = max(c8[2 * i + 1], w);
-                f.set(j, i, make_float2(inf_to_nan(v.x), inf_to_nan(v.y)));
+                if constexpr (PACKED && NORM) {
+                    const uint32_t nx = u == 0 && mag_bits(v.x) >= kInfBits ? 0x7fffu : 0u;
+                    const uint32_t ny = w == 0 && mag_bits(v.y) >= kInfBits ? 0x7fff0000u : 0u;
+                    f.v[j][i] |= nx | ny;            // the factor's NaN makes the product NaN
+                } else {
+                    f.set(j, i, make_float2(inf_to_nan(v.x), inf_to_nan(v.y)));
+                }
             }
             all = max(all, rm[j]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) cm[i] = F::of_bits(c8[2 * i], c8[2 * i + 1]);
     }
+    if constexpr (PACKED && NORM) f.again();
     float sq_inv = 1.f;
     if (SQUARE) {
         uint32_t* wm = reinterpret_cast<uint32_t*>(colmax);
@@ -273,6 +308,7 @@ __global__ void __launch_bounds__(kThreads) q8_quant_kernel(const QuantParams p)
             }
         }
     }
+    if constexpr (PACKED && NORM && ROWS && COLS) f.again();
     if (COLS) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -338,7 +374,8 @@ template <typename T>
 cudaError_t typed(const QuantParams& p, dion_q8_format fmt, cudaStream_t st)
 {
     const size_t e = sizeof(T);
-    const bool vec = ((uintptr_t)p.a.x % 16 == 0) && (p.a.ldx * e) % 16 == 0 && (p.a.batch == 1 || (p.a.sx * e) % 16 == 0);
+    const bool vec = ((uintptr_t)p.a.x % 16 == 0) && (p.a.ldx * e) % 16 == 0 && (p.a.batch == 1 || (p.a.sx * e) % 16 == 0) &&
+                     (uintptr_t)p.a.weight % 16 == 0;
     if (fmt == DION_E4M3) return vec ? pick<T, DION_E4M3, true>(p, st) : pick<T, DION_E4M3, false>(p, st);
     return vec ? pick<T, DION_E5M2, true>(p, st) : pick<T, DION_E5M2, false>(p, st);
 }
