@@ -143,6 +143,59 @@ __device__ __forceinline__ void pack8(Raw8<float>& r, const float2 (&f)[4])
                             __float_as_uint(f[2 * i + 1].y));
 }
 
+// Eight consecutive values at any address: the 16-byte words that hold them
+// (none that holds no byte of them is read), shifted into place.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_shifted(const T* p)
+{
+    constexpr int W = sizeof(T) * 2;                    // 32-bit words of the values
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uint4* b = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
+    const uint32_t m = (uint32_t)a & 15u;
+    uint32_t w[W + 4];
+#pragma unroll
+    for (int i = 0; i <= W / 4; ++i) {
+        const uint4 u = i < W / 4 || m ? b[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = u.x;
+        w[4 * i + 1] = u.y;
+        w[4 * i + 2] = u.z;
+        w[4 * i + 3] = u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+    if (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = m & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    }
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) r.u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    return r;
+}
+// A lane's eight consecutive values of the block at column c0 of a row that may
+// start anywhere; zeros past the row.
+template <bool SHIFT, typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* row, int c0, int cols, int l)
+{
+    const T* p = row + c0 + 8 * l;
+    Raw8<T> r;
+    if (c0 + 8 * l + 8 <= cols) {
+        if (SHIFT) return load_shifted(p);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+        float2 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = make_float2(c0 + 8 * l + 2 * i < cols ? to_f(p[2 * i]) : 0.f,
+                               c0 + 8 * l + 2 * i + 1 < cols ? to_f(p[2 * i + 1]) : 0.f);
+        pack8(r, f);
+    }
+    return r;
+}
+
 // A lane's eight values of the block at column c0 of a row; zeros past the row.
 template <bool VEC, typename T>
 __device__ __forceinline__ void load8(const T* row, int c0, int cols, int l, float2 (&f)[4])

@@ -126,7 +126,8 @@ __device__ __forceinline__ uint32_t max16_of8(const uint32_t (&v)[8], int l)
     return max(c, __shfl_xor_sync(0xffffffffu, c, 1));
 }
 
-template <typename T, int FMT, bool ROWS, bool COLS, bool SQUARE, bool VEC, bool NORM>
+// SHIFT: rows of x that do not start on 16-byte boundaries.
+template <typename T, int FMT, bool ROWS, bool COLS, bool SQUARE, bool SHIFT, bool NORM>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS && COLS ? 3 : 4) q8_quant_kernel(const QuantParams p)
 {
     constexpr bool PACKED = sizeof(T) == 2;
@@ -142,49 +143,39 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
     const T* x = reinterpret_cast<const T*>(a.x) + (long long)b * a.sx;
 
     F f;
-    if (VEC && r0 + 8 <= a.rows && c0 + kTile <= a.cols) {
+    Raw8<T> u[8];
+    if (r0 + 8 <= a.rows && c0 + kTile <= a.cols && !SHIFT) {
         const T* src = x + (long long)r0 * a.ldx + c0 + 8 * l;
-        if constexpr (sizeof(T) == 2) {
-            uint4 u[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = *reinterpret_cast<const uint4*>(src + j * a.ldx);
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (PACKED) f.v[j][i] = w[i];
-                    else f.v[j][i] = unpack2(w[i]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 u = *reinterpret_cast<const float4*>(src + j * a.ldx), w = *reinterpret_cast<const float4*>(src + j * a.ldx + 4);
-                f.set(j, 0, make_float2(u.x, u.y));
-                f.set(j, 1, make_float2(u.z, u.w));
-                f.set(j, 2, make_float2(w.x, w.y));
-                f.set(j, 3, make_float2(w.z, w.w));
-            }
-        }
+            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) u[j].u[i] = reinterpret_cast<const uint4*>(src + j * a.ldx)[i];
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float2 e[4];
             if (r0 + j < a.rows) {
-                load8<VEC>(x + (long long)(r0 + j) * a.ldx, c0, a.cols, l, e);
+                u[j] = load_raw8<SHIFT>(x + (long long)(r0 + j) * a.ldx, c0, a.cols, l);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = make_float2(0.f, 0.f);
+                for (int i = 0; i < (int)(sizeof(T) / 2); ++i) u[j].u[i] = make_uint4(0, 0, 0, 0);
             }
+        }
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f.set(j, i, e[i]);
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (PACKED) {
+            f.v[j][0] = u[j].u[0].x;
+            f.v[j][1] = u[j].u[0].y;
+            f.v[j][2] = u[j].u[0].z;
+            f.v[j][3] = u[j].u[0].w;
+        } else {
+            unpack8(u[j], f.v[j]);
         }
     }
     if constexpr (NORM) {
         float2 w[4];
-        if (p.wf32) load8<VEC>(reinterpret_cast<const float*>(a.weight), c0, a.cols, l, w);
-        else load8<VEC>(reinterpret_cast<const bf16*>(a.weight), c0, a.cols, l, w);
+        if (p.wf32) unpack8(load_raw8<true>(reinterpret_cast<const float*>(a.weight), c0, a.cols, l), w);
+        else unpack8(load_raw8<true>(reinterpret_cast<const bf16*>(a.weight), c0, a.cols, l), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f.norm(j, r0 + j < a.rows ? a.rstd[r0 + j] : 0.f, w);
     }
@@ -269,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
             const int i = threadIdx.x & 3, lc = threadIdx.x >> 2;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int c = elem<VEC>(lc, 2 * i + e);
+                const int c = 8 * lc + 2 * i + e;
                 const uint32_t sb = scale_byte<FMT>(e ? m1 : m0);
                 colinv[c] = inv_scale(sb);
                 if (c0 + c < a.cols) a.st[(long long)b * a.sst + (long long)(c0 + c) * a.ldst + tr] = (uint8_t)sb;
@@ -286,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
             if (!(l & 1) && r0 + (l >> 1) < a.rows)
                 a.s[(long long)b * a.ss + (long long)(r0 + (l >> 1)) * a.lds + tc] = (uint8_t)byte;
         }
-        const bool in = VEC && c0 + 8 * l + 8 <= a.cols;
+        const bool in = c0 + 8 * l + 8 <= a.cols;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float s = SQUARE ? inv : __shfl_sync(0xffffffffu, inv, (lane & 16) + 2 * j);
@@ -302,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int c = c0 + elem<VEC>(l, i);
+                    const int c = c0 + 8 * l + i;
                     if (c < a.cols) q[j * a.ldq + c] = (uint8_t)(w[i >> 1] >> (8 * (i & 1)));
                 }
             }
@@ -312,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
     if (COLS) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int ca = elem<VEC>(l, 2 * i), cb = elem<VEC>(l, 2 * i + 1);
+            const int ca = 8 * l + 2 * i, cb = ca + 1;
             const float2 inv = SQUARE ? make_float2(sq_inv, sq_inv) : make_float2(colinv[ca], colinv[cb]);
             uint32_t wa[4], wb[4];
 #pragma unroll
@@ -347,37 +338,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
     }
 }
 
-template <typename T, int FMT, bool ROWS, bool COLS, bool SQUARE, bool VEC>
+template <typename T, int FMT, bool ROWS, bool COLS, bool SQUARE, bool SHIFT>
 cudaError_t go(const QuantParams& p, cudaStream_t st)
 {
     const dim3 grid((unsigned)(cdiv(p.a.rows, kTile) * p.tiles_c), (unsigned)p.a.batch);
     if (p.a.rstd)
-        return launch("q8_quantize_norm", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, VEC, true>, grid,
+        return launch("q8_quantize_norm", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, SHIFT, true>, grid,
                       dim3(kThreads), 0, st, p);
-    return launch("q8_quantize", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, VEC, false>, grid, dim3(kThreads), 0,
+    return launch("q8_quantize", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, SHIFT, false>, grid, dim3(kThreads), 0,
                   st, p);
 }
 
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, bool SHIFT>
 cudaError_t pick(const QuantParams& p, cudaStream_t st)
 {
     const bool rows = p.a.q != nullptr, cols = p.a.qt != nullptr;
     if (p.a.square) {
-        if (rows && cols) return go<T, FMT, true, true, true, VEC>(p, st);
-        return rows ? go<T, FMT, true, false, true, VEC>(p, st) : go<T, FMT, false, true, true, VEC>(p, st);
+        if (rows && cols) return go<T, FMT, true, true, true, SHIFT>(p, st);
+        return rows ? go<T, FMT, true, false, true, SHIFT>(p, st) : go<T, FMT, false, true, true, SHIFT>(p, st);
     }
-    if (rows && cols) return go<T, FMT, true, true, false, VEC>(p, st);
-    return rows ? go<T, FMT, true, false, false, VEC>(p, st) : go<T, FMT, false, true, false, VEC>(p, st);
+    if (rows && cols) return go<T, FMT, true, true, false, SHIFT>(p, st);
+    return rows ? go<T, FMT, true, false, false, SHIFT>(p, st) : go<T, FMT, false, true, false, SHIFT>(p, st);
 }
 
 template <typename T>
 cudaError_t typed(const QuantParams& p, dion_q8_format fmt, cudaStream_t st)
 {
     const size_t e = sizeof(T);
-    const bool vec = ((uintptr_t)p.a.x % 16 == 0) && (p.a.ldx * e) % 16 == 0 && (p.a.batch == 1 || (p.a.sx * e) % 16 == 0) &&
-                     (uintptr_t)p.a.weight % 16 == 0;
-    if (fmt == DION_E4M3) return vec ? pick<T, DION_E4M3, true>(p, st) : pick<T, DION_E4M3, false>(p, st);
-    return vec ? pick<T, DION_E5M2, true>(p, st) : pick<T, DION_E5M2, false>(p, st);
+    const bool shift = (uintptr_t)p.a.x % 16 || (p.a.ldx * e) % 16 || (p.a.batch > 1 && (p.a.sx * e) % 16);
+    if (fmt == DION_E4M3) return shift ? pick<T, DION_E4M3, true>(p, st) : pick<T, DION_E4M3, false>(p, st);
+    return shift ? pick<T, DION_E5M2, true>(p, st) : pick<T, DION_E5M2, false>(p, st);
 }
 
 }  // namespace
