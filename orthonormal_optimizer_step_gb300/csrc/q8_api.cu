@@ -50,7 +50,8 @@ extern "C" dion_status dion_q8_quantize(int batch, int rows, int cols, dion_dtyp
         if (qt && (sqt % 16 || sqt < (long long)(cols - 1) * ldqt + rows || sst % 4 || sst < (sc - 1) * ldst + cdiv(rows, 128)))
             return DION_ERR_INVALID_ARG;
     }
-    if (batch > 65535 || !tiles_fit(rows, cols)) return DION_ERR_UNSUPPORTED;
+    // indices round up to whole tiles in 32 bits
+    if (batch > 65535 || rows > 0x7fff0000 || cols > 0x7fff0000 || !tiles_fit(rows, cols)) return DION_ERR_UNSUPPORTED;
     Q8QuantArgs a{};
     a.batch = batch; a.rows = rows; a.cols = cols;
     a.x = x; a.ldx = ldx; a.sx = sx;

@@ -19,9 +19,11 @@ that meets this for any size; tensors of a program's own may be passed as well.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
+from torch import empty, empty_strided
 
 import orthonormal_optimizer_step_gb300 as _od
 
@@ -29,6 +31,8 @@ _E4M3, _E5M2, _E8M0 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0f
 _F32 = torch.float32
 _FORMATS = {_E4M3: 0, _E5M2: 1}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_FORMS = {"rows": (True, False), "cols": (False, True), "both": (True, True)}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _status = {}
 
 
@@ -38,7 +42,11 @@ class Q8(NamedTuple):
     scale: torch.Tensor
 
 
-# ---- checks and layout (the calls below are short: a few microseconds of host time count)
+# Small calls are bound by the host: their checks read each attribute once, and
+# the common form of an argument is recognised before a failing one is explained.
+# With `stream`, a call makes it current and starts over, so that what it
+# allocates comes from that stream's pool (memory that another stream's work
+# still uses is then not written early).
 def _type(dtype, what):
     code = _TYPES.get(dtype)
     if code is None:
@@ -54,9 +62,10 @@ def _format(dtype):
 
 
 def _cuda(t, what):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def _same_device(dev, **tensors):
@@ -79,7 +88,7 @@ def _pitch(rows, cols, ld, one, what):
 def _matrix(t, what):
     """(matrix of t's rows, row pitch) of a tensor [..., cols], without a copy."""
     if t.dim() == 2:
-        (rows, cols), (ld, one) = t.shape, t.stride()
+        (_, cols), (ld, one) = t.shape, t.stride()
         if one == 1 and ld >= cols:
             return t, ld
     else:
@@ -93,37 +102,32 @@ def _matrix(t, what):
 
 
 def _vector(t, n, what):
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n}")
 
 
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _empty(shape, dtype, device, stream):
-    """Memory from the pool of the stream that the call runs on, so that what
-    another stream's work still uses is not written early."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def new_q8(rows, cols, *, dtype=_E4M3, square=False, batch=None, device="cuda", stream=None):
+def new_q8(rows, cols, *, dtype=_E4M3, square=False, batch=None, device="cuda"):
     """An uninitialized quantized matrix (`batch` of them) with aligned rows."""
     _format(dtype)
-    return _new_q8(rows, cols, dtype, square, batch, device, stream)
+    return _new_q8(rows, cols, dtype, square, batch, device)
 
 
-def _new_q8(rows, cols, dtype, square, batch, device, stream):
-    sr, sc = ((rows + 127) // 128 if square else rows), (cols + 127) // 128
-    ld, lds = (cols + 15) // 16 * 16, (sc + 3) // 4 * 4
+def _new_q8(rows, cols, dtype, square, batch, device):
+    sr, sc = (rows + 127 >> 7 if square else rows), cols + 127 >> 7
+    ld, lds = cols + 15 & -16, sc + 3 & -4
+    # (the allocator's sizes are multiples of 512 bytes, so a last row of scales
+    # can be read to a multiple of 4 as well)
     if batch is None:
-        data, scale = _empty((rows, ld), dtype, device, stream), _empty((sr, lds), _E8M0, device, stream)
+        data = (empty((rows, cols), dtype=dtype, device=device) if ld == cols else
+                empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device))
+        scale = (empty((sr, sc), dtype=_E8M0, device=device) if lds == sc else
+                 empty_strided((sr, sc), (lds, 1), dtype=_E8M0, device=device))
     else:
-        data, scale = _empty((batch, rows, ld), dtype, device, stream), _empty((batch, sr, lds), _E8M0, device, stream)
-    return Q8(data if ld == cols else data[..., :cols], scale if lds == sc else scale[..., :sc])
+        data = (empty((batch, rows, cols), dtype=dtype, device=device) if ld == cols else
+                empty_strided((batch, rows, cols), (rows * ld, ld, 1), dtype=dtype, device=device))
+        scale = (empty((batch, sr, sc), dtype=_E8M0, device=device) if lds == sc else
+                 empty_strided((batch, sr, sc), (sr * lds, lds, 1), dtype=_E8M0, device=device))
+    return Q8(data, scale)
 
 
 def _q8(q, what):
@@ -154,23 +158,22 @@ def _q8(q, what):
     return rows, cols, fmt, ld, lds, sr != rows, dptr, sptr
 
 
-def _out_q8(q, rows, cols, dtype, square, batch, what="out"):
+def _out_q8(q, rows, cols, dtype, square, batch, dev):
     """(data pitch, scale pitch) of a quantized matrix that a call is to write."""
-    _, _, _, ld, lds, _, _, _ = _q8(q, what)
+    _, _, _, ld, lds, _, _, _ = _q8(q, "out")
     shape = (rows, cols) if batch is None else (batch, rows, cols)
     if tuple(q.data.shape) != shape or q.data.dtype is not dtype or q.scale.shape[-2] != ((rows + 127) // 128 if square else rows):
-        raise ValueError(f"{what} does not have the shape, dtype and scales asked for")
+        raise ValueError("out does not have the shape, dtype and scales asked for")
+    _same_device(dev, out=q.data, out_scale=q.scale)
     return ld, lds
 
 
 # ---- status word of the products
-def _status_word(dev, device):
-    w = _status.get(dev)
-    if w is None:
-        t = torch.zeros(1, dtype=torch.int32, device=device)
-        torch.cuda.current_stream(device).synchronize()   # once: later calls may run on any stream
-        w = _status[dev] = (t.data_ptr(), t)
-    return w[0]
+def _status_word(dev):
+    t = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
+    torch.cuda.current_stream(dev).synchronize()   # once: later calls may run on any stream
+    _status[dev] = (t.data_ptr(), t)
+    return _status[dev]
 
 
 def dion_q8_status(device=None) -> int:
@@ -182,6 +185,22 @@ def dion_q8_status(device=None) -> int:
 
 
 # ---- operators
+_NO_Q8 = (None, 0, 0, None, 0, 0)
+
+
+def _q8_args(out, rows, cols, dtype, square, batch, dev, device):
+    """The quantized matrix to write (a new one if `out` is None) and its arguments."""
+    if out is None:
+        out = _new_q8(rows, cols, dtype, square, batch, device)
+        ld, lds = cols + 15 & -16, (cols + 127 >> 7) + 3 & -4
+    else:
+        ld, lds = _out_q8(out, rows, cols, dtype, square, batch, dev)
+    data, scale = out
+    if batch is None:
+        return out, (data.data_ptr(), ld, 0, scale.data_ptr(), lds, 0)
+    return out, (data.data_ptr(), ld, data.stride(0), scale.data_ptr(), lds, scale.stride(0))
+
+
 def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, weight=None, out=None, stream=None):
     """Quantizes x [rows, cols] or [batch, rows, cols] (float32 or bfloat16).
 
@@ -190,14 +209,21 @@ def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, we
     a Q8 or None.  square: one scale for each 128 x 128 block.  With rstd [rows]
     and weight [cols], x * rstd * weight is quantized instead of x.  out: the
     pair (rows, cols) to write into."""
-    if form not in ("rows", "cols", "both"):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dion_q8_quantize(x, form=form, square=square, dtype=dtype, rstd=rstd, weight=weight, out=out)
+    wanted = _FORMS.get(form)
+    if wanted is None:
         raise ValueError(f"form must be 'rows', 'cols' or 'both', got {form!r}")
-    shape, stride = x.shape, x.stride()
-    if len(shape) != 2 and len(shape) != 3:
+    if x.dim() == 2:
+        (rows, cols), (ld, one), batch, sx = x.shape, x.stride(), None, 0
+    elif x.dim() == 3:
+        (batch, rows, cols), (sx, ld, one) = x.shape, x.stride()
+    else:
         raise ValueError("expected a [rows, cols] or [batch, rows, cols] tensor")
-    dt, fmt, dev = _type(x.dtype, "x"), _format(dtype), _cuda(x, "x")
-    rows, cols = shape[-2], shape[-1]
-    batch = shape[0] if len(shape) == 3 else None
+    dt, fmt, dev, device = _type(x.dtype, "x"), _format(dtype), _cuda(x, "x"), x.device
+    if one != 1 or ld < cols:
+        ld = _pitch(rows, cols, ld, one, "x")
     wdt, rptr, wptr = 0, None, None
     if rstd is not None or weight is not None:
         if rstd is None or weight is None or batch is not None:
@@ -209,50 +235,36 @@ def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, we
         _vector(rstd, rows, "rstd")
         _same_device(dev, rstd=rstd, weight=weight)
         rptr, wptr = rstd.data_ptr(), weight.data_ptr()
-    ldx = _pitch(rows, cols, stride[-2], stride[-1], "x")
-    pair, args = [None, None], []
-    for i, r, c in ((0, rows, cols), (1, cols, rows)):
-        if form == ("cols", "rows")[i]:
-            args += (None, 0, 0, None, 0, 0)
-            continue
-        if out is None or out[i] is None:
-            q = _new_q8(r, c, dtype, square, batch, x.device, stream)
-            ld, lds = (c + 15) // 16 * 16, ((c + 127) // 128 + 3) // 4 * 4
-        else:
-            q = out[i]
-            ld, lds = _out_q8(q, r, c, dtype, square, batch)
-            _same_device(dev, out=q.data, out_scale=q.scale)
-        pair[i] = q
-        data, scale = q
-        if batch is None:
-            args += (data.data_ptr(), ld, 0, scale.data_ptr(), lds, 0)
-        else:
-            args += (data.data_ptr(), ld, data.stride(0), scale.data_ptr(), lds, scale.stride(0))
-    if rows == 0 or cols == 0 or batch == 0:
-        return pair[0], pair[1]
-    code = _od.lib().dion_q8_quantize(1 if batch is None else batch, rows, cols, dt, x.data_ptr(), ldx,
-                                      0 if batch is None else stride[0], rptr, wptr, wdt, square, fmt, *args,
-                                      _raw_stream(stream, dev))
-    if code:
-        _od._check(code, "dion_q8_quantize")
-    return pair[0], pair[1]
+    q = qt = None
+    qa = qta = _NO_Q8
+    if wanted[0]:
+        q, qa = _q8_args(None if out is None else out[0], rows, cols, dtype, square, batch, dev, device)
+    if wanted[1]:
+        qt, qta = _q8_args(None if out is None else out[1], cols, rows, dtype, square, batch, dev, device)
+    if rows and cols and batch != 0:
+        code = _od.lib().dion_q8_quantize(1 if batch is None else batch, rows, cols, dt, x.data_ptr(), ld, sx, rptr, wptr,
+                                          wdt, square, fmt, *qa, *qta, _raw_stream(dev))
+        if code:
+            _od._check(code, "dion_q8_quantize")
+    return q, qt
 
 
 def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
     """a b^T [m, n] of quantized matrices a [m, k] and b [n, k], in float32 sums
     rounded once to out_dtype (bfloat16 or float32; that of `out` if given)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dion_q8_matmul(a, b, out=out, out_dtype=out_dtype)
     m, k, af, lda, ldsa, a_sq, aptr, saptr = _q8(a, "a")
     n, k2, bf, ldb, ldsb, b_sq, bptr, sbptr = _q8(b, "b")
     ad, asc = a
     bd, bsc = b
     if k != k2 or ad.dim() != 2 or bd.dim() != 2:
         raise ValueError(f"expected [m, k] and [n, k], got {tuple(ad.shape)} and {tuple(bd.shape)}")
-    dev = ad.get_device()
-    if dev < 0:
-        raise ValueError("a must be a CUDA tensor")
+    dev = _cuda(ad, "a")
     if out is None:
         ct, ldc = _type(out_dtype, "out_dtype"), n
-        out = _empty((m, n), out_dtype, ad.device, stream)
+        out = empty((m, n), dtype=out_dtype, device=ad.device)
     else:
         if out.shape != (m, n):
             raise ValueError(f"out must be {m} x {n}, got {tuple(out.shape)}")
@@ -260,7 +272,7 @@ def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
     if not dev == asc.get_device() == bd.get_device() == bsc.get_device() == out.get_device():
         _same_device(dev, a_scale=asc, b=bd, b_scale=bsc, out=out)
     code = _od.lib().dion_q8_matmul(m, n, k, aptr, lda, af, saptr, ldsa, a_sq, bptr, ldb, bf, sbptr, ldsb, b_sq,
-                                    out.data_ptr(), ldc, ct, _status_word(dev, ad.device), _raw_stream(stream, dev))
+                                    out.data_ptr(), ldc, ct, (_status.get(dev) or _status_word(dev))[0], _raw_stream(dev))
     if code:
         _od._check(code, "dion_q8_matmul")
     return out
@@ -273,6 +285,9 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
     (y, h, rstd): the Q8 of all rows, the sum in x's type and shape (x itself
     without a residual; `h` may be given, also as x or residual) and
     1 / sqrt(mean(h^2) + eps) of each row, which the backward pass reads."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dion_rms_norm_q8(x, weight, residual=residual, eps=eps, dtype=dtype, h=h, out=out, rstd=rstd)
     xdt, device = x.dtype, x.device
     dt, wdt, dev = _type(xdt, "x"), _type(weight.dtype, "weight"), _cuda(x, "x")
     x2, ldx = _matrix(x, "x")
@@ -280,28 +295,31 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
     _vector(weight, cols, "weight")
     rptr, ldr, hptr, ldh = None, 0, None, 0
     if residual is not None:
-        if residual.shape != x.shape or residual.dtype is not xdt:
+        shape = x.shape
+        if residual.shape != shape or residual.dtype is not xdt:
             raise ValueError("residual must have x's shape and dtype")
-        if h is None:
-            h = _empty(x.shape, xdt, device, stream)
-        elif h.shape != x.shape or h.dtype is not xdt:
-            raise ValueError("h must have x's shape and dtype")
         r2, ldr = _matrix(residual, "residual")
-        h2, ldh = _matrix(h, "h")
-        rptr, hptr = r2.data_ptr(), h2.data_ptr()
+        if h is None:
+            h = empty(shape, dtype=xdt, device=device)
+            hptr, ldh = h.data_ptr(), cols
+        else:
+            if h.shape != shape or h.dtype is not xdt:
+                raise ValueError("h must have x's shape and dtype")
+            h2, ldh = _matrix(h, "h")
+            hptr = h2.data_ptr()
+        rptr = r2.data_ptr()
         if not dev == residual.get_device() == h.get_device():
             _same_device(dev, residual=residual, h=h)
     elif h is not None:
         raise ValueError("h is written only with a residual")
     if out is None:
-        fmt, ldq, lds = _format(dtype), (cols + 15) // 16 * 16, ((cols + 127) // 128 + 3) // 4 * 4
-        out = _new_q8(rows, cols, dtype, False, None, device, stream)
+        fmt, ldq, lds = _format(dtype), cols + 15 & -16, (cols + 127 >> 7) + 3 & -4
+        out = _new_q8(rows, cols, dtype, False, None, device)
     else:
         fmt = _format(out.data.dtype)
-        ldq, lds = _out_q8(out, rows, cols, out.data.dtype, False, None)
-        _same_device(dev, out=out.data, out_scale=out.scale)
+        ldq, lds = _out_q8(out, rows, cols, out.data.dtype, False, None, dev)
     if rstd is None:
-        rstd = _empty((rows,), _F32, device, stream)
+        rstd = empty((rows,), dtype=_F32, device=device)
     else:
         if rstd.dtype is not _F32:
             raise TypeError(f"rstd must be float32, got {rstd.dtype}")
@@ -311,12 +329,13 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
     if rows and cols:
         code = _od.lib().dion_rms_norm_q8(rows, cols, dt, x2.data_ptr(), ldx, rptr, ldr, weight.data_ptr(), wdt, eps,
                                           hptr, ldh, fmt, out[0].data_ptr(), ldq, out[1].data_ptr(), lds,
-                                          rstd.data_ptr(), _raw_stream(stream, dev))
+                                          rstd.data_ptr(), _raw_stream(dev))
         if code:
             _od._check(code, "dion_rms_norm_q8")
     return out, (x if residual is None else h), rstd
 
 
+@functools.lru_cache(maxsize=256)
 def dion_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
     out = ctypes.c_size_t(0)
     _od._check(_od.lib().dion_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)),
@@ -329,37 +348,46 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     (unquantized) rows, and dh, that of h along the residual stream, which is
     added to dx.  dx is the gradient of both x and residual and may be dy or dh
     itself; dweight is float32."""
-    ydt, shape = dy.dtype, dy.shape
-    dt, dev, device = _type(ydt, "dy"), _cuda(dy, "dy"), dy.device
-    if dx is None:
-        dx = _empty(shape, ydt, device, stream)
-    for t in (h, dx) if dh is None else (h, dx, dh):
-        if t.shape != shape or t.dtype is not ydt:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dion_rms_norm_backward(dy, h, rstd, weight, dh=dh, dx=dx, dweight=dweight, workspace=workspace)
+    ydt, shape, device = dy.dtype, dy.shape, dy.device
+    dt, wdt, dev = _type(ydt, "dy"), _type(weight.dtype, "weight"), _cuda(dy, "dy")
+    for t in (h, dx, dh):
+        if t is not None and (t.shape != shape or t.dtype is not ydt):
             raise ValueError(f"{'h' if t is h else 'dx' if t is dx else 'dh'} must have dy's shape and dtype")
-    (y2, ldy), (h2, ldh), (x2, ldx) = _matrix(dy, "dy"), _matrix(h, "h"), _matrix(dx, "dx")
+    (y2, ldy), (h2, ldh) = _matrix(dy, "dy"), _matrix(h, "h")
+    rows, cols = y2.shape
     dptr, lddh = None, 0
     if dh is not None:
         d2, lddh = _matrix(dh, "dh")
         dptr = d2.data_ptr()
         _same_device(dev, dh=dh)
-    rows, cols = y2.shape
-    wdt = _type(weight.dtype, "weight")
+    if dx is None:
+        dx = empty(shape, dtype=ydt, device=device)
+        xptr, ldx = dx.data_ptr(), cols
+    else:
+        x2, ldx = _matrix(dx, "dx")
+        xptr = x2.data_ptr()
     _vector(weight, cols, "weight")
     if dweight is None:
-        dweight = _empty((cols,), _F32, device, stream)
+        dweight = empty((cols,), dtype=_F32, device=device)
     if rstd.dtype is not _F32 or dweight.dtype is not _F32:
         raise TypeError("rstd and dweight must be float32")
     _vector(rstd, rows, "rstd")
     _vector(dweight, cols, "dweight")
     if workspace is None:
-        workspace = _empty((max(256, dion_rms_norm_backward_workspace_size(rows, cols)),), torch.uint8, device, stream)
-    if not dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device() == workspace.get_device():
+        nbytes = max(256, dion_rms_norm_backward_workspace_size(rows, cols))
+        workspace = empty((nbytes,), dtype=torch.uint8, device=device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    if not (dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device()
+            == workspace.get_device()):
         _same_device(dev, h=h, rstd=rstd, weight=weight, dx=dx, dweight=dweight, workspace=workspace)
     if cols:
-        code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh,
-                                                rstd.data_ptr(), weight.data_ptr(), wdt, dptr, lddh, x2.data_ptr(), ldx,
-                                                dweight.data_ptr(), workspace.data_ptr(),
-                                                workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+        code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh, rstd.data_ptr(),
+                                                weight.data_ptr(), wdt, dptr, lddh, xptr, ldx, dweight.data_ptr(),
+                                                workspace.data_ptr(), nbytes, _raw_stream(dev))
         if code:
             _od._check(code, "dion_rms_norm_backward")
     return dx, dweight

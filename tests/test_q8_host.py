@@ -43,6 +43,7 @@ def test_quantize_empty_and_too_large(lib):
     for kw in (dict(batch=0), dict(rows=0), dict(cols=0)):
         assert quant(lib, **kw) == OK
     assert quant(lib, batch=65536, sx=1 << 14, sq=1 << 14, ss=256) == UNSUPPORTED
+    assert quant(lib, rows=0x7fffffff) == UNSUPPORTED
 
 
 def matmul(lib, **kw):
