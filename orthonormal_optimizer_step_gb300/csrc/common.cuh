@@ -78,28 +78,47 @@ cudaError_t launch(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 b
     return e;
 }
 
-// The same with thread-block clusters of `cluster` consecutive CTAs.
+// For kernels that call wait_previous() before they touch memory: the launch
+// may begin while the stream's previous kernel is still finishing (if that
+// kernel has called allow_next(); otherwise when it ends).  launch_cluster:
+// with thread-block clusters of `cluster` consecutive CTAs.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
                            cudaStream_t s, Args&&... args)
 {
     if (grid.x == 0 || grid.y == 0 || grid.z == 0) return cudaSuccess;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const int slot = prof_begin(name, s);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     prof_end(slot, s);
     return e;
 }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              Args&&... args)
+{
+    return launch_cluster(name, kernel, grid, block, 1, smem, s, std::forward<Args>(args)...);
+}
+
+// Device side of the two.  wait_previous: the stream's earlier
+// kernels are complete and their writes visible; every thread that reads or
+// writes memory of the caller's calls it first (or is ordered after one that
+// did).  allow_next: the next kernel's CTAs may take what this one leaves free.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Raises a kernel's dynamic shared-memory limit on the current device, once
 // per device (the attribute is per device).  `done` is a bit mask of devices

@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
     else __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 0) allow_next();
     const int tiles = p.tiles_p * p.tiles_q;
     const int kblocks = (p.k + 127) / 128;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
         if (elect_one()) {
             tc::tma_prefetch_desc(&tmP);
             tc::tma_prefetch_desc(&tmQ);
+            wait_previous();             // (the epilogue's stores come after these loads)
             int stage = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -463,6 +465,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             }
         }
     } else if (warp == 2) {
+        wait_previous();
         int slot = 0;
         uint32_t sph = 0;
         bool ok = true;
@@ -626,6 +629,7 @@ __global__ void __launch_bounds__(256, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 0) allow_next();
     const int tile = blockIdx.x / splits, tq = tile % p.tiles_q, tp = tile / p.tiles_q;
     const int kblocks = (p.k + 127) / 128, per = (kblocks + splits - 1) / splits;
     const int kb0 = min(share * per, kblocks), kb1 = min(kb0 + per, kblocks);
@@ -633,6 +637,7 @@ __global__ void __launch_bounds__(256, 1)
 
     if (warp == 0) {
         if (elect_one()) {
+            wait_previous();             // (the stores to C come after these loads)
             int stage = 0;
             uint32_t ph = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -676,6 +681,7 @@ __global__ void __launch_bounds__(256, 1)
             if (ok && kb1 > kb0) commit<1>(acc_full);
         }
     } else if (warp == 2) {
+        wait_previous();
         int slot = 0;
         uint32_t sph = 0;
         bool ok = true;
@@ -814,7 +820,7 @@ cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
     const unsigned grid = (unsigned)(CG * std::min<long long>(tiles, num_sms() / CG));
     const dim3 block(128 + 32 * C::EW);
     if (CG == 1)
-        return launch("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, C::SMEM, st, tmP, tmQ, tmC,
+        return launch_overlapped("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, C::SMEM, st, tmP, tmQ, tmC,
                       p);
     return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, tmC, p);
 }

@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(1024) norm_q8_kernel(const NormParams p)
 {
     __shared__ float red[32];
     const Q8NormArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const long long row = blockIdx.x;
     const int l = threadIdx.x & 15, hw = threadIdx.x >> 4, nhw = blockDim.x >> 4;
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
@@ -156,6 +158,8 @@ __global__ void __launch_bounds__(1024) norm_q8_long_kernel(const NormParams p)
 {
     __shared__ float red[32];
     const Q8NormArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const long long row = blockIdx.x;
     const int l = threadIdx.x & 15, hw = threadIdx.x >> 4, nhw = blockDim.x >> 4;
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
@@ -247,6 +251,8 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) norm_q8_stream_kernel(co
     extern __shared__ uint4 ring_smem[];
     __shared__ float red[2][32];
     const Q8NormArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const Ring<T, RES ? 2 : 1, NV, S> ring{ring_smem + threadIdx.x};
     const int l = threadIdx.x & 15, hw = threadIdx.x >> 4, nhw = blockDim.x >> 4;
     const int cols = a.cols, c = hw * 128 + 8 * l, kstep = nhw * 128;     // chunk k at c + k * kstep
@@ -343,7 +349,7 @@ cudaError_t norm_stream(const NormParams& p, const StreamPlan& s, cudaStream_t s
     static std::atomic<unsigned long long> attr{0};
     const cudaError_t e = smem_attr_once((const void*)norm_q8_stream_kernel<T, FMT, RES, NV, kNormStages>, (int)kRingRoom, attr);
     if (e != cudaSuccess) return e;
-    return launch("rms_norm_q8_stream", norm_q8_stream_kernel<T, FMT, RES, NV, kNormStages>, dim3((unsigned)(num_sms() * s.ctas)),
+    return launch_overlapped("rms_norm_q8_stream", norm_q8_stream_kernel<T, FMT, RES, NV, kNormStages>, dim3((unsigned)(num_sms() * s.ctas)),
                   dim3((unsigned)s.threads), s.smem, st, p);
 }
 
@@ -366,10 +372,10 @@ cudaError_t norm_go(const NormParams& p, cudaStream_t st)
     const dim3 grid((unsigned)p.a.rows);
     // two half-warps a warp, as many blocks a half-warp as it takes
     if (blocks <= 16)
-        return launch("rms_norm_q8", norm_q8_kernel<T, FMT, VEC, 1>, grid, dim3((unsigned)cdiv(blocks, 2) * 32), 0, st, p);
+        return launch_overlapped("rms_norm_q8", norm_q8_kernel<T, FMT, VEC, 1>, grid, dim3((unsigned)cdiv(blocks, 2) * 32), 0, st, p);
     if (blocks <= 128)
-        return launch("rms_norm_q8", norm_q8_kernel<T, FMT, VEC, 2>, grid, dim3((unsigned)cdiv(blocks, 4) * 32), 0, st, p);
-    return launch("rms_norm_q8_long", norm_q8_long_kernel<T, FMT, VEC>, grid, dim3(1024), 0, st, p);
+        return launch_overlapped("rms_norm_q8", norm_q8_kernel<T, FMT, VEC, 2>, grid, dim3((unsigned)cdiv(blocks, 4) * 32), 0, st, p);
+    return launch_overlapped("rms_norm_q8_long", norm_q8_long_kernel<T, FMT, VEC>, grid, dim3(1024), 0, st, p);
 }
 
 template <typename T>
@@ -429,6 +435,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_bwd_kernel(const Bw
 {
     __shared__ float red[2][32];
     const NormBwdArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const int l = threadIdx.x & 15, hw = threadIdx.x >> 4, nhw = blockDim.x >> 4;
     float2 dw[NV][4], w[4];
 #pragma unroll
@@ -477,6 +485,8 @@ __global__ void __maxnreg__(NV <= 2 ? 80 : 128) norm_bwd_stream_kernel(const Bwd
     extern __shared__ uint4 ring_smem[];
     __shared__ float red[2][32];
     const NormBwdArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const Ring<T, DH ? 3 : 2, NV, S> ring{ring_smem + threadIdx.x};
     float4* wmine = reinterpret_cast<float4*>(ring_smem + (Ring<T, DH ? 3 : 2, NV, S>::bytes(blockDim.x)) / 16) + threadIdx.x;
     const int l = threadIdx.x & 15, hw = threadIdx.x >> 4, nhw = blockDim.x >> 4;
@@ -572,6 +582,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const BwdParams p)
 {
     __shared__ float red[2][32];
     const NormBwdArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const int l = threadIdx.x & 15, hw = threadIdx.x >> 4, nhw = blockDim.x >> 4;
     float* part = a.part + (long long)blockIdx.x * a.cols;
     int flip = 0;
@@ -620,6 +632,8 @@ template <int W>
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int groups, int cols, float* dw)
 {
     __shared__ float t[W][33];
+    allow_next();
+    wait_previous();
     const int x = threadIdx.x % W, y = threadIdx.x / W, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * W + x;
     float s = 0.f;
@@ -661,7 +675,7 @@ cudaError_t bwd_stream(const BwdParams& p, const StreamPlan& s, cudaStream_t st)
     static std::atomic<unsigned long long> attr{0};
     const cudaError_t e = smem_attr_once((const void*)norm_bwd_stream_kernel<T, DH, NV, bwd_stages(NV)>, (int)kRingRoom, attr);
     if (e != cudaSuccess) return e;
-    return launch("rms_norm_backward_stream", norm_bwd_stream_kernel<T, DH, NV, bwd_stages(NV)>, dim3((unsigned)(num_sms() * s.ctas)),
+    return launch_overlapped("rms_norm_backward_stream", norm_bwd_stream_kernel<T, DH, NV, bwd_stages(NV)>, dim3((unsigned)(num_sms() * s.ctas)),
                   dim3((unsigned)s.threads), s.smem, st, p);
 }
 
@@ -688,9 +702,9 @@ cudaError_t bwd_rows(const BwdParams& p, int& groups, cudaStream_t st)
     }
     groups = bwd_groups(p.a.rows, cols);
     const dim3 grid((unsigned)groups), block((unsigned)bwd_threads(cols));
-    if (blocks <= 64) return launch("rms_norm_backward", norm_bwd_kernel<T, VEC, 1>, grid, block, 0, st, p);
-    if (blocks <= 128) return launch("rms_norm_backward", norm_bwd_kernel<T, VEC, 4>, grid, block, 0, st, p);
-    return launch("rms_norm_backward_long", norm_bwd_long_kernel<T, VEC>, grid, block, 0, st, p);
+    if (blocks <= 64) return launch_overlapped("rms_norm_backward", norm_bwd_kernel<T, VEC, 1>, grid, block, 0, st, p);
+    if (blocks <= 128) return launch_overlapped("rms_norm_backward", norm_bwd_kernel<T, VEC, 4>, grid, block, 0, st, p);
+    return launch_overlapped("rms_norm_backward_long", norm_bwd_long_kernel<T, VEC>, grid, block, 0, st, p);
 }
 
 template <typename T>
@@ -706,9 +720,9 @@ cudaError_t bwd_typed(const BwdParams& p, cudaStream_t st)
     const cudaError_t err = vec ? bwd_rows<T, true>(p, groups, st) : bwd_rows<T, false>(p, groups, st);
     if (err != cudaSuccess) return err;
     if (a.cols < 1024)
-        return launch("rms_norm_backward_sum", norm_bwd_sum_kernel<8>, dim3((unsigned)cdiv(a.cols, 8)), dim3(1024), 0, st,
+        return launch_overlapped("rms_norm_backward_sum", norm_bwd_sum_kernel<8>, dim3((unsigned)cdiv(a.cols, 8)), dim3(1024), 0, st,
                       (const float*)a.part, groups, a.cols, a.dw);
-    return launch("rms_norm_backward_sum", norm_bwd_sum_kernel<32>, dim3((unsigned)cdiv(a.cols, 32)), dim3(1024), 0, st,
+    return launch_overlapped("rms_norm_backward_sum", norm_bwd_sum_kernel<32>, dim3((unsigned)cdiv(a.cols, 32)), dim3(1024), 0, st,
                   (const float*)a.part, groups, a.cols, a.dw);
 }
 

@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : NORM ? 3 : ROWS
     __shared__ typename F::Max colmax[(COLS || SQUARE) ? kThreads / 32 : 1][kTile / 2];
     __shared__ float colinv[kTile];
     const Q8QuantArgs& a = p.a;
+    allow_next();
+    wait_previous();
     const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c, b = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
     const int g = warp * 2 + half;                    // row granule of this half-warp
@@ -343,9 +345,9 @@ cudaError_t go(const QuantParams& p, cudaStream_t st)
 {
     const dim3 grid((unsigned)(cdiv(p.a.rows, kTile) * p.tiles_c), (unsigned)p.a.batch);
     if (p.a.rstd)
-        return launch("q8_quantize_norm", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, SHIFT, true>, grid,
+        return launch_overlapped("q8_quantize_norm", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, SHIFT, true>, grid,
                       dim3(kThreads), 0, st, p);
-    return launch("q8_quantize", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, SHIFT, false>, grid, dim3(kThreads), 0,
+    return launch_overlapped("q8_quantize", q8_quant_kernel<T, FMT, ROWS, COLS, SQUARE, SHIFT, false>, grid, dim3(kThreads), 0,
                   st, p);
 }
 
