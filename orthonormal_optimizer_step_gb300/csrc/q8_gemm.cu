@@ -578,11 +578,12 @@ template <int BN>
 struct SplitCfg {
     static constexpr int BM = 128;
     static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = BN * 128, STAGE = P_BYTES + Q_BYTES;
-    static constexpr int STAGES = BN >= 128 ? 6 : 8;
-    static constexpr uint32_t SF_BYTES = 1024;           // scale words of 128 rows of each operand
+    static constexpr int STAGES = BN > 128 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int SFQ = (BN + 127) / 128;
+    static constexpr uint32_t SF_BYTES = 512 * (1 + SFQ);
     static constexpr uint32_t ACC = BN < 32 ? 32 : BN;
-    static constexpr uint32_t SF_COL = ACC, SF_COLS = 8;
-    static constexpr uint32_t TMEM = BN <= 32 ? 64 : BN == 64 ? 128 : 256;
+    static constexpr uint32_t SF_COL = ACC, SF_COLS = 4 + 4 * SFQ;
+    static constexpr uint32_t TMEM = BN <= 32 ? 64 : BN == 64 ? 128 : BN == 128 ? 256 : 512;
     // Sums [column][128 rows] float, in the place of the stages, which the MMAs have all read by then.
     static constexpr uint32_t SUMS = BN * 512;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kSfSlots * SF_BYTES + 512;
@@ -661,7 +662,8 @@ __global__ void __launch_bounds__(256, 1)
                     tc::tc_fence_after();
                     const uint32_t src = tc::smem_u32(sf + slot * C::SF_BYTES);
                     tmem_cp_scales<1>(sfp, src);
-                    tmem_cp_scales<1>(sfq, src + 512);
+#pragma unroll
+                    for (int i = 0; i < C::SFQ; ++i) tmem_cp_scales<1>(sfq + 4 * i, src + 512 * (1 + i));
                 }
                 if (!(ok = tc::mbar_wait(&full[stage], ph, abrt, p.status))) break;
                 tc::tc_fence_after();
@@ -687,12 +689,14 @@ __global__ void __launch_bounds__(256, 1)
         bool ok = true;
         const int g1 = kb1 > kb0 ? (kb1 + 3) / 4 : 0;
         for (int g0 = kb0 / 4; g0 < g1 && ok; g0 += kSfBatch) {
-            uint4 w[kSfBatch][2];
+            uint4 w[kSfBatch][1 + C::SFQ];
 #pragma unroll
             for (int j = 0; j < kSfBatch; ++j) {
                 if (g0 + j >= g1) break;
                 w[j][0] = scale_words(p.sp, p.ldsp, p.sp_shift, p.sp_rows, prow, C::BM, g0 + j, lane);
-                w[j][1] = scale_words(p.sq, p.ldsq, p.sq_shift, p.sq_rows, qrow, BN, g0 + j, lane);
+#pragma unroll
+                for (int i = 0; i < C::SFQ; ++i)
+                    w[j][1 + i] = scale_words(p.sq, p.ldsq, p.sq_shift, p.sq_rows, qrow + 128 * i, BN - 128 * i, g0 + j, lane);
             }
 #pragma unroll
             for (int j = 0; j < kSfBatch; ++j) {
@@ -700,8 +704,8 @@ __global__ void __launch_bounds__(256, 1)
                 ok = tc::mbar_wait(&sf_empty[slot], sph ^ 1, abrt, p.status);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 uint4* dst = reinterpret_cast<uint4*>(sf + slot * C::SF_BYTES);
-                dst[lane] = w[j][0];
-                dst[32 + lane] = w[j][1];
+#pragma unroll
+                for (int i = 0; i < 1 + C::SFQ; ++i) dst[32 * i + lane] = w[j][i];
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sf_full[slot]);
@@ -822,7 +826,7 @@ cudaError_t gemm_go(const Q8MatArgs& a, cudaStream_t st)
     if (CG == 1)
         return launch_overlapped("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, C::SMEM, st, tmP, tmQ, tmC,
                       p);
-    return launch_cluster("q8_matmul", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, tmC, p);
+    return launch_cluster("q8_matmul_pair", q8_gemm_kernel<CG, BN, F32, ROWS>, dim3(grid), block, CG, C::SMEM, st, tmP, tmQ, tmC, p);
 }
 
 template <int BN, bool F32>
@@ -869,6 +873,13 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     if (m <= 16) return gemm_narrow<16, F32>(a, st);
     if (m <= 32) return gemm_narrow<32, F32>(a, st);
     if (m <= 64) return gemm_narrow<64, F32>(a, st);
+    // All rows of A in one 256-wide tile, where two 128-wide ones are too many
+    // for shares: 200x4096x14336 22.3 us against 27.3, 192x4096x8192 17.4 against
+    // 18.9; short contractions lose (200x4096x4096 13.9 against 10.2).
+    if (m > 128 && m <= 256 && kb >= 64 && shares(2 * cdiv(n, 128), kb) == 1) {
+        const int s = shares(cdiv(n, 128), kb);
+        if (s > 1) return gemm_split<256, F32>(a, s, st);
+    }
     // TMA stores move whole 16-byte words: C's rows start and end on such boundaries
     const bool aligned = (uintptr_t)a.c % 16 == 0 && (a.ldc * (F32 ? 4 : 2)) % 16 == 0 && n % (F32 ? 4 : 8) == 0;
     // 128 x 128 tiles of one CTA against tiles of a pair, 256 x 256 or 256 x 224

@@ -170,10 +170,33 @@ def test_matmul_sizes(m, n, k):
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
 @pytest.mark.parametrize("m,n,k", [(512, 768, 768), (1024, 2304, 768), (257, 4096, 4096), (1000, 1500, 8200),
-                                   (2048, 2048, 256), (5, 4096, 14336), (100, 64, 16384), (3000, 40, 128)])
+                                   (2048, 2048, 256), (5, 4096, 14336), (200, 4000, 8300), (256, 3500, 8192), (1000, 6144, 2000),
+                                   (2048, 4608, 1030), (100, 64, 16384), (3000, 40, 128)])
 def test_matmul_larger(m, n, k, out_dtype):
     check_matmul(q8_operand(m, k, square=True), q8_operand(n, k, square=True, seed=1), out_dtype)
     check_matmul(q8_operand(m, k), q8_operand(n, k, seed=1), out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("m,n,k", [(395, 4984, 2000), (601, 5632, 4000), (397, 4865, 4000), (1001, 4104, 4100)])
+def test_matmul_pairs(m, n, k, out_dtype):
+    """Sizes that CTA pairs take (224 and 256 wide, and 256 wide with C's rows
+    unaligned), whole and into a part of a larger matrix."""
+    a, b = q8_operand(m, k, fmt=E5M2), q8_operand(n, k, square=True, seed=1)
+    va, vb = (torch.from_numpy(ref.values(q)).cuda() for q in (a, b))
+    want, size = (va @ vb.T).cpu().numpy(), (va.abs() @ vb.abs().T).cpu().numpy()
+    big = torch.full((m + 2, n + 24), 7.0, dtype=out_dtype, device="cuda")
+    with od.profile() as p:
+        c = od.dion_q8_matmul(a, b, out_dtype=out_dtype)
+        od.dion_q8_matmul(a, b, out=big[1:m + 1, 8:8 + n])
+    torch.cuda.synchronize()
+    assert od.dion_q8_status() == 0
+    assert set(p.read()) == {"q8_matmul_pair"}
+    tol = (k / 32 + 32) * 2.0 ** -23 * size + rounding(want, out_dtype)
+    assert np.all(np.abs(ref.f64(c) - want) <= tol)
+    assert torch.equal(big[1:m + 1, 8:8 + n], c)
+    big[1:m + 1, 8:8 + n] = 7.0
+    assert bool((big == 7).all())
 
 
 @pytest.mark.parametrize("af", [E4M3, E5M2])
@@ -299,6 +322,28 @@ def test_norm(rows, cols, residual, dtype, wdtype, fmt):
     check_norm(x, r, w, 1e-6, fmt, od.dion_rms_norm_q8(x, w, residual=r, dtype=fmt))
 
 
+# rows enough for the kernels that stream them: one, two and four chunks a thread, some of them past the row
+STREAM_SIZES = [(5100, 72), (5100, 512), (3100, 1032), (1300, 4096), (1300, 4104), (700, 8192), (340, 16384)]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", STREAM_SIZES)
+def test_norm_streamed(rows, cols, residual):
+    x, w = randn(rows, cols, dtype=BF16, spread=0.5), (1 + 0.1 * randn(cols, seed=1)).to(BF16)
+    r = randn(rows, cols, dtype=BF16, seed=2, std=3.0) if residual else None
+    x[rows - 1, 3] = float("nan")
+    want = od.dion_rms_norm_q8(x[:200], w, residual=None if r is None else r[:200])       # a row a CTA
+    with od.profile() as p:
+        got = od.dion_rms_norm_q8(x, w, residual=r, h=None if r is None else r.clone())
+    torch.cuda.synchronize()
+    assert set(p.read()) == {"rms_norm_q8_stream"}
+    assert torch.equal(got[1][:200], want[1][:200]) and torch.allclose(got[2][:200], want[2], rtol=TOL_RSTD, atol=0)
+    q, h, rstd = got
+    assert bool(torch.isnan(q.data[rows - 1].float()).all()) and bool(torch.isnan(rstd[rows - 1]))
+    keep = torch.arange(rows, device="cuda") != rows - 1
+    check_norm(x[keep], None if r is None else r[keep], w, 1e-6, E4M3, (od.Q8(q.data[keep], q.scale[keep]), h[keep], rstd[keep]))
+
+
 def test_norm_shapes_strides_and_in_place():
     w = 1 + 0.1 * randn(300, seed=1)
     base = randn(4, 50, 333, dtype=BF16)
@@ -355,6 +400,20 @@ def test_backward(rows, cols, residual, dtype, wdtype):
     dh = randn(rows, cols, dtype=dtype, seed=3, std=0.01) if residual else None
     rstd = 1.0 / torch.sqrt(h.float().square().mean(1) + 1e-6)
     check_backward(dy, h, rstd, w, dh, od.dion_rms_norm_backward(dy, h, rstd, w, dh=dh), dtype)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", STREAM_SIZES)
+def test_backward_streamed(rows, cols, residual):
+    h, w = randn(rows, cols, dtype=BF16, spread=0.5), (1 + 0.1 * randn(cols, seed=1)).to(BF16)
+    dy = randn(rows, cols, dtype=BF16, seed=2, std=0.01)
+    dh = randn(rows, cols, dtype=BF16, seed=3, std=0.01) if residual else None
+    rstd = 1.0 / torch.sqrt(h.float().square().mean(1) + 1e-6)
+    with od.profile() as p:
+        got = od.dion_rms_norm_backward(dy, h, rstd, w, dh=dh, dx=None if dh is None else dh.clone())
+    torch.cuda.synchronize()
+    assert set(p.read()) == {"rms_norm_backward_stream", "rms_norm_backward_sum"}
+    check_backward(dy, h, rstd, w, dh, got, BF16)
 
 
 def test_backward_against_differences():
