@@ -58,8 +58,8 @@ __host__ uint32_t idesc_mx(int M, int N, uint32_t fmt_m, uint32_t fmt_n)
 }
 __device__ __forceinline__ uint32_t idesc_sf(uint32_t sel) { return (sel << 4) | (sel << 29); }
 
-// CG = 2: the two CTAs of a pair work on one tile, each with its 128 rows of B
-// and half of the tile's rows of A in its own shared memory; the pair's first
+// CG = 2: the two CTAs of a pair work on one tile, each with its 128 rows of P
+// and half of the tile's rows of Q in its own shared memory; the pair's first
 // CTA issues for both.
 template <int CG>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
@@ -228,11 +228,11 @@ static_assert(kSfBatch == 4, "scale_words4 loads four");
 
 template <int CG, int BN>
 struct Cfg {
-    static constexpr int BM = 128;                     // rows of B that a CTA holds
-    static constexpr int QROWS = BN / CG;              // rows of A that a CTA holds
+    static constexpr int BM = 128;                     // rows of P that a CTA holds
+    static constexpr int QROWS = BN / CG;              // rows of Q that a CTA holds
     static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = QROWS * 128, STAGE = P_BYTES + Q_BYTES;
     static constexpr int STAGES = QROWS >= 96 ? 6 : 8;
-    static constexpr int SFQ = (BN + 127) / 128;       // 128-row scale groups of A's side
+    static constexpr int SFQ = (BN + 127) / 128;       // 128-row scale groups of Q
     static constexpr uint32_t SF_BYTES = 512 * (1 + SFQ);
     static constexpr uint32_t ACC = BN < 32 ? 32 : BN; // accumulator columns
     // 512 columns hold two accumulators and the scales up to 224 columns wide.
@@ -242,7 +242,7 @@ struct Cfg {
     static constexpr int EW = CG == 2 ? 8 : 4;         // epilogue warps
     static constexpr int EGROUPS = EW / 4;             // warps on each lane quarter, and the columns of one
     static constexpr int ECOLS = EGROUPS == 1 ? BN : (BN / 2 + 31) / 32 * 32;
-    static constexpr uint32_t SF_COL = BUFS * ACC;     // scales: 4 (B) + 4 SFQ (A) columns a slot
+    static constexpr uint32_t SF_COL = BUFS * ACC;     // scales: 4 (P) + 4 SFQ (Q) columns a slot
     static constexpr uint32_t SF_COLS = 4 + 4 * SFQ;
     static constexpr uint32_t TMEM = BN <= 32 ? 128 : BN <= 64 ? 256 : 512;
     static constexpr int OUTS = BN < 32 ? 0 : BN > 224 ? 1 : 2;   // such blocks of an epilogue warp
@@ -312,10 +312,11 @@ __device__ __forceinline__ void store_cols(const GemmParams& p, int row0, int co
 }
 
 // A on the M side: this lane holds columns col0 .. col0 + 31 of row row0 + lane
-// of C, whose rows start and end on 16-byte boundaries.  The warp's block leaves as TMA
-// stores of 32 rows x 64 bytes from shared memory (16-byte word c of row r at
-// c ^ (r / 2 % 4), the 64-byte swizzle, so that the lanes' writes meet no bank
-// twice); what lies outside C is not written.  Shared memory's bandwidth
+// of C, whose rows start and end on 16-byte boundaries (TMA stores whole
+// 16-byte words).  The warp's block leaves as stores of 32 rows x 64 bytes from
+// shared memory (16-byte word c of row r at c ^ (r / 2 % 4), the 64-byte
+// swizzle, so that the lanes' writes meet no bank twice); what lies outside C
+// is not written.  Shared memory's bandwidth
 // bounds the main loop (a block of a 256 x 224 tile moves 30 KB in by TMA and
 // about 30 KB out to the MMAs, at 128 bytes a cycle 470 of its 490 cycles), so
 // the epilogue's use of it counts: 8192 x 14336 x 4096 takes 254 us without

@@ -364,6 +364,24 @@ def test_norm_shapes_strides_and_in_place():
     assert q.data.shape == (0, 300)
 
 
+def test_norm_and_gradient_long_pitches():
+    """Rows more than 2^31 elements apart."""
+    far = 1 << 31
+    big = torch.empty(2 * far + 4096, dtype=BF16, device="cuda")
+
+    def at(off, seed):
+        t = big.as_strided((3, 264), (far, 1), off)
+        t.copy_(randn(3, 264, dtype=BF16, seed=seed))
+        return t
+
+    x, r, dy = at(0, 1), at(264, 2), at(528, 3)
+    h, dx = big.as_strided((3, 264), (far, 1), 800), big.as_strided((3, 264), (far, 1), 1064)
+    w = (1 + 0.1 * randn(264, seed=4)).to(BF16)
+    got = od.dion_rms_norm_q8(x, w, residual=r, h=h)
+    check_norm(x, r, w, 1e-6, E4M3, got)
+    check_backward(dy, h, got[2], w, r, od.dion_rms_norm_backward(dy, h, got[2], w, dh=r, dx=dx), BF16)
+
+
 def test_norm_zero_rows_of_values_and_non_finite_rows():
     x = randn(5, 256)
     x[1], x[2, 7], x[3, 9] = 0.0, float("inf"), float("nan")
