@@ -291,9 +291,10 @@ struct NormBwdArgs {
     const void* dh; long long lddh;
     void* dx; long long lddx;
     float* dw;
-    float* part;                // workspace: row groups x cols partial sums of dw
+    float* part;                // workspace: row groups x cols partial sums of dw; null: a small problem's one launch
 };
 size_t norm_backward_workspace(int rows, int cols);
+bool norm_backward_small(int rows, int cols);    // needs no workspace if dx is apart from dy and h
 cudaError_t rms_norm_backward(const NormBwdArgs& a, dion_dtype dt, cudaStream_t stream);
 
 // One operand of the product: rows of 8-bit values, their format and scales.

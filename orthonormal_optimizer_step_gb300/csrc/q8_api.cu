@@ -24,6 +24,14 @@ bool q8_scale_ok(const void* p, int cols, long long ld)
 // Tiles of 128 x 128 in one launch.
 bool tiles_fit(int rows, int cols) { return cdiv(rows, 128) * cdiv(cols, 128) <= 0x7fffffffll; }
 
+// Whether two matrices' address ranges meet.
+bool overlap(const void* p, long long ldp, const void* q, long long ldq, int rows, int cols, dion_dtype dt)
+{
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    const uintptr_t la = ((uintptr_t)(rows - 1) * ldp + cols) * bytes_of(dt), lb = ((uintptr_t)(rows - 1) * ldq + cols) * bytes_of(dt);
+    return a < b + lb && b < a + la;
+}
+
 dion_status done(cudaError_t e) { return e == cudaSuccess ? DION_OK : DION_ERR_CUDA; }
 
 }  // namespace
@@ -132,8 +140,11 @@ extern "C" dion_status dion_rms_norm_backward(int rows, int cols, dion_dtype dt,
             return DION_ERR_INVALID_ARG;
         if (dh && !matrix_ok(dh, dt, cols, lddh)) return DION_ERR_INVALID_ARG;
         if (cols > 0x7fff0000) return DION_ERR_UNSUPPORTED;
-        if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < norm_backward_workspace(rows, cols))
+        const bool alone = norm_backward_small(rows, cols) && !overlap(dx, lddx, dy, lddy, rows, cols, dt) &&
+                           !overlap(dx, lddx, h, ldh, rows, cols, dt);
+        if (workspace ? (uintptr_t)workspace % 256 || workspace_bytes < norm_backward_workspace(rows, cols) : !alone)
             return DION_ERR_WORKSPACE;
+        if (alone) workspace = nullptr;
     }
     NormBwdArgs a{};
     a.rows = rows; a.cols = cols;

@@ -363,9 +363,11 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
         d2, lddh = _matrix(dh, "dh")
         dptr = d2.data_ptr()
         _same_device(dev, dh=dh)
+    small = False
     if dx is None:
         dx = empty(shape, dtype=ydt, device=device)
         xptr, ldx = dx.data_ptr(), cols
+        small = cols <= 8192 and rows <= 2048 and rows * cols <= 1 << 21      # no workspace is used then
     else:
         x2, ldx = _matrix(dx, "dx")
         xptr = x2.data_ptr()
@@ -376,18 +378,20 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
         raise TypeError("rstd and dweight must be float32")
     _vector(rstd, rows, "rstd")
     _vector(dweight, cols, "dweight")
-    if workspace is None:
+    wsptr, nbytes = None, 0
+    if workspace is not None:
+        _same_device(dev, workspace=workspace)
+        wsptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif not small:
         nbytes = max(256, dion_rms_norm_backward_workspace_size(rows, cols))
         workspace = empty((nbytes,), dtype=torch.uint8, device=device)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    if not (dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device()
-            == workspace.get_device()):
-        _same_device(dev, h=h, rstd=rstd, weight=weight, dx=dx, dweight=dweight, workspace=workspace)
+        wsptr = workspace.data_ptr()
+    if not dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device():
+        _same_device(dev, h=h, rstd=rstd, weight=weight, dx=dx, dweight=dweight)
     if cols:
         code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh, rstd.data_ptr(),
                                                 weight.data_ptr(), wdt, dptr, lddh, xptr, ldx, dweight.data_ptr(),
-                                                workspace.data_ptr(), nbytes, _raw_stream(dev))
+                                                wsptr, nbytes, _raw_stream(dev))
         if code:
             _od._check(code, "dion_rms_norm_backward")
     return dx, dweight

@@ -434,6 +434,26 @@ def test_backward_streamed(rows, cols, residual):
     check_backward(dy, h, rstd, w, dh, got, BF16)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 8192), (2048, 1000), (2048, 1024), (255, 8190), (77, 40), (2049, 100), (300, 8193)])
+def test_backward_in_one_launch(rows, cols):
+    """Small problems take one kernel and no workspace; in place, or just too
+    large, the others; all agree."""
+    h, w, dy, dh = randn(rows, cols), 1 + 0.1 * randn(cols, seed=1), randn(rows, cols, seed=2), randn(rows, cols, seed=3)
+    rstd = torch.rand(rows, device="cuda") + 0.5
+    small = rows <= 2048 and cols <= 8192
+    with od.profile() as p:
+        got = od.dion_rms_norm_backward(dy, h, rstd, w, dh=dh)
+    torch.cuda.synchronize()
+    assert (set(p.read()) == {"rms_norm_backward_small"}) == small
+    check_backward(dy, h, rstd, w, dh, got, F32)
+    own = dy.clone()
+    with od.profile() as p:
+        inplace = od.dion_rms_norm_backward(own, h, rstd, w, dh=dh, dx=own)
+    torch.cuda.synchronize()
+    assert "rms_norm_backward_small" not in p.read()
+    check_backward(dy, h, rstd, w, dh, inplace, F32)
+
+
 def test_backward_against_differences():
     """L = sum(dy * norm(h) w) + sum(dh * h): derivative along random directions, by
     central differences in 64 bits (error of order step^2) against the kernel's."""
