@@ -222,7 +222,14 @@ __device__ __noinline__ void drain_after_abort()
 }
 
 constexpr int kOutBytes = 2048;  // a block of C on its way out: 32 rows of 64 bytes
-constexpr int kSfSlots = 4;      // scale groups (four blocks of the contraction) in flight
+// Scales move in groups of four blocks of the contraction; a slot is what one
+// barrier hands over, two groups: in a pair the hand-over is an arrival with
+// release at cluster scope, about 1600 cycles beside the operands' traffic (a
+// block of a 256 x 224 tile takes 490), and one for every group set the pace
+// (8192 x 14336 x 4096 293 us, now 274).
+constexpr int kSfSlots = 2;
+constexpr int kSfGroups = 2;     // of a slot
+constexpr int kSplitSlots = 4;   // of one group each, in the split kernel (one CTA)
 constexpr int kSfBatch = 4;      // groups whose words are loaded together
 static_assert(kSfBatch == 4, "scale_words4 loads four");
 
@@ -233,7 +240,7 @@ struct Cfg {
     static constexpr uint32_t P_BYTES = BM * 128, Q_BYTES = QROWS * 128, STAGE = P_BYTES + Q_BYTES;
     static constexpr int STAGES = QROWS >= 96 ? 6 : 8;
     static constexpr int SFQ = (BN + 127) / 128;       // 128-row scale groups of Q
-    static constexpr uint32_t SF_BYTES = 512 * (1 + SFQ);
+    static constexpr uint32_t SFG_BYTES = 512 * (1 + SFQ), SF_BYTES = kSfGroups * SFG_BYTES;   // a group's, a slot's
     static constexpr uint32_t ACC = BN < 32 ? 32 : BN; // accumulator columns
     // 512 columns hold two accumulators and the scales up to 224 columns wide.
     // The 256-wide accumulator is single: its eight epilogue warps take it
@@ -242,8 +249,8 @@ struct Cfg {
     static constexpr int EW = CG == 2 ? 8 : 4;         // epilogue warps
     static constexpr int EGROUPS = EW / 4;             // warps on each lane quarter, and the columns of one
     static constexpr int ECOLS = EGROUPS == 1 ? BN : (BN / 2 + 31) / 32 * 32;
-    static constexpr uint32_t SF_COL = BUFS * ACC;     // scales: 4 (P) + 4 SFQ (Q) columns a slot
-    static constexpr uint32_t SF_COLS = 4 + 4 * SFQ;
+    static constexpr uint32_t SF_COL = BUFS * ACC;     // scales: 4 (P) + 4 SFQ (Q) columns a group
+    static constexpr uint32_t SFG_COLS = 4 + 4 * SFQ, SF_COLS = kSfGroups * SFG_COLS;
     static constexpr uint32_t TMEM = BN <= 32 ? 128 : BN <= 64 ? 256 : 512;
     static constexpr int OUTS = BN < 32 ? 0 : BN > 224 ? 1 : 2;   // such blocks of an epilogue warp
     static constexpr uint32_t OUT = EW * OUTS * kOutBytes;
@@ -320,7 +327,8 @@ __device__ __forceinline__ void store_cols(const GemmParams& p, int row0, int co
 // bounds the main loop (a block of a 256 x 224 tile moves 30 KB in by TMA and
 // about 30 KB out to the MMAs, at 128 bytes a cycle 470 of its 490 cycles), so
 // the epilogue's use of it counts: 8192 x 14336 x 4096 takes 254 us without
-// stores, 293 as here, 298 through shared memory and back through registers.
+// stores, 293 with them, 298 through shared memory and back through registers
+// (before the scales' hand-over was halved, see kSfGroups).
 template <bool F32, int OUTS>
 __device__ __forceinline__ void store_rows(const GemmParams& p, const CUtensorMap* tmC, int row0, int col0,
                                            const uint32_t (&v)[32], uint8_t* buf, int& turn, int lane)
@@ -437,11 +445,14 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
                 tc::tc_fence_after();
                 const uint32_t d = tmem + buf * C::ACC;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    const uint32_t sfp = tmem + C::SF_COL + slot * C::SF_COLS, sfq = sfp + 4;
+                    const int grp = kb / 4 % kSfGroups;
+                    const uint32_t sfp = tmem + C::SF_COL + slot * C::SF_COLS + grp * C::SFG_COLS, sfq = sfp + 4;
                     if ((kb & 3) == 0) {
-                        if (!(ok = wait_peer<CG>(&sf_full[slot], sph, abrt, p.status))) break;
-                        tc::tc_fence_after();
-                        const uint32_t src = tc::smem_u32(sf + slot * C::SF_BYTES);
+                        if (grp == 0) {
+                            if (!(ok = wait_peer<CG>(&sf_full[slot], sph, abrt, p.status))) break;
+                            tc::tc_fence_after();
+                        }
+                        const uint32_t src = tc::smem_u32(sf + slot * C::SF_BYTES + grp * C::SFG_BYTES);
                         tmem_cp_scales<CG>(sfp, src);
 #pragma unroll
                         for (int i = 0; i < C::SFQ; ++i) tmem_cp_scales<CG>(sfq + 4 * i, src + 512 * (1 + i));
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
                                    sfp, sfq, (kb | j) != 0);
                     commit<CG>(&empty[stage]);
                     if (++stage == C::STAGES) { stage = 0; ph ^= 1; }
-                    if ((kb & 3) == 3 || kb == kblocks - 1) {
+                    if (kb % (4 * kSfGroups) == 4 * kSfGroups - 1 || kb == kblocks - 1) {
                         commit<CG>(&sf_empty[slot]);
                         if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
                     }
@@ -478,7 +489,7 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
             // group's MMAs) set the pace
             const int groups = (kblocks + 3) / 4;
             for (int g0 = 0; g0 < groups && ok; g0 += kSfBatch) {
-                uint4 w[kSfBatch][1 + C::SFQ];
+                uint4 w[kSfBatch][1 + C::SFQ] = {};
                 if (p.sf16 && g0 + 4 <= groups) {
                     scale_words4(p.sp, p.ldsp, p.sp_shift, p.sp_rows, (tp * CG + rank) * C::BM, C::BM, g0, lane, w[0][0],
                                  w[1][0], w[2][0], w[3][0]);
@@ -498,13 +509,16 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < kSfBatch; ++j) {
+                for (int j = 0; j < kSfBatch; j += kSfGroups) {
                     if (g0 + j >= groups) break;
                     ok = tc::mbar_wait(&sf_empty[slot], sph ^ 1, abrt, p.status);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    uint4* dst = reinterpret_cast<uint4*>(sf + slot * C::SF_BYTES);
 #pragma unroll
-                    for (int i = 0; i < 1 + C::SFQ; ++i) dst[32 * i + lane] = w[j][i];
+                    for (int e = 0; e < kSfGroups; ++e) {        // (words past the last group are not read)
+                        uint4* dst = reinterpret_cast<uint4*>(sf + slot * C::SF_BYTES + e * C::SFG_BYTES);
+#pragma unroll
+                        for (int i = 0; i < 1 + C::SFQ; ++i) dst[32 * i + lane] = w[j + e][i];
+                    }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive_first<CG>(&sf_full[slot]);
@@ -587,8 +601,8 @@ struct SplitCfg {
     static constexpr uint32_t TMEM = BN <= 32 ? 64 : BN == 64 ? 128 : BN == 128 ? 256 : 512;
     // Sums [column][128 rows] float, in the place of the stages, which the MMAs have all read by then.
     static constexpr uint32_t SUMS = BN * 512;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kSfSlots * SF_BYTES + 512;
-    static_assert(SF_COL + kSfSlots * SF_COLS <= TMEM, "tensor memory columns");
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kSplitSlots * SF_BYTES + 512;
+    static_assert(SF_COL + kSplitSlots * SF_COLS <= TMEM, "tensor memory columns");
     static_assert(SUMS <= STAGES * STAGE, "sums in the stages' place");
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
@@ -603,11 +617,11 @@ __global__ void __launch_bounds__(256, 1)
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sf = smem + C::STAGES * C::STAGE;
     float* sums = (float*)smem;
-    uint64_t* full = (uint64_t*)(sf + kSfSlots * C::SF_BYTES);
+    uint64_t* full = (uint64_t*)(sf + kSplitSlots * C::SF_BYTES);
     uint64_t* empty = full + C::STAGES;
     uint64_t* sf_full = empty + C::STAGES;
-    uint64_t* sf_empty = sf_full + kSfSlots;
-    uint64_t* acc_full = sf_empty + kSfSlots;
+    uint64_t* sf_empty = sf_full + kSplitSlots;
+    uint64_t* acc_full = sf_empty + kSplitSlots;
     uint32_t* tmem_slot = (uint32_t*)(acc_full + 1);
     volatile int* abrt = (volatile int*)(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -618,7 +632,7 @@ __global__ void __launch_bounds__(256, 1)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < kSfSlots; ++s) {
+        for (int s = 0; s < kSplitSlots; ++s) {
             tc::mbar_init(&sf_full[s], 1);
             tc::mbar_init(&sf_empty[s], 1);
         }
@@ -678,7 +692,7 @@ __global__ void __launch_bounds__(256, 1)
                 if (++stage == C::STAGES) { stage = 0; ph ^= 1; }
                 if ((kb & 3) == 3) {
                     commit<1>(&sf_empty[slot]);
-                    if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
+                    if (++slot == kSplitSlots) { slot = 0; sph ^= 1; }
                 }
             }
             if (ok && kb1 > kb0) commit<1>(acc_full);
@@ -710,7 +724,7 @@ __global__ void __launch_bounds__(256, 1)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sf_full[slot]);
-                if (++slot == kSfSlots) { slot = 0; sph ^= 1; }
+                if (++slot == kSplitSlots) { slot = 0; sph ^= 1; }
             }
         }
     }
@@ -888,19 +902,18 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     // take: start + waves * (time a block * blocks + a tile's end), in us on 152
     // SMs.  A pair reads half as much a product but starts and ends later.
     // Measured, us:                  128     224     256
-    //    512 x  4096 x  4096        11.8            17.1
-    //   8192 x  2304 x   768        17.1    19.4    19.2
-    //   4096 x  4096 x  4096        52.6    45.0    47.9
-    //   8192 x  1024 x  4096        35.4    36.4    27.2    (the last wave of 224 is nearly empty)
-    //   8192 x 14336 x  4096         368     293     328
-    //   4096 x 14336 x  8192         362     318     304
+    //    512 x  4096 x  4096        10.4            17.1
+    //   8192 x  2304 x   768        16.0    17.5    17.8
+    //   4096 x  4096 x  4096        51.0    41.0    46.6
+    //   8192 x  1024 x  4096        36.0    35.8    28.8    (the last wave of 224 is nearly empty)
+    //   8192 x 14336 x  4096         372     274     321
     // Without alignment for TMA stores a 224-wide tile's stores take longer
-    // than its share of the main loop is worth (4096 x 4097 x 4096: 58.1, 256: 53.6).
+    // than its share of the main loop is worth (4096 x 4097 x 4096: 57.5, 256: 50.7).
     const long long t1 = cdiv(m, 128) * cdiv(n, 128);
     const int q = aligned ? n : m, other = aligned ? m : n;      // rows of the operand on the N side
-    const float one = 3.5f + (float)cdiv(t1, 152) * (0.215f * kb + 0.4f);
-    const float w256 = 5.f + (float)cdiv(cdiv(q, 256) * cdiv(other, 256), 76) * (0.335f * kb + 1.8f);
-    const float w224 = 5.f + (float)cdiv(cdiv(q, 224) * cdiv(other, 256), 76) * (0.30f * kb + 0.9f);
+    const float one = 3.5f + (float)cdiv(t1, 152) * (0.21f * kb + 0.35f);
+    const float w256 = 5.f + (float)cdiv(cdiv(q, 256) * cdiv(other, 256), 76) * (0.30f * kb + 1.2f);
+    const float w224 = 5.f + (float)cdiv(cdiv(q, 224) * cdiv(other, 256), 76) * (0.265f * kb + 0.8f);
     if (aligned && w224 < one && w224 < w256) return gemm_go<2, 224, F32, true>(a, st);
     if (w256 < one) return aligned ? gemm_go<2, 256, F32, true>(a, st) : gemm_go<2, 256, F32, false>(a, st);
     const int s = shares(t1, kb);
