@@ -583,12 +583,12 @@ __global__ void __launch_bounds__(128 + 32 * Cfg<CG, BN>::EW, 1)
 }
 
 // -------------------------------------------- few tiles: the contraction split
-// One tile a cluster of `splits` CTAs, B on the M side.  Each contracts its share of the blocks and leaves its sums in its
-// shared memory; then every CTA finishes BN / splits columns of its rows: it
-// reads them from all CTAs that hold the same rows (16 bytes a lane through
-// distributed shared memory; 4-byte remote stores of the sums took several
-// times as long) and adds them in the order of the shares, so the bits are the
-// same every time.
+// One tile a cluster of `splits` CTAs, B on the M side.  Each contracts its
+// share of the blocks and leaves its sums in its shared memory; then every CTA
+// finishes BN / splits of the tile's columns: it reads them from all CTAs (16
+// bytes a lane through distributed shared memory; 4-byte remote stores of the
+// sums took several times as long) and adds them in the order of the shares,
+// so the bits are the same every time.
 template <int BN>
 struct SplitCfg {
     static constexpr int BM = 128;
