@@ -6,6 +6,7 @@ and `scale` [rows, ceil(cols / 128)] in torch.float8_e8m0fnu, one power of two
 for each 1 x 128 block (or [ceil(rows / 128), ceil(cols / 128)], one for each
 128 x 128 block), rows starting on 4-byte boundaries.  `new_q8` allocates one
 that meets this for any size; tensors of a program's own may be passed as well.
+All tensors of a call are on the current device.
 
     w8, w8t = dion_q8_quantize(W, form="both", square=True)      # weights, both orders
     x8, h, rstd = dion_rms_norm_q8(x, weight, residual=r)        # layer input
@@ -33,6 +34,7 @@ _FORMATS = {_E4M3: 0, _E5M2: 1}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _FORMS = {"rows": (True, False), "cols": (False, True), "both": (True, True)}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _status = {}
 
 
@@ -62,9 +64,13 @@ def _format(dtype):
 
 
 def _cuda(t, what):
+    """The device of a CUDA tensor; it has to be the current one, where the kernels run (the default stream's handle is
+    the same on every device, so a launch elsewhere would read this one's addresses)."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, but the current device is cuda:{_current_device()}")
     return dev
 
 
@@ -336,6 +342,11 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
 
 
 @functools.lru_cache(maxsize=256)
+def _backward_workspace(rows, cols, dev):
+    """dion_rms_norm_backward_workspace_size on the current device, `dev` (the size follows its number of SMs)."""
+    return dion_rms_norm_backward_workspace_size(rows, cols)
+
+
 def dion_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
     out = ctypes.c_size_t(0)
     _od._check(_od.lib().dion_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)),
@@ -383,7 +394,7 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
         _same_device(dev, workspace=workspace)
         wsptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif not small:
-        nbytes = max(256, dion_rms_norm_backward_workspace_size(rows, cols))
+        nbytes = max(256, _backward_workspace(rows, cols, dev))
         workspace = empty((nbytes,), dtype=torch.uint8, device=device)
         wsptr = workspace.data_ptr()
     if not dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device():
