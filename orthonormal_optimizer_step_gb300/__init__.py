@@ -4,7 +4,8 @@ on one NVIDIA GB300.
 A thin ctypes binding over libdion.so (C ABI in include/dion.h and, for the
 8-bit linear layer's operators, include/dion_q8.h).  The binding
 only marshals arguments: every step of the computation runs in libdion's CUDA
-kernels.  PyTorch supplies device memory and the current CUDA stream.  If
+kernels.  PyTorch supplies device memory and the current CUDA stream; a call's
+tensors are on the current device.  If
 libdion.so is missing the import of a function raises; there is no fallback.
 
     from orthonormal_optimizer_step_gb300 import dion_step_batched, muon_ns_batched
@@ -124,6 +125,16 @@ def _stream_ptr(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _on_current_device(*tensors):
+    """Refuses CUDA tensors of a device other than the current one: the kernels run on the current one, and the default
+    stream's handle is the same on every device."""
+    import torch
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
 
@@ -188,6 +199,7 @@ def dion_step_batched(X, G, M, Q, *, mu: float = None, lr: float = None, weight_
     for t in (X, G, M, Q):
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+    _on_current_device(X, G, M, Q, hyper, workspace)
     if workspace is None:
         workspace = new_workspace(dion_workspace_size(batch, m, n, r, dt), X.device)
     if hyper is not None:
@@ -220,6 +232,7 @@ def dion_step_batched_static(X, G, M, Q, *, mu: float, lr: float, weight_decay: 
     for t in (X, G, M, Q):
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+    _on_current_device(X, G, M, Q)
     code = lib().dion_step_batched_static(batch, m, n, r, dt, _ptr(X), _ptr(G), _ptr(M), _ptr(Q), float(mu),
                                           float(lr), float(weight_decay), _stream_ptr(stream))
     _check(code, "dion_step_batched_static")
@@ -236,6 +249,7 @@ def muon_ns_batched(G, *, X=None, M=None, O=None, head_dim: int = 0, steps: int 
     for t in (X, G, M, O):
         if t is not None and not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+    _on_current_device(X, G, M, O, workspace)
     if workspace is None:
         workspace = new_workspace(muon_workspace_size(batch, m, n, head_dim, dt), G.device)
     cf = (ctypes.c_float * 3)(*[float(c) for c in coeff])
