@@ -304,5 +304,21 @@ class profile:
         return out
 
 
-from .q8 import (Q8, dion_q8_matmul, dion_q8_quantize, dion_q8_status, dion_rms_norm_backward,  # noqa: E402
-                 dion_rms_norm_backward_workspace_size, dion_rms_norm_q8, new_q8)
+# The 8-bit operators (q8.py) read torch when they are imported, so that waits
+# for their first use: the package itself imports, and its library loads, without torch.
+_Q8_NAMES = ("Q8", "dion_q8_matmul", "dion_q8_quantize", "dion_q8_status", "dion_rms_norm_backward",
+             "dion_rms_norm_backward_workspace_size", "dion_rms_norm_q8", "new_q8")
+
+
+def __getattr__(name):
+    if name != "q8" and name not in _Q8_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    q8 = importlib.import_module(".q8", __name__)
+    for n in _Q8_NAMES:
+        globals()[n] = getattr(q8, n)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_Q8_NAMES, "q8"})

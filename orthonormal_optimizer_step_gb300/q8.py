@@ -33,8 +33,9 @@ _F32 = torch.float32
 _FORMATS = {_E4M3: 0, _E5M2: 1}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _FORMS = {"rows": (True, False), "cols": (False, True), "both": (True, True)}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (absent from builds of torch without CUDA, which have no tensor to call them for)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _status = {}
 
 
