@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 from typing import NamedTuple
 
 import torch
@@ -37,6 +38,7 @@ _FORMS = {"rows": (True, False), "cols": (False, True), "both": (True, True)}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 _status = {}
+_status_lock = threading.Lock()
 
 
 class Q8(NamedTuple):
@@ -177,10 +179,15 @@ def _out_q8(q, rows, cols, dtype, square, batch, dev):
 
 # ---- status word of the products
 def _status_word(dev):
-    t = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
-    torch.cuda.current_stream(dev).synchronize()   # once: later calls may run on any stream
-    _status[dev] = (t.data_ptr(), t)
-    return _status[dev]
+    with _status_lock:                             # one word a device, whichever thread comes first
+        if dev not in _status:
+            # what a capture allocates and clears belongs to its graph, and it cannot be waited for
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the first dion_q8_matmul on a device sets up its status word; make it before any stream capture")
+            t = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
+            torch.cuda.current_stream(dev).synchronize()   # once: later calls may run on any stream
+            _status[dev] = (t.data_ptr(), t)
+        return _status[dev]
 
 
 def dion_q8_status(device=None) -> int:
@@ -258,7 +265,10 @@ def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, we
 
 def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
     """a b^T [m, n] of quantized matrices a [m, k] and b [n, k], in float32 sums
-    rounded once to out_dtype (bfloat16 or float32; that of `out` if given)."""
+    rounded once to out_dtype (bfloat16 or float32; that of `out` if given).
+
+    The first call on a device sets up its status word (dion_q8_status); make it
+    before any stream capture."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return dion_q8_matmul(a, b, out=out, out_dtype=out_dtype)

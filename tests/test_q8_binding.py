@@ -1,4 +1,8 @@
 """The binding of the 8-bit operators: what it refuses or sets up before a launch."""
+import threading
+import time
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -45,3 +49,63 @@ def test_every_operator_checks_the_device(monkeypatch):
                  lambda: od.dion_rms_norm_backward(x, x, rstd, w)):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+# ---------------------------------------------------------------- status word
+def fake_torch(made, capturing=False):
+    """As much of torch as a status word takes; allocating it takes a while."""
+    def zeros(*_, device, **__):
+        time.sleep(0.05)
+        made.append(SimpleNamespace(data_ptr=lambda n=len(made): 1000 + n))
+        return made[-1]
+
+    cuda = SimpleNamespace(is_current_stream_capturing=lambda: capturing,
+                           current_stream=lambda dev: SimpleNamespace(synchronize=lambda: None))
+    return SimpleNamespace(zeros=zeros, int32=None, device=lambda kind, dev: (kind, dev), cuda=cuda)
+
+
+def test_threads_share_one_status_word(monkeypatch):
+    made, got = [], []
+    monkeypatch.setattr(q8, "torch", fake_torch(made))
+    monkeypatch.setattr(q8, "_status", {})
+    threads = [threading.Thread(target=lambda: got.append(q8._status_word(0)[0])) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(made) == 1 and got == [1000] * 8
+
+
+def test_status_word_is_not_made_in_a_capture(monkeypatch):
+    made = []
+    monkeypatch.setattr(q8, "_status", {})
+    monkeypatch.setattr(q8, "torch", fake_torch(made, capturing=True))
+    with pytest.raises(RuntimeError, match="before any stream capture"):
+        q8._status_word(0)
+    assert not made and not q8._status
+    monkeypatch.setattr(q8, "torch", fake_torch(made))
+    word = q8._status_word(0)
+    monkeypatch.setattr(q8, "torch", fake_torch(made, capturing=True))
+    assert q8._status_word(0) is word and len(made) == 1
+
+
+@pytest.mark.gpu
+def test_first_product_in_a_capture(monkeypatch):
+    a, _ = od.dion_q8_quantize(torch.randn(4, 256, device="cuda"))
+    od.dion_q8_matmul(a, a)
+    words = dict(q8._status)
+    x = torch.zeros(8, device="cuda")
+    monkeypatch.setattr(q8, "_status", {})
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x += 1
+        with pytest.raises(RuntimeError, match="before any stream capture"):
+            od.dion_q8_matmul(a, a)
+    g.replay()                                     # the refusal left the capture as it was
+    assert bool((x == 1).all())
+    monkeypatch.setattr(q8, "_status", words)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c = od.dion_q8_matmul(a, a)
+    g.replay()
+    assert torch.equal(c, od.dion_q8_matmul(a, a))
