@@ -8,6 +8,11 @@ for each 1 x 128 block (or [ceil(rows / 128), ceil(cols / 128)], one for each
 that meets this for any size; tensors of a program's own may be passed as well.
 All tensors of a call are on the current device.
 
+The calls are the pieces of a backward pass that a program writes itself: they
+have no derivative of their own.  What a call returns for inputs that require
+gradients (with gradients enabled) raises in a backward pass that reaches it;
+buffers that the program passed to be written carry no record.
+
     w8, w8t = dion_q8_quantize(W, form="both", square=True)      # weights, both orders
     x8, h, rstd = dion_rms_norm_q8(x, weight, residual=r)        # layer input
     y = dion_q8_matmul(x8, w8)                                   # y = x8 w8^T
@@ -113,6 +118,24 @@ def _matrix(t, what):
 def _vector(t, n, what):
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n}")
+
+
+class _NoDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, call, outputs, *inputs):
+        ctx.call = call
+        return outputs
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError(f"{ctx.call} has no derivative: compute it with this module's calls, or detach its inputs")
+
+
+def _underived(call, outputs, inputs):
+    """Records that new tensors came out of `call`, so that a backward pass through them raises
+    instead of stopping there; for inputs of which one requires a gradient."""
+    if torch.is_grad_enabled():
+        _NoDerivative.apply(call, tuple(t for t in outputs if t is not None), *inputs)
 
 
 def new_q8(rows, cols, *, dtype=_E4M3, square=False, batch=None, device="cuda"):
@@ -260,6 +283,10 @@ def dion_q8_quantize(x, *, form="rows", square=False, dtype=_E4M3, rstd=None, we
                                           wdt, square, fmt, *qa, *qta, _raw_stream(dev))
         if code:
             _od._check(code, "dion_q8_quantize")
+    if x.requires_grad or rstd is not None and (rstd.requires_grad or weight.requires_grad):
+        given = (None, None) if out is None else out
+        _underived("dion_q8_quantize", [t for new, o in ((q, given[0]), (qt, given[1])) if o is None and new
+                                        for t in new], (x, rstd, weight))
     return q, qt
 
 
@@ -278,7 +305,7 @@ def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
     bd, bsc = b
     if k != k2 or ad.dim() != 2 or bd.dim() != 2:
         raise ValueError(f"expected [m, k] and [n, k], got {tuple(ad.shape)} and {tuple(bd.shape)}")
-    dev = _cuda(ad, "a")
+    dev, given = _cuda(ad, "a"), out
     if out is None:
         ct, ldc = _type(out_dtype, "out_dtype"), n
         out = empty((m, n), dtype=out_dtype, device=ad.device)
@@ -292,6 +319,8 @@ def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
                                     out.data_ptr(), ldc, ct, (_status.get(dev) or _status_word(dev))[0], _raw_stream(dev))
     if code:
         _od._check(code, "dion_q8_matmul")
+    if given is None and (ad.requires_grad or bd.requires_grad or asc.requires_grad or bsc.requires_grad):
+        _underived("dion_q8_matmul", (out,), (ad, asc, bd, bsc))
     return out
 
 
@@ -305,6 +334,7 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
     if stream is not None:
         with torch.cuda.stream(stream):
             return dion_rms_norm_q8(x, weight, residual=residual, eps=eps, dtype=dtype, h=h, out=out, rstd=rstd)
+    given = h, out, rstd
     xdt, device = x.dtype, x.device
     dt, wdt, dev = _type(xdt, "x"), _type(weight.dtype, "weight"), _cuda(x, "x")
     x2, ldx = _matrix(x, "x")
@@ -349,6 +379,10 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
                                           rstd.data_ptr(), _raw_stream(dev))
         if code:
             _od._check(code, "dion_rms_norm_q8")
+    if x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad:
+        _underived("dion_rms_norm_q8", (h if residual is not None and given[0] is None else None,
+                                        *((None, None) if given[1] is not None else out),
+                                        rstd if given[2] is None else None), (x, weight, residual))
     return out, (x if residual is None else h), rstd
 
 
@@ -373,6 +407,7 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     if stream is not None:
         with torch.cuda.stream(stream):
             return dion_rms_norm_backward(dy, h, rstd, weight, dh=dh, dx=dx, dweight=dweight, workspace=workspace)
+    given = dx, dweight
     ydt, shape, device = dy.dtype, dy.shape, dy.device
     dt, wdt, dev = _type(ydt, "dy"), _type(weight.dtype, "weight"), _cuda(dy, "dy")
     for t in (h, dx, dh):
@@ -416,4 +451,7 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
                                                 wsptr, nbytes, _raw_stream(dev))
         if code:
             _od._check(code, "dion_rms_norm_backward")
+    if dy.requires_grad or h.requires_grad or rstd.requires_grad or weight.requires_grad or dh is not None and dh.requires_grad:
+        _underived("dion_rms_norm_backward", (None if given[0] is not None else dx, None if given[1] is not None else dweight),
+                   (dy, h, rstd, weight, dh))
     return dx, dweight

@@ -109,3 +109,54 @@ def test_first_product_in_a_capture(monkeypatch):
         c = od.dion_q8_matmul(a, a)
     g.replay()
     assert torch.equal(c, od.dion_q8_matmul(a, a))
+
+
+# ------------------------------------------------------------------ gradients
+def test_outputs_without_a_derivative():
+    a, q, r = torch.ones(4, requires_grad=True), torch.ones(4, 8)[:, :4], torch.ones(4)
+    with torch.no_grad():
+        q8._underived("call", (q, None, r), (a, None))
+        assert not q.requires_grad
+    q8._underived("call", (q, None, r), (a, None))
+    assert q.requires_grad and r.requires_grad
+    with pytest.raises(NotImplementedError, match="call has no derivative"):
+        (q.sum() + a.sum()).backward()
+
+
+@pytest.mark.gpu
+def test_no_operator_drops_a_gradient():
+    def leaf(*shape):
+        return torch.randn(*shape, device="cuda", requires_grad=True)
+
+    x, r, w, rstd = torch.randn(4, 256, device="cuda"), torch.randn(4, 256, device="cuda"), torch.ones(256, device="cuda"), torch.ones(4, device="cuda")
+    x8, _ = od.dion_q8_quantize(x)
+    want = {"q": x8.data.view(torch.uint8), "c": od.dion_q8_matmul(x8, x8), "y": od.dion_rms_norm_q8(x, w, residual=r),
+            "g": od.dion_rms_norm_backward(x, r, rstd, w)}
+
+    def with_grad(t):
+        return t.clone().requires_grad_()
+
+    got_q = od.dion_q8_quantize(with_grad(x), form="both")
+    a8 = od.Q8(with_grad(x8.data), x8.scale)
+    cases = [[got_q[0].data, got_q[1].data], [od.dion_q8_matmul(a8, x8)], [od.dion_q8_matmul(x8, a8)]]
+    for i in range(3):
+        args = [with_grad(t) if j == i else t for j, t in enumerate((x, w, r))]
+        y, h, s = od.dion_rms_norm_q8(args[0], args[1], residual=args[2])
+        cases.append([y.data, h, s])
+    for i in range(5):
+        args = [with_grad(t) if j == i else t for j, t in enumerate((x, r, rstd, w, r))]
+        cases.append(list(od.dion_rms_norm_backward(*args[:4], dh=args[4])))
+    for outputs in cases:
+        for t in outputs:
+            with pytest.raises(NotImplementedError, match="no derivative"):
+                t.float().sum().backward()
+    assert torch.equal(got_q[0].data.detach().view(torch.uint8), want["q"])          # the values are what they were
+    assert torch.equal(cases[1][0], want["c"]) and torch.equal(cases[3][1], want["y"][1])
+    with torch.no_grad():
+        assert not od.dion_q8_matmul(a8, x8).requires_grad and not od.dion_q8_quantize(leaf(4, 256))[0].data.requires_grad
+    own = torch.empty(4, 4, dtype=torch.bfloat16, device="cuda")
+    assert od.dion_q8_matmul(a8, x8, out=own) is own and not own.requires_grad       # a buffer of the program's
+    xg = with_grad(x)
+    y, h, _ = od.dion_rms_norm_q8(xg, w)
+    assert h is xg                                                                   # x itself: nothing is lost on it
+    assert not want["c"].requires_grad
