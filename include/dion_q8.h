@@ -110,7 +110,8 @@ dion_status dion_rms_norm_backward_workspace_size(int rows, int cols, size_t* by
  * [rows, cols] of type dt; dx may be dy or dh itself.  dw [cols] float32, its
  * sum over the rows taken in a fixed order (the same bits every time).
  * Up to 2048 rows, 8192 columns and 2^21 elements, with dx apart from dy and
- * from h, no workspace is used, and it may be NULL.
+ * from h, no workspace is used, and it may be NULL.  Apart: the address ranges
+ * do not meet, or the pitches are the same and no element is shared.
  */
 dion_status dion_rms_norm_backward(int rows, int cols, dion_dtype dt, const void* dy, long long lddy, const void* h,
                                    long long ldh, const float* rstd, const void* weight, dion_dtype wdt,

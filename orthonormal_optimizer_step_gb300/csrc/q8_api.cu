@@ -24,12 +24,18 @@ bool q8_scale_ok(const void* p, int cols, long long ld)
 // Tiles of 128 x 128 in one launch.
 bool tiles_fit(int rows, int cols) { return cdiv(rows, 128) * cdiv(cols, 128) <= 0x7fffffffll; }
 
-// Whether two matrices' address ranges meet.
+// Whether two rows x cols matrices share an element's byte.  With one pitch
+// (columns of a wider matrix, say) they may lie between each other's rows: the
+// rows of one start at the same distance behind those of the other everywhere.
+// Else their address ranges decide.
 bool overlap(const void* p, long long ldp, const void* q, long long ldq, int rows, int cols, dion_dtype dt)
 {
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    const uintptr_t la = ((uintptr_t)(rows - 1) * ldp + cols) * bytes_of(dt), lb = ((uintptr_t)(rows - 1) * ldq + cols) * bytes_of(dt);
-    return a < b + lb && b < a + la;
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q, row = (uintptr_t)cols * bytes_of(dt);
+    const uintptr_t pitch_p = (uintptr_t)ldp * bytes_of(dt), pitch_q = (uintptr_t)ldq * bytes_of(dt);
+    if (a >= b + (rows - 1) * pitch_q + row || b >= a + (rows - 1) * pitch_p + row) return false;
+    if (ldp != ldq) return true;
+    const uintptr_t behind = (a > b ? a - b : b - a) % pitch_p;
+    return behind < row || pitch_p - behind < row;
 }
 
 dion_status done(cudaError_t e) { return e == cudaSuccess ? DION_OK : DION_ERR_CUDA; }

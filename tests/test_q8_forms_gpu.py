@@ -1,11 +1,13 @@
 """Forms of the norm, its gradient and the quantization that need particular
 sizes, types or values to be reached, against 64 bits with the tolerances of
 test_q8_gpu, and the norm's stored sum bit for bit."""
+import ctypes
+
 import pytest
 import torch
 
 import orthonormal_optimizer_step_gb300 as od
-from test_q8_gpu import BF16, E4M3, E5M2, F32, NORM_SIZES, STREAM_SIZES, randn
+from test_q8_gpu import BF16, E4M3, E5M2, F32, NORM_SIZES, STREAM_SIZES, check_backward, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +42,40 @@ def test_norm_stores_the_rounded_sum(rows, cols, special, dtype):
     _, h, _ = od.dion_rms_norm_q8(x, w, residual=r)
     torch.testing.assert_close(h, want, rtol=0, atol=0, equal_nan=True)
     assert torch.equal(torch.signbit(h)[~torch.isnan(h)], torch.signbit(want)[~torch.isnan(want)])
+
+
+# ----------------------------------------------------- the gradient's workspace
+def backward_without_workspace(dy, h, rstd, w, dx, dw):
+    """The C entry, float32, no workspace: its status."""
+    rows, cols = dy.shape
+    return od.lib().dion_rms_norm_backward(rows, cols, 0, dy.data_ptr(), dy.stride(0), h.data_ptr(), h.stride(0),
+                                           rstd.data_ptr(), w.data_ptr(), 0, None, 0, dx.data_ptr(), dx.stride(0),
+                                           dw.data_ptr(), None, ctypes.c_size_t(0), torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (2, 0, 1), (1, 2, 0)])
+@pytest.mark.parametrize("rows,cols,gap", [(1, 64, 0), (40, 96, 0), (40, 99, 1), (300, 256, 4)])
+def test_backward_between_the_rows_of_its_inputs(rows, cols, gap, order):
+    """dx, dy and h as columns of one matrix: apart, so no workspace is needed."""
+    base = randn(rows, 3 * (cols + gap))
+    dy, h, dx = (base[:, o * (cols + gap):o * (cols + gap) + cols] for o in order)
+    rstd, w, dw = torch.rand(rows, device="cuda") + 0.5, 1 + 0.1 * randn(cols, seed=1), torch.empty(cols, device="cuda")
+    before = base.clone()
+    assert backward_without_workspace(dy, h, rstd, w, dx, dw) == od.DION_OK
+    check_backward(dy, h, rstd, w, None, (dx, dw), F32)
+    dx.copy_(before[:, order[2] * (cols + gap):order[2] * (cols + gap) + cols])
+    assert torch.equal(base, before)
+
+
+def test_backward_over_its_inputs_needs_a_workspace():
+    rows, cols = 40, 96
+    base, rstd, w, dw = randn(rows + 1, 300), torch.rand(rows, device="cuda"), randn(cols), torch.empty(cols, device="cuda")
+    dy, h = base[:rows, :cols], base[:rows, 200:296]
+    wide = randn(rows, 400)
+    for dx in (dy, h, base[1:, :cols], base[:rows, 95:191], base[:rows, 105:201], base[1:, 200:296], base[:rows, 201:297]):
+        assert backward_without_workspace(dy, h, rstd, w, dx, dw) == od.DION_ERR_WORKSPACE
+        assert backward_without_workspace(h, dy, rstd, w, dx, dw) == od.DION_ERR_WORKSPACE
+    # another pitch over the same addresses
+    other = base.view(-1)[:rows * 301 - 5].as_strided((rows - 1, cols), (301, 1))
+    assert backward_without_workspace(dy[:-1], h[:-1], rstd[:-1], w, other, dw) == od.DION_ERR_WORKSPACE
+    assert backward_without_workspace(dy, h, rstd, w, wide[:, 8:104], dw) == od.DION_OK
