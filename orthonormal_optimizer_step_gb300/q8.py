@@ -424,7 +424,8 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     if dx is None:
         dx = empty(shape, dtype=ydt, device=device)
         xptr, ldx = dx.data_ptr(), cols
-        small = cols <= 8192 and rows <= 2048 and rows * cols <= 1 << 21      # no workspace is used then
+        # the library uses no workspace then; should its limit be lower, its answer says so
+        small = cols <= 8192 and rows <= 2048 and rows * cols <= 1 << 21
     else:
         x2, ldx = _matrix(dx, "dx")
         xptr = x2.data_ptr()
@@ -446,10 +447,14 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     if not dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device():
         _same_device(dev, h=h, rstd=rstd, weight=weight, dx=dx, dweight=dweight)
     if cols:
-        code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh, rstd.data_ptr(),
-                                                weight.data_ptr(), wdt, dptr, lddh, xptr, ldx, dweight.data_ptr(),
-                                                wsptr, nbytes, _raw_stream(dev))
+        args = (rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh, rstd.data_ptr(), weight.data_ptr(), wdt, dptr, lddh,
+                xptr, ldx, dweight.data_ptr())
+        code = _od.lib().dion_rms_norm_backward(*args, wsptr, nbytes, _raw_stream(dev))
         if code:
+            if code == _od.DION_ERR_WORKSPACE and workspace is None:
+                nbytes = max(256, _backward_workspace(rows, cols, dev))
+                workspace = empty((nbytes,), dtype=torch.uint8, device=device)
+                code = _od.lib().dion_rms_norm_backward(*args, workspace.data_ptr(), nbytes, _raw_stream(dev))
             _od._check(code, "dion_rms_norm_backward")
     if dy.requires_grad or h.requires_grad or rstd.requires_grad or weight.requires_grad or dh is not None and dh.requires_grad:
         _underived("dion_rms_norm_backward", (None if given[0] is not None else dx, None if given[1] is not None else dweight),

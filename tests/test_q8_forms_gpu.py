@@ -79,3 +79,30 @@ def test_backward_over_its_inputs_needs_a_workspace():
     other = base.view(-1)[:rows * 301 - 5].as_strided((rows - 1, cols), (301, 1))
     assert backward_without_workspace(dy[:-1], h[:-1], rstd[:-1], w, other, dw) == od.DION_ERR_WORKSPACE
     assert backward_without_workspace(dy, h, rstd, w, wide[:, 8:104], dw) == od.DION_OK
+
+
+class LowerLimit:
+    """The library with a one-launch limit below the binding's."""
+
+    def __init__(self, lib):
+        self.lib, self.refused = lib, 0
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name)
+
+    def dion_rms_norm_backward(self, *args):
+        if args[-3] is None:
+            self.refused += 1
+            return od.DION_ERR_WORKSPACE
+        return self.lib.dion_rms_norm_backward(*args)
+
+
+def test_binding_follows_the_librarys_limit(monkeypatch):
+    dy, h, w, rstd = randn(50, 96), randn(50, 96, seed=1), randn(96, seed=2), torch.rand(50, device="cuda") + 0.5
+    lower = LowerLimit(od.lib())
+    monkeypatch.setattr(od, "lib", lambda: lower)
+    got = od.dion_rms_norm_backward(dy, h, rstd, w)
+    assert lower.refused == 1
+    check_backward(dy, h, rstd, w, None, got, F32)
+    with pytest.raises(od.DionError):              # a workspace of the caller's is not replaced
+        od.dion_rms_norm_backward(dy, h, rstd, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
