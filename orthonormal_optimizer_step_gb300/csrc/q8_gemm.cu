@@ -867,8 +867,13 @@ cudaError_t gemm_split(const Q8MatArgs& a, int splits, cudaStream_t st)
 
 // Shares of the contraction for `tiles` tiles of 128 rows of B: as many as the
 // clusters that run at once allow (an SM group holds whole clusters only: 152
-// SMs take 46 clusters of 3, 36 of 4, 28, 23, 15, 15 of 8), three blocks each
-// at least, and none for short contractions.  Measured, split / whole:
+// SMs take 46 clusters of 3, 36 of 4, 28, 23, 15, 15 of 8), and none for short
+// contractions.  Each takes ceil(kblocks / shares) blocks, the last what is left;
+// a share that would have none is dropped (64x1920x2500, 20 blocks: five shares
+// 6.3 us, six 6.6; 500x500x2048, four 7.4, five 7.9), but eight stay eight: they
+// divide the join evenly, which the eighth does without a block of its own
+// (64x1000x3200, 25 blocks: eight 5.6 us, seven 6.1).
+// Measured, split / whole:
 // 1x4096x14336 13.6 / 24.9 us, 64x4096x4096 9.2 / 11.3, 768x768x16384 20.9 / 30.0;
 // 16x1024x1024 (8 blocks) 5.0 / 4.6; two shares gain nothing over one
 // (1024x1024x8192 17.8 / 17.4).
@@ -877,7 +882,7 @@ int shares(long long tiles, int kblocks)
     constexpr int at_once[9] = {0, 0, 0, 46, 36, 28, 23, 15, 15};
     if (kblocks < 16) return 1;
     for (int s = 8; s > 2; --s)
-        if (3 * s <= kblocks && tiles <= at_once[s]) return s;
+        if (3 * s <= kblocks && tiles <= at_once[s]) return s == 8 ? 8 : (int)cdiv(kblocks, cdiv(kblocks, s));
     return 1;
 }
 

@@ -1,7 +1,9 @@
 """Rules that the kernels of the 8-bit operators keep in their source."""
+import ctypes
 import glob
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -50,3 +52,25 @@ def test_waits_for_the_previous_kernel_come_first(name):
         assert waited or use is None or 0 <= first < use.start(), block[:200]
         waited = waited or block.strip() == "wait_previous();"
     assert waited or uses.search(KERNELS[name])
+
+
+def test_shares_of_a_split_contraction_have_blocks(tmp_path):
+    """The rule itself, compiled for the host, with the kernel's division of the blocks: only the last of eight may have none."""
+    text = open(os.path.join(CSRC, "q8_gemm.cu")).read()
+    m = re.search(r"^int shares\(long long tiles, int kblocks\)\n\{.*?^\}", text, re.S | re.M)
+    src = tmp_path / "shares.cc"
+    src.write_text("static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }\n"
+                   'extern "C" ' + m.group(0) + "\n")
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", str(tmp_path / "shares.so"), str(src)], check=True)
+    shares = ctypes.CDLL(str(tmp_path / "shares.so")).shares
+    shares.argtypes = [ctypes.c_longlong, ctypes.c_int]
+    seen = set()
+    for kblocks in range(1, 700):
+        for tiles in (1, 15, 16, 23, 28, 29, 36, 46, 47, 200):
+            s = shares(tiles, kblocks)
+            assert s == 1 or 3 <= s <= 8
+            per = -(-kblocks // s)
+            with_blocks = -(-kblocks // per)
+            assert with_blocks == s or (s == 8 and with_blocks == 7), (kblocks, tiles, s)
+            seen.add(s)
+    assert seen == {1, 3, 4, 5, 6, 7, 8}
