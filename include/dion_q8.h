@@ -91,7 +91,7 @@ dion_status dion_q8_matmul(int m, int n, int k, const void* a, long long lda, di
  * x, residual, h [rows, cols] of type dt; residual and h are NULL together
  * (h = x then), or h may be x or residual itself.  weight [cols] of type wdt.
  * Sums and products are in float32.  rstd [rows] float32 is written for the
- * backward pass (nullable).
+ * backward pass (nullable).  Zero rows or columns write nothing.
  */
 dion_status dion_rms_norm_q8(int rows, int cols, dion_dtype dt, const void* x, long long ldx, const void* residual,
                              long long ldr, const void* weight, dion_dtype wdt, float eps, void* h, long long ldh,

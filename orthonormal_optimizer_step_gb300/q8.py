@@ -373,7 +373,9 @@ def dion_rms_norm_q8(x, weight, *, residual=None, eps=1e-6, dtype=_E4M3, h=None,
         _vector(rstd, rows, "rstd")
     if not dev == weight.get_device() == rstd.get_device():
         _same_device(dev, weight=weight, rstd=rstd)
-    if rows and cols:
+    if not cols:
+        rstd.fill_(float("nan"))                   # the mean of nothing
+    elif rows:
         code = _od.lib().dion_rms_norm_q8(rows, cols, dt, x2.data_ptr(), ldx, rptr, ldr, weight.data_ptr(), wdt, eps,
                                           hptr, ldh, fmt, out[0].data_ptr(), ldq, out[1].data_ptr(), lds,
                                           rstd.data_ptr(), _raw_stream(dev))

@@ -44,6 +44,15 @@ def test_norm_stores_the_rounded_sum(rows, cols, special, dtype):
     assert torch.equal(torch.signbit(h)[~torch.isnan(h)], torch.signbit(want)[~torch.isnan(want)])
 
 
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_rows_without_columns(residual):
+    x, w = torch.empty(7, 0, device="cuda"), torch.empty(0, device="cuda")
+    q, h, rstd = od.dion_rms_norm_q8(x, w, residual=x if residual else None, rstd=torch.full((7,), 5.0, device="cuda"))
+    assert q.data.shape == h.shape == (7, 0) and bool(torch.isnan(rstd).all())      # the mean of nothing
+    dx, dw = od.dion_rms_norm_backward(x, x, rstd, w)
+    assert dx.shape == (7, 0) and dw.shape == (0,)
+
+
 # ----------------------------------------------------- the gradient's workspace
 def backward_without_workspace(dy, h, rstd, w, dx, dw):
     """The C entry, float32, no workspace: its status."""
