@@ -98,13 +98,17 @@ class Clocks:
 # ------------------------------------------------ DRAM traffic from ncu
 
 def csrc_digest():
-    """sha256 over libdion's sources: a DRAM-traffic figure captured with other
-    sources no longer describes the kernel and is not reported."""
+    """sha256 over the sources of the step's kernels (all of libdion's but those
+    of the 8-bit operators, q8*, which no step launches): a DRAM-traffic figure
+    captured with other sources no longer describes the kernel and is not
+    reported."""
     import glob
     import hashlib
     h = hashlib.sha256()
     src = os.path.join(ROOT, "orthonormal_optimizer_step_gb300", "csrc")
     for f in sorted(glob.glob(os.path.join(src, "*"))):
+        if os.path.basename(f).startswith("q8"):
+            continue
         h.update(os.path.basename(f).encode())
         h.update(open(f, "rb").read())
     return h.hexdigest()
