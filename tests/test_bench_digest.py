@@ -21,9 +21,3 @@ def test_digest_follows_the_steps_sources_alone(tmp_path, monkeypatch):
         with open(tmp_path / CSRC / name, "a") as f:
             f.write("// changed\n")
         assert bench.csrc_digest() != before
-
-
-def test_the_committed_capture_describes_the_sources():
-    """The default workload's figure is reported (it is null when the step's sources have changed since)."""
-    value, source = bench.profiled_traffic("llama3-8b-megabatch", "dion_update_tc")
-    assert value and value > 1e10, source
