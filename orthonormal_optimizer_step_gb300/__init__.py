@@ -317,6 +317,7 @@ def __getattr__(name):
     q8 = importlib.import_module(".q8", __name__)
     for n in _Q8_NAMES:
         globals()[n] = getattr(q8, n)
+    globals().pop("__getattr__", None)             # all names are there now, and a module without it is read faster
     return globals()[name]
 
 

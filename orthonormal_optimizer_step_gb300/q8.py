@@ -36,6 +36,7 @@ import orthonormal_optimizer_step_gb300 as _od
 
 _E4M3, _E5M2, _E8M0 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu
 _F32 = torch.float32
+_ERR_WORKSPACE = _od.DION_ERR_WORKSPACE
 _FORMATS = {_E4M3: 0, _E5M2: 1}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _FORMS = {"rows": (True, False), "cols": (False, True), "both": (True, True)}
@@ -319,8 +320,8 @@ def dion_q8_matmul(a, b, *, out=None, out_dtype=torch.bfloat16, stream=None):
                                     out.data_ptr(), ldc, ct, (_status.get(dev) or _status_word(dev))[0], _raw_stream(dev))
     if code:
         _od._check(code, "dion_q8_matmul")
-    if given is None and (ad.requires_grad or bd.requires_grad or asc.requires_grad or bsc.requires_grad):
-        _underived("dion_q8_matmul", (out,), (ad, asc, bd, bsc))
+    if given is None and (ad.requires_grad or bd.requires_grad):
+        _underived("dion_q8_matmul", (out,), (ad, bd))
     return out
 
 
@@ -421,7 +422,8 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     if dh is not None:
         d2, lddh = _matrix(dh, "dh")
         dptr = d2.data_ptr()
-        _same_device(dev, dh=dh)
+        if dh.get_device() != dev:
+            _same_device(dev, dh=dh)
     small = False
     if dx is None:
         dx = empty(shape, dtype=ydt, device=device)
@@ -449,14 +451,12 @@ def dion_rms_norm_backward(dy, h, rstd, weight, *, dh=None, dx=None, dweight=Non
     if not dev == h.get_device() == rstd.get_device() == weight.get_device() == dx.get_device() == dweight.get_device():
         _same_device(dev, h=h, rstd=rstd, weight=weight, dx=dx, dweight=dweight)
     if cols:
-        args = (rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh, rstd.data_ptr(), weight.data_ptr(), wdt, dptr, lddh,
-                xptr, ldx, dweight.data_ptr())
-        code = _od.lib().dion_rms_norm_backward(*args, wsptr, nbytes, _raw_stream(dev))
-        if code:
-            if code == _od.DION_ERR_WORKSPACE and workspace is None:
-                nbytes = max(256, _backward_workspace(rows, cols, dev))
-                workspace = empty((nbytes,), dtype=torch.uint8, device=device)
-                code = _od.lib().dion_rms_norm_backward(*args, workspace.data_ptr(), nbytes, _raw_stream(dev))
+        code = _od.lib().dion_rms_norm_backward(rows, cols, dt, y2.data_ptr(), ldy, h2.data_ptr(), ldh, rstd.data_ptr(),
+                                                weight.data_ptr(), wdt, dptr, lddh, xptr, ldx, dweight.data_ptr(),
+                                                wsptr, nbytes, _raw_stream(dev))
+        if code == _ERR_WORKSPACE and workspace is None:      # (with a dx given, the call takes one)
+            dion_rms_norm_backward(dy, h, rstd, weight, dh=dh, dx=dx, dweight=dweight)
+        elif code:
             _od._check(code, "dion_rms_norm_backward")
     if dy.requires_grad or h.requires_grad or rstd.requires_grad or weight.requires_grad or dh is not None and dh.requires_grad:
         _underived("dion_rms_norm_backward", (None if given[0] is not None else dx, None if given[1] is not None else dweight),
