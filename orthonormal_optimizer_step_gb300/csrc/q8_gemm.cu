@@ -229,7 +229,7 @@ constexpr int kOutBytes = 2048;  // a block of C on its way out: 32 rows of 64 b
 // barrier hands over, two groups: in a pair the hand-over is an arrival with
 // release at cluster scope, about 1600 cycles beside the operands' traffic (a
 // block of a 256 x 224 tile takes 490), and one for every group set the pace
-// (8192 x 14336 x 4096 293 us, now 274).
+// (8192 x 14336 x 4096 in short loops on one GPU: 293 us, with two groups 274).
 constexpr int kSfSlots = 2;
 constexpr int kSfGroups = 2;     // of a slot
 constexpr int kSplitSlots = 4;   // of one group each, in the split kernel (one CTA)
@@ -873,10 +873,12 @@ cudaError_t gemm_split(const Q8MatArgs& a, int splits, cudaStream_t st)
 // 6.3 us, six 6.6; 500x500x2048, four 7.4, five 7.9), but eight stay eight: they
 // divide the join evenly, which the eighth does without a block of its own
 // (64x1000x3200, 25 blocks: eight 5.6 us, seven 6.1).
-// Measured, split / whole:
-// 1x4096x14336 13.6 / 24.9 us, 64x4096x4096 9.2 / 11.3, 768x768x16384 20.9 / 30.0;
-// 16x1024x1024 (8 blocks) 5.0 / 4.6; two shares gain nothing over one
-// (1024x1024x8192 17.8 / 17.4).
+// Measured, split / whole, operands from memory: 1x4096x14336 12.9 / 23.7 us,
+// 64x4096x4096 8.3 / 10.4, 768x768x16384 16.4 / 29.0; 16x1024x1024 (8 blocks)
+// 3.9 / 3.7, 1x4096x1024 4.1 / 4.0, though 12 to 15 blocks would gain
+// (64x1500x1500 6.1 / 6.4).  Two shares lose where the tiles fill half the SMs
+// with long contractions (1024x1024x8192 16.3 / 16.2), though others would gain
+// (900x900x5000 15.4 / 19.5).
 int shares(long long tiles, int kblocks)
 {
     constexpr int at_once[9] = {0, 0, 0, 46, 36, 28, 23, 15, 15};
@@ -901,8 +903,11 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     if (m <= 32) return gemm_narrow<32, F32>(a, st);
     if (m <= 64) return gemm_narrow<64, F32>(a, st);
     // All rows of A in one 256-wide tile, where two 128-wide ones are too many
-    // for shares: 200x4096x14336 22.3 us against 27.3, 192x4096x8192 17.4 against
-    // 18.9; short contractions lose (200x4096x4096 13.9 against 10.2).
+    // for shares (operands from memory): 200x4096x14336 23.1 us against 27.4,
+    // 192x4096x9216 19.1 against 18.9, 192x2500x8192 13.8 against 18.8; short
+    // contractions lose (200x4096x4096 13.9 against 10.2).  With 24 to 28 tiles in
+    // five shares it wins from 112 blocks on only (192x3500x8192 22.0 against
+    // 18.9, 192x3500x14336 26.3 against 28.9).
     if (m > 128 && m <= 256 && kb >= 64 && shares(2 * cdiv(n, 128), kb) == 1) {
         const int s = shares(cdiv(n, 128), kb);
         if (s > 1) return gemm_split<256, F32>(a, s, st);
@@ -918,7 +923,7 @@ cudaError_t gemm_pick(const Q8MatArgs& a, cudaStream_t st)
     //   8192 x  2304 x   768        16.0    17.5    17.8
     //   4096 x  4096 x  4096        51.0    41.0    46.6
     //   8192 x  1024 x  4096        36.0    35.8    28.8    (the last wave of 224 is nearly empty)
-    //   8192 x 14336 x  4096         372     274     321
+    //   8192 x 14336 x  4096         372     274     321    (short loops; 293 to 306 in longer ones)
     // Without alignment for TMA stores a 224-wide tile's stores take longer
     // than its share of the main loop is worth (4096 x 4097 x 4096: 57.5, 256: 50.7).
     const long long t1 = cdiv(m, 128) * cdiv(n, 128);
