@@ -1,8 +1,9 @@
 """Orthonormalized optimizer step (Dion power iteration, Muon Newton-Schulz)
 on one NVIDIA GB300.
 
-A thin ctypes binding over libdion.so (C ABI in include/dion.h and, for the
-8-bit linear layer's operators, include/dion_q8.h).  The binding
+A thin ctypes binding over libdion.so (C ABI in include/dion.h; for the 8-bit
+linear layer's operators include/dion_q8.h, for AdamW over many tensors
+include/dion_adamw.h, for 4-bit weights include/dion_q4.h).  The binding
 only marshals arguments: every step of the computation runs in libdion's CUDA
 kernels.  PyTorch supplies device memory and the current CUDA stream; a call's
 tensors are on the current device.  If
@@ -16,6 +17,13 @@ libdion.so is missing the import of a function raises; there is no fallback.
     w8, w8t = dion_q8_quantize(W, form="both", square=True)
     x8, h, rstd = dion_rms_norm_q8(x, weight, residual=r)
     y = dion_q8_matmul(x8, w8)
+
+    from orthonormal_optimizer_step_gb300 import dion_adamw_plan, dion_adamw_state, dion_adamw_step, dion_grad_norm
+    plan = dion_adamw_plan(params, grads, *dion_adamw_state(params, bits=8))
+    dion_adamw_step(plan, step=t, lr=1e-3, grad_scale=dion_grad_norm(plan, max_norm=1.0)[1:])
+
+    from orthonormal_optimizer_step_gb300 import dion_q4_quantize, dion_q4_matmul
+    y = dion_q4_matmul(x8, dion_q4_quantize(W))
 """
 from __future__ import annotations
 
@@ -30,14 +38,18 @@ LIB_PATH = os.path.join(_PKG, "libdion.so")
 DION_OK, DION_ERR_INVALID_ARG, DION_ERR_UNSUPPORTED, DION_ERR_WORKSPACE, DION_ERR_CUDA, DION_ERR_NUMERIC = range(6)
 DION_F32, DION_BF16 = 0, 1
 
-# The exported symbols of include/dion.h and include/dion_q8.h.
+# The exported symbols of include/*.h.
 EXPORTS = ("dion_workspace_size", "dion_workspace_panels", "dion_step_batched", "dion_step_batched_dev",
            "dion_step_batched_static", "muon_workspace_size", "muon_ns_batched",
            "dion_get_status", "dion_status_string", "dion_profile_begin", "dion_profile_end",
            "dion_profile_count", "dion_profile_entry", "dion_profile_dropped",
            # include/dion_q8.h
            "dion_q8_quantize", "dion_q8_matmul", "dion_rms_norm_q8", "dion_rms_norm_backward_workspace_size",
-           "dion_rms_norm_backward")
+           "dion_rms_norm_backward",
+           # include/dion_adamw.h
+           "dion_adamw_step", "dion_adamw_step_dev", "dion_grad_norm_workspace_size", "dion_grad_norm",
+           # include/dion_q4.h
+           "dion_q4_quantize", "dion_q4_dequantize", "dion_q4_matmul")
 
 # Muon's published quintic Newton-Schulz coefficients (a, b, c).
 QUINTIC = (3.4445, -4.7750, 2.0315)
@@ -91,11 +103,21 @@ def lib() -> ctypes.CDLL:
         L.dion_rms_norm_backward_workspace_size.argtypes = [c_int, c_int, ctypes.POINTER(c_size)]
         L.dion_rms_norm_backward.argtypes = ([c_int] * 3 + [vp, ll, vp, ll, vp, vp, c_int, vp, ll, vp, ll]
                                              + [vp, vp, c_size, vp])
+        c_double, c_uint = ctypes.c_double, ctypes.c_uint
+        L.dion_adamw_step.argtypes = [c_int, vp] + [c_double] * 5 + [ll, c_uint, vp, vp]
+        L.dion_adamw_step_dev.argtypes = [c_int, vp, vp, vp, c_uint, vp, vp, c_size, vp]
+        L.dion_grad_norm_workspace_size.argtypes = [c_int, ctypes.POINTER(c_size)]
+        L.dion_grad_norm.argtypes = [c_int, vp, c_double, vp, vp, c_size, vp]
+        L.dion_q4_quantize.argtypes = [c_int] * 4 + [vp, ll] * 3 + [vp]
+        L.dion_q4_dequantize.argtypes = [c_int] * 3 + [vp, ll] * 2 + [c_int, vp, ll, vp]
+        L.dion_q4_matmul.argtypes = [c_int] * 4 + [vp, ll] * 2 + [c_int] + [vp, ll] * 2 + [c_int, vp, ll, vp]
         for f in ("dion_workspace_size", "dion_workspace_panels", "dion_step_batched", "dion_step_batched_dev",
                   "dion_step_batched_static", "muon_workspace_size", "muon_ns_batched",
                   "dion_get_status", "dion_profile_begin", "dion_profile_end", "dion_profile_count",
                   "dion_profile_entry", "dion_profile_dropped", "dion_q8_quantize", "dion_q8_matmul",
-                  "dion_rms_norm_q8", "dion_rms_norm_backward_workspace_size", "dion_rms_norm_backward"):
+                  "dion_rms_norm_q8", "dion_rms_norm_backward_workspace_size", "dion_rms_norm_backward",
+                  "dion_adamw_step", "dion_adamw_step_dev", "dion_grad_norm_workspace_size", "dion_grad_norm",
+                  "dion_q4_quantize", "dion_q4_dequantize", "dion_q4_matmul"):
             getattr(L, f).restype = c_int
         _lib = L
         return L
@@ -304,22 +326,27 @@ class profile:
         return out
 
 
-# The 8-bit operators (q8.py) read torch when they are imported, so that waits
-# for their first use: the package itself imports, and its library loads, without torch.
+# The operators around the step (q8.py, adamw.py, q4.py) read torch when they are imported, so that
+# waits for their first use: the package itself imports, and its library loads, without torch.
 _Q8_NAMES = ("Q8", "dion_q8_matmul", "dion_q8_quantize", "dion_q8_status", "dion_rms_norm_backward",
              "dion_rms_norm_backward_workspace_size", "dion_rms_norm_q8", "new_q8")
+_ADAMW_NAMES = ("AdamWPlan", "GradList", "State8", "dion_adamw_plan", "dion_adamw_state", "dion_adamw_step",
+                "dion_grad_list", "dion_grad_norm", "dion_grad_norm_workspace_size")
+_Q4_NAMES = ("Q4", "dion_q4_dequantize", "dion_q4_matmul", "dion_q4_quantize", "new_q4")
+_MODULES = {"q8": _Q8_NAMES, "adamw": _ADAMW_NAMES, "q4": _Q4_NAMES}
 
 
 def __getattr__(name):
-    if name != "q8" and name not in _Q8_NAMES:
+    if not any(name == m or name in names for m, names in _MODULES.items()):
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     import importlib
-    q8 = importlib.import_module(".q8", __name__)
-    for n in _Q8_NAMES:
-        globals()[n] = getattr(q8, n)
+    for m, names in _MODULES.items():
+        module = importlib.import_module("." + m, __name__)
+        for n in names:
+            globals()[n] = getattr(module, n)
     globals().pop("__getattr__", None)             # all names are there now, and a module without it is read faster
     return globals()[name]
 
 
 def __dir__():
-    return sorted({*globals(), *_Q8_NAMES, "q8"})
+    return sorted({*globals(), *_MODULES, *(n for names in _MODULES.values() for n in names)})

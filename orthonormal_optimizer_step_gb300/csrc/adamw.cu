@@ -1,0 +1,644 @@
+// adamw.cu -- AdamW over many tensors in one launch, and the norm of many
+// gradients (include/dion_adamw.h).
+//
+// The list travels in the kernel's parameters (up to 32 KB), so a call moves
+// nothing to the device first and can be captured.  Tensors are cut into chunks
+// of 2048 values, eight consecutive ones a thread, numbered through the list; a
+// CTA finds its first chunk's tensor by bisection over the first chunk of each.
+// A warp's 256 values are one block of an 8-bit state, so a block's largest
+// magnitude is one reduction over the warp.
+#include <algorithm>
+#include <cmath>
+
+#include "q8.cuh"
+#include "../../include/dion_adamw.h"
+
+namespace dion {
+
+int num_sms();
+
+namespace {
+
+using namespace q8;
+
+constexpr int kThreads = 256, kPer = 8, kChunk = kThreads * kPer;
+static_assert(32 * kPer == DION_ADAMW_BLOCK, "a warp holds one block of an 8-bit state");
+
+enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kWide = 8 };   // kWide: 16-byte accesses
+
+struct Entry {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* ms;
+    float* vs;
+    bf16* copy;
+    long long n;
+    float lr_factor, decay_factor;
+    uint32_t index, flags;
+};
+
+template <int CAP>
+struct Table {
+    int count;
+    uint32_t chunks;
+    uint32_t first[CAP];           // number of each tensor's first chunk
+    Entry e[CAP];
+};
+constexpr int kSmall = 32, kLarge = 384;
+static_assert(sizeof(Table<kLarge>) <= 32764 - 256, "kernel parameters");
+
+// Constants of a step, each formed in float64 and rounded once.
+struct Constants {
+    float b1, c1, b2, c2;          // c = 1 - b
+    float rate, root, eps, decay;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), eps, lr * weight_decay
+    uint32_t key;                  // of the dither
+};
+
+// A hash of a 32-bit word: two rounds of shift, exclusive or and product.
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x)
+{
+    x = (x ^ (x >> 16)) * 0x9E3779B1u;
+    x = (x ^ (x >> 15)) * 0x85EBCA6Bu;
+    return x ^ (x >> 16);
+}
+
+__host__ __device__ inline Constants constants(double lr, double b1, double b2, double eps, double wd, long long step,
+                                               uint32_t seed)
+{
+    Constants c;
+    c.b1 = (float)b1;
+    c.c1 = (float)(1.0 - b1);
+    c.b2 = (float)b2;
+    c.c2 = (float)(1.0 - b2);
+    c.rate = (float)(lr / (1.0 - pow(b1, (double)step)));
+    c.root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)step)));
+    c.eps = (float)eps;
+    c.decay = (float)(lr * wd);
+    c.key = mix(seed * 0x632BE5ABu + (uint32_t)step);
+    return c;
+}
+
+// Tensor of chunk c: the last one whose first chunk is at or before it.
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Table<CAP>& t, uint32_t c)
+{
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.first[mid] <= c) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Eight consecutive values from p on, of which the first `k` exist.
+template <typename T>
+__device__ __forceinline__ void load_values(const T* p, bool wide, int k, float2 (&f)[4])
+{
+    if (wide && k >= 8) {
+        Raw8<T> r;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+        unpack8(r, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = make_float2(2 * i < k ? to_f(p[2 * i]) : 0.f, 2 * i + 1 < k ? to_f(p[2 * i + 1]) : 0.f);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_values(T* p, bool wide, int k, const float2 (&f)[4])
+{
+    if (wide && k >= 8) {
+        Raw8<T> r;
+        pack8(r, f);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.u[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (2 * i < k) p[2 * i] = from_f<T>(f[i].x);
+            if (2 * i + 1 < k) p[2 * i + 1] = from_f<T>(f[i].y);
+        }
+    }
+}
+__device__ __forceinline__ uint2 load_bytes(const uint8_t* p, bool wide, int k)
+{
+    if (wide && k >= 8) return *reinterpret_cast<const uint2*>(p);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < k) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_bytes(uint8_t* p, bool wide, int k, const uint32_t (&w)[2])
+{
+    if (wide && k >= 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < k) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+}
+
+// Two E4M3 bytes (the first in the low one) to float32.
+__device__ __forceinline__ float2 e4m3_pair(uint32_t w)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+    float2 f;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t"
+        "cvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+__device__ __forceinline__ void e4m3_values(uint2 b, float scale, float2 (&f)[4])
+{
+    const float2 s = make_float2(scale, scale);
+    f[0] = mul2(e4m3_pair(b.x & 0xffffu), s);
+    f[1] = mul2(e4m3_pair(b.x >> 16), s);
+    f[2] = mul2(e4m3_pair(b.y & 0xffffu), s);
+    f[3] = mul2(e4m3_pair(b.y >> 16), s);
+}
+
+// A block's scale from its largest finite magnitude.  The division is a
+// product with the reciprocal of 448 and Markstein's correction, whose
+// remainder is exact, so that the quotient is rounded once; below 2^-100 only
+// the bound counts.
+__device__ __forceinline__ float block_scale(float amax)
+{
+    constexpr float inv = 1.f / 448.f;
+    const float q = __fmul_rn(amax, inv);
+    return fmaxf(__fmaf_rn(__fmaf_rn(-q, 448.f, amax), inv, q), 0x1p-100f);
+}
+
+// Each element's dither, 20 bits, is the top of mix((at + j) ^ key) with at a
+// multiple of eight, so that (at + j) ^ key = x ^ j and mix's first shift is
+// the same for all eight.
+struct Dither {
+    uint32_t y;
+    __device__ __forceinline__ Dither(long long at, uint32_t key)
+    {
+        const uint32_t x = (uint32_t)at ^ key ^ (uint32_t)(at >> 32);
+        y = x ^ (x >> 16);
+    }
+    __device__ __forceinline__ uint32_t operator()(int j) const
+    {
+        uint32_t w = (y ^ (uint32_t)j) * 0x9E3779B1u;
+        w = (w ^ (w >> 15)) * 0x85EBCA6Bu;
+        return (w ^ (w >> 16)) >> 12;
+    }
+};
+
+// E4M3 byte of x = r / scale >= 0 (finite), rounded up where the dither
+// carries; 0 where an r above zero might have to be raised.  Times 2^-120 a
+// float's exponent is that of E4M3 (biases 127 and 7), its subnormals being
+// among the float's, and the 20 mantissa bits below E4M3's three are the place
+// between two values.  (x may exceed 448 by a rounding.)
+__device__ __forceinline__ uint32_t dithered(float x, uint32_t dither)
+{
+    return min((__float_as_uint(x) + dither) >> 20, 126u);
+}
+
+// What a thread holds of a chunk: eight values of each, of which k exist (the
+// others are zero).
+struct Values {
+    float2 p[4], g[4], m[4], v[4];
+};
+
+// Moments after the step.  Each operation is rounded once (none is contracted),
+// so that 8-bit states do not depend on how a compiler fuses them.
+__device__ __forceinline__ void moments(Values& x, const Constants& c, float f)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 g = mul2(x.g[j], make_float2(f, f));
+        x.m[j] = add2(mul2(x.m[j], make_float2(c.b1, c.b1)), mul2(g, make_float2(c.c1, c.c1)));
+        x.v[j] = add2(mul2(x.v[j], make_float2(c.b2, c.b2)), mul2(mul2(g, g), make_float2(c.c2, c.c2)));
+    }
+}
+
+// The parameters after the step, for r = sqrt(v).  The quotient is within two
+// units of the last place: an update is a thousandth of the parameter or less.
+__device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], const Constants& c, float rate, float keep)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 d = fma2(r[j], make_float2(c.root, c.root), make_float2(c.eps, c.eps));
+        float2 i;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.x) : "f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.y) : "f"(d.y));
+        const float2 u = mul2(mul2(x.m[j], make_float2(-rate, -rate)), i);
+        x.p[j] = fma2(x.p[j], make_float2(keep, keep), u);
+    }
+}
+
+__device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b, uint32_t c) { return max(max(a, b), c); }
+
+// The 8-bit states of a warp's block of 256, for moments m and roots r.
+__device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&r)[4], const Dither& dither, float& ms, float& rs,
+                                       uint32_t (&mw)[2], uint32_t (&rw)[2])
+{
+    // infinities reach the maxima, and an r that is NaN; a NaN of m does not, and has its own byte in the conversion
+    float mmax = 0.f;
+    uint32_t rmax = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        mmax = fmaxf(mmax, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
+        rmax = max3(rmax, __float_as_uint(r[j].x), __float_as_uint(r[j].y));
+    }
+    uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(mmax));
+    rmax = __reduce_max_sync(0xffffffffu, rmax);
+    const bool finite = mbits < kInfBits && rmax < kInfBits;       // the same in all lanes
+    if (!finite) {
+        mbits = rmax = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            mbits = max3(mbits, finite_mag_bits(m[j].x), finite_mag_bits(m[j].y));
+            rmax = max3(rmax, finite_mag_bits(r[j].x), finite_mag_bits(r[j].y));
+        }
+        mbits = __reduce_max_sync(0xffffffffu, mbits);
+        rmax = __reduce_max_sync(0xffffffffu, rmax);
+    }
+    ms = block_scale(__uint_as_float(mbits));
+    rs = block_scale(__uint_as_float(rmax));
+    const float mi = __frcp_rn(ms), ri = __frcp_rn(rs);
+    uint32_t code[8], least = 0xffffffffu;
+    float2 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 y = mul2(m[j], make_float2(mi, mi));
+        const uint32_t w = finite ? cvt2<DION_E4M3>(y.x, y.y) : cvt2<DION_E4M3>(inf_to_nan(y.x), inf_to_nan(y.y));
+        mw[j >> 1] = j & 1 ? mw[j >> 1] | (w << 16) : w;
+        x[j] = mul2(mul2(r[j], make_float2(ri, ri)), make_float2(0x1p-120f, 0x1p-120f));
+        code[2 * j] = dithered(x[j].x, dither(2 * j));
+        code[2 * j + 1] = dithered(x[j].y, dither(2 * j + 1));
+        least = min(min(least, __float_as_uint(x[j].x)), __float_as_uint(x[j].y));
+    }
+    if (least < 1u << 20) {                          // below E4M3's least value, 2^-9: may have become zero
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if ((j & 1 ? r[j >> 1].y : r[j >> 1].x) > 0.f) code[j] = max(code[j], 1u);
+    }
+    if (!finite) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (mag_bits(j & 1 ? r[j >> 1].y : r[j >> 1].x) >= kInfBits) code[j] = 0x7fu;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        rw[i] = (code[4 * i] + code[4 * i + 1] * 256u) + (code[4 * i + 2] + code[4 * i + 3] * 256u) * 65536u;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    adamw_kernel(const __grid_constant__ Table<CAP> t, const Constants given, const Constants* dev, const float* scale,
+                 const uint32_t per)
+{
+    wait_previous();
+    allow_next();
+    const float f = scale ? *scale : 1.f;
+    if (f != f) return;
+    const Constants c = dev ? *dev : given;
+    const int lane = threadIdx.x & 31;
+    uint32_t chunk = blockIdx.x * per;
+    const uint32_t end = min(chunk + per, t.chunks);
+    for (int i = tensor_of(t, chunk); chunk < end; ++i) {
+        const Entry& e = t.e[i];
+        const uint32_t first = t.first[i], stop = i + 1 < t.count ? min(end, t.first[i + 1]) : end;
+        const uint32_t flags = e.flags;
+        const bool wide = flags & kWide;
+        const float rate = c.rate * e.lr_factor, keep = 1.f - c.decay * e.lr_factor * e.decay_factor;
+        const uint32_t key = mix(c.key ^ e.index);
+        for (; chunk < stop; ++chunk) {
+            const long long at = (long long)(chunk - first) * kChunk + threadIdx.x * kPer;
+            const long long left = e.n - at;
+            // (of the last chunk whole warps may have nothing; a warp stays together)
+            if (left + lane * kPer <= 0) continue;
+            const int k = (int)max(0ll, min(left, 8ll));
+            Values x;
+            float2 r[4];
+            if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
+            else load_values((const float*)e.p + at, wide, k, x.p);
+            if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
+            else load_values((const float*)e.g + at, wide, k, x.g);
+            if (flags & kState8) {
+                const long long block = at / DION_ADAMW_BLOCK;
+                const uint2 mb = load_bytes((const uint8_t*)e.m + at, wide, k), rb = load_bytes((const uint8_t*)e.v + at, wide, k);
+                e4m3_values(mb, e.ms[block], x.m);
+                e4m3_values(rb, e.vs[block], x.v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
+                moments(x, c, f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = make_float2(__fsqrt_rn(x.v[j].x), __fsqrt_rn(x.v[j].y));
+                float ms, rs;
+                uint32_t mw[2], rw[2];
+                encode(x.m, r, Dither(at, key), ms, rs, mw, rw);
+                __syncwarp();                        // all lanes have read the block's scales
+                if (lane == 0) {
+                    e.ms[block] = ms;
+                    e.vs[block] = rs;
+                }
+                store_bytes((uint8_t*)e.m + at, wide, k, mw);
+                store_bytes((uint8_t*)e.v + at, wide, k, rw);
+            } else {
+                load_values((const float*)e.m + at, wide, k, x.m);
+                load_values((const float*)e.v + at, wide, k, x.v);
+                moments(x, c, f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
+                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
+                }
+                store_values((float*)e.m + at, wide, k, x.m);
+                store_values((float*)e.v + at, wide, k, x.v);
+            }
+            parameters(x, r, c, rate, keep);
+            if (flags & kParamBf16) {
+                store_values((bf16*)e.p + at, wide, k, x.p);
+            } else {
+                store_values((float*)e.p + at, wide, k, x.p);
+                if (e.copy) store_values(e.copy + at, wide, k, x.p);
+            }
+        }
+    }
+}
+
+// The constants of a step whose numbers are on the device, and its count.
+__global__ void adamw_constants_kernel(const double* hyper, long long* step, uint32_t seed, const float* scale,
+                                       Constants* out)
+{
+    wait_previous();
+    allow_next();
+    if (scale && *scale != *scale) return;          // a skipped step does not count
+    const long long t = *step + 1;
+    *out = constants(hyper[0], hyper[1], hyper[2], hyper[3], hyper[4], t, seed);
+    *step = t;
+}
+
+// ------------------------------------------------------------- gradient norm
+// Squares of a thread's eight values of each of N chunks, all loaded first.
+template <int N, typename T>
+__device__ __forceinline__ float squares(const T* g)
+{
+    Raw8<T> raw[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) raw[u].u[i] = reinterpret_cast<const uint4*>(g + u * kChunk)[i];
+    float2 acc[2] = {};
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        float2 x[4];
+        unpack8(raw[u], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j & 1] = fma2(x[j], x[j], acc[j & 1]);
+    }
+    return (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ Table<CAP> t, double* part)
+{
+    constexpr int N = 4;                             // chunks in flight
+    __shared__ double sums[kThreads / 32];
+    wait_previous();
+    allow_next();
+    uint32_t chunk = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
+    const uint32_t end = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
+    double sum = 0;                                  // of at most 32 float32 squares at a time
+    for (int i = tensor_of(t, chunk); chunk < end; ++i) {
+        const Entry& e = t.e[i];
+        const uint32_t stop = i + 1 < t.count ? min(end, t.first[i + 1]) : end;
+        const uint32_t flags = e.flags;
+        long long at = (long long)(chunk - t.first[i]) * kChunk + threadIdx.x * kPer;
+        while (chunk < stop) {
+            if ((flags & kWide) && chunk + N <= stop && at + (N - 1) * kChunk + (kThreads - threadIdx.x) * kPer <= e.n) {
+                sum += (double)(flags & kGradBf16 ? squares<N>((const bf16*)e.g + at) : squares<N>((const float*)e.g + at));
+                chunk += N;
+                at += N * kChunk;
+            } else {
+                const int k = (int)max(0ll, min(e.n - at, 8ll));
+                float2 g[4], acc = make_float2(0.f, 0.f);
+                if (flags & kGradBf16) load_values((const bf16*)e.g + at, flags & kWide, k, g);
+                else load_values((const float*)e.g + at, flags & kWide, k, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc = fma2(g[j], g[j], acc);
+                sum += (double)(acc.x + acc.y);
+                ++chunk;
+                at += kChunk;
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 32; ++w) sum += sums[w];
+        part[blockIdx.x] = sum;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* part, int parts, double max_norm, float* out)
+{
+    __shared__ double sums[kThreads / 32];
+    wait_previous();
+    allow_next();
+    double sum = 0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) sum += part[i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 32; ++w) sum += sums[w];
+        const double norm = sqrt(sum);
+        out[0] = (float)norm;
+        out[1] = isfinite(norm) ? (float)fmin(1.0, max_norm / (norm + 1e-6)) : __int_as_float(0x7fffffff);
+    }
+}
+
+// ---------------------------------------------------------------------- host
+size_t bytes_of(dion_dtype t) { return t == DION_F32 ? 4 : 2; }
+bool type_ok(dion_dtype t) { return t == DION_F32 || t == DION_BF16; }
+bool at_least(const void* p, size_t a) { return p && (uintptr_t)p % a == 0; }
+
+constexpr long long kMostValues = 1ll << 38;
+
+bool grad_ok(const dion_adamw_tensor& t) { return type_ok(t.g_type) && at_least(t.g, bytes_of(t.g_type)); }
+
+bool tensor_ok(const dion_adamw_tensor& t)
+{
+    if (!grad_ok(t) || !type_ok(t.p_type) || !at_least(t.p, bytes_of(t.p_type))) return false;
+    if (!t.m || !t.v || !t.m_scale != !t.v_scale) return false;
+    if (t.m_scale ? !at_least(t.m_scale, 4) || !at_least(t.v_scale, 4) : !at_least(t.m, 4) || !at_least(t.v, 4)) return false;
+    if (t.copy && (t.p_type != DION_F32 || (uintptr_t)t.copy % 2)) return false;
+    return std::isfinite(t.lr_factor) && std::isfinite(t.decay_factor);
+}
+
+// Checks a list; `full`: also what a step reads beside the gradients.
+dion_status list_ok(int count, const dion_adamw_tensor* tensors, bool full)
+{
+    if (count < 0 || (count > 0 && !tensors)) return DION_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        const dion_adamw_tensor& t = tensors[i];
+        if (t.n < 0) return DION_ERR_INVALID_ARG;
+        if (t.n > 0 && !(full ? tensor_ok(t) : grad_ok(t))) return DION_ERR_INVALID_ARG;
+        if (t.n > kMostValues) return DION_ERR_UNSUPPORTED;
+    }
+    return DION_OK;
+}
+
+// Fills a table with tensors from `i` on; returns the next one's number.
+template <int CAP>
+int fill(Table<CAP>& t, int i, int count, const dion_adamw_tensor* tensors, bool full)
+{
+    t.count = 0;
+    t.chunks = 0;
+    for (; i < count && t.count < CAP; ++i) {
+        const dion_adamw_tensor& s = tensors[i];
+        if (s.n == 0) continue;
+        const uint32_t chunks = (uint32_t)cdiv(s.n, kChunk);
+        if (t.chunks + (uint64_t)chunks > 0x7fffffffu) break;      // (the next launch takes it)
+        Entry& e = t.e[t.count];
+        e.g = s.g;
+        e.n = s.n;
+        e.flags = s.g_type == DION_BF16 ? (uint32_t)kGradBf16 : 0u;
+        uintptr_t all = (uintptr_t)s.g;
+        if (full) {
+            e.p = s.p;
+            e.m = s.m;
+            e.v = s.v;
+            e.ms = s.m_scale;
+            e.vs = s.v_scale;
+            e.copy = (bf16*)s.copy;
+            e.lr_factor = s.lr_factor;
+            e.decay_factor = s.decay_factor;
+            e.index = (uint32_t)i;
+            e.flags |= (s.p_type == DION_BF16 ? kParamBf16 : 0u) | (s.m_scale ? kState8 : 0u);
+            // eight 8-bit states are 8 bytes
+            all |= (uintptr_t)s.p | (uintptr_t)s.copy | ((uintptr_t)s.m | (uintptr_t)s.v) << (s.m_scale ? 1 : 0);
+        }
+        if (all % 16 == 0) e.flags |= kWide;
+        t.first[t.count++] = t.chunks;
+        t.chunks += chunks;
+    }
+    return i;
+}
+
+// Chunks a CTA: enough CTAs to fill the GPU several times, so that its end is
+// ragged by little, and otherwise few searches.
+uint32_t chunks_per_cta(uint32_t chunks)
+{
+    return (uint32_t)std::min<long long>(8, std::max<long long>(1, chunks / (32ll * num_sms())));
+}
+
+template <int CAP>
+cudaError_t step_some(int& i, int count, const dion_adamw_tensor* tensors, const Constants& c, const Constants* dev,
+                      const float* scale, cudaStream_t st)
+{
+    Table<CAP> t;
+    i = fill(t, i, count, tensors, true);
+    if (t.chunks == 0) return cudaSuccess;
+    const uint32_t per = chunks_per_cta(t.chunks);
+    return launch_overlapped("adamw", adamw_kernel<CAP>, dim3((unsigned)cdiv(t.chunks, per)), dim3(kThreads), 0, st, t, c, dev,
+                             scale, per);
+}
+
+dion_status step_all(int count, const dion_adamw_tensor* tensors, const Constants& c, const Constants* dev,
+                     const float* scale, cudaStream_t st)
+{
+    for (int i = 0; i < count;)
+        DION_TRY(count - i <= kSmall ? step_some<kSmall>(i, count, tensors, c, dev, scale, st)
+                                     : step_some<kLarge>(i, count, tensors, c, dev, scale, st));
+    return DION_OK;
+}
+
+template <int CAP>
+cudaError_t norm_some(int& i, int count, const dion_adamw_tensor* tensors, double* part, int most, int& parts,
+                      cudaStream_t st)
+{
+    Table<CAP> t;
+    i = fill(t, i, count, tensors, false);
+    if (t.chunks == 0) return cudaSuccess;
+    const int grid = (int)std::min<long long>(t.chunks, most);
+    double* at = part + parts;
+    parts += grid;
+    return launch_overlapped("grad_norm", grad_norm_kernel<CAP>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, at);
+}
+
+int norm_ctas() { return 8 * num_sms(); }
+// Launches of a list: by tensors, and by the chunks that a table counts (a
+// tensor of kMostValues has 2^27, so one takes 15 at least).
+long long norm_launches(int count) { return cdiv(count, kLarge) + cdiv(count, 15); }
+
+bool hyper_ok(double lr, double b1, double b2, double eps, double wd)
+{
+    return std::isfinite(lr) && std::isfinite(wd) && std::isfinite(eps) && eps >= 0 && b1 >= 0 && b1 < 1 && b2 >= 0 && b2 < 1;
+}
+
+}  // namespace
+}  // namespace dion
+
+using namespace dion;
+
+extern "C" dion_status dion_adamw_step(int count, const dion_adamw_tensor* tensors, double lr, double beta1, double beta2,
+                                       double eps, double weight_decay, long long step, unsigned int seed,
+                                       const float* grad_scale, void* cuda_stream)
+{
+    const dion_status ok = list_ok(count, tensors, true);
+    if (ok != DION_OK) return ok;
+    if (!hyper_ok(lr, beta1, beta2, eps, weight_decay) || step < 1 || (uintptr_t)grad_scale % 4) return DION_ERR_INVALID_ARG;
+    return step_all(count, tensors, constants(lr, beta1, beta2, eps, weight_decay, step, seed), nullptr, grad_scale,
+                    (cudaStream_t)cuda_stream);
+}
+
+extern "C" dion_status dion_adamw_step_dev(int count, const dion_adamw_tensor* tensors, const double* hyper,
+                                           long long* step, unsigned int seed, const float* grad_scale, void* workspace,
+                                           size_t workspace_bytes, void* cuda_stream)
+{
+    const dion_status ok = list_ok(count, tensors, true);
+    if (ok != DION_OK) return ok;
+    if (!at_least(hyper, 8) || !at_least(step, 8) || (uintptr_t)grad_scale % 4) return DION_ERR_INVALID_ARG;
+    if (!at_least(workspace, 16) || workspace_bytes < 256) return DION_ERR_WORKSPACE;
+    Constants* c = (Constants*)workspace;
+    DION_TRY(launch_overlapped("adamw_constants", adamw_constants_kernel, dim3(1), dim3(1), 0, (cudaStream_t)cuda_stream, hyper,
+                               step, (uint32_t)seed, grad_scale, c));
+    return step_all(count, tensors, Constants{}, c, grad_scale, (cudaStream_t)cuda_stream);
+}
+
+extern "C" dion_status dion_grad_norm_workspace_size(int count, size_t* bytes)
+{
+    if (count < 0 || !bytes) return DION_ERR_INVALID_ARG;
+    *bytes = (size_t)norm_launches(count) * norm_ctas() * sizeof(double);
+    return DION_OK;
+}
+
+extern "C" dion_status dion_grad_norm(int count, const dion_adamw_tensor* tensors, double max_norm, float* out,
+                                      void* workspace, size_t workspace_bytes, void* cuda_stream)
+{
+    const dion_status ok = list_ok(count, tensors, false);
+    if (ok != DION_OK) return ok;
+    if (!(max_norm > 0) || !at_least(out, 4)) return DION_ERR_INVALID_ARG;
+    size_t need = 0;
+    dion_grad_norm_workspace_size(count, &need);
+    if (need && (!at_least(workspace, 8) || workspace_bytes < need)) return DION_ERR_WORKSPACE;
+    const cudaStream_t st = (cudaStream_t)cuda_stream;
+    double* part = (double*)workspace;
+    int parts = 0;
+    for (int i = 0; i < count;)
+        DION_TRY(count - i <= kSmall ? norm_some<kSmall>(i, count, tensors, part, norm_ctas(), parts, st)
+                                     : norm_some<kLarge>(i, count, tensors, part, norm_ctas(), parts, st));
+    DION_TRY(launch_overlapped("grad_norm_join", grad_norm_join_kernel, dim3(1), dim3(kThreads), 0, st, (const double*)part, parts,
+                               max_norm, out));
+    return DION_OK;
+}
