@@ -2,20 +2,29 @@
 // scales.
 //
 // The time is that of reading the weights once, so everything else has to fit
-// beside the loads: a lane reads 16 bytes (32 weights) of two rows and needs
-// about 1.5 instructions a weight.  The products run on the tensor cores as
-// mma.m16n8k16 (16 rows of W against 8 columns, the columns being x's rows): a
-// weight q + 8 becomes the bfloat16 128 + (q + 8) by one shift and one logic
-// operation, a packed subtraction leaves q, exactly, and products of it with
-// bfloat16 x are exact in the float32 accumulator.  The held layout puts a
-// lane's operands of eight such products into its 16 bytes and keeps each
-// product inside one group, whose scale then multiplies the accumulated sum.
-// x float32 goes in as three bfloat16 terms in columns of their own, 8-bit rows
-// as the bfloat16 they are exactly.
+// beside the loads: a lane reads 16 bytes (32 weights) of two rows and has about
+// 1.9 instructions a weight if the memory is not to wait.  The products run on
+// the tensor cores as mma.m16n8k16 (16 rows of W against 8 columns, the columns
+// being x's rows): a weight q + 8 becomes the float16 1024 + (q + 8) or, four bits
+// higher, 1024 + 16 (q + 8) by one logic operation, and a packed addition or
+// multiply-add leaves q, exactly: 9 instructions for eight weights (bfloat16, whose
+// mantissa has no room for the higher place, takes 11).  The held layout puts a
+// lane's operands of eight such products into its 16 bytes and keeps each product
+// inside one group, whose scale then multiplies the accumulated sum.
 //
-// A CTA takes 64 rows of W, a warp 16 of them.  Where these are too few CTAs to
-// fill the GPU, a cluster of up to eight splits the contraction and joins
-// through distributed shared memory, in the order of the shares.
+// x enters as float16 times a power of two for each row and 128 columns, its
+// largest value there in [2^14, 2^15): bfloat16 exactly (down to 2^-32 of that
+// largest value, within 2^-39 of it below), 8-bit rows exactly with the scale that
+// they have, and float32 as two terms (within 2^-24, and 2^-39 of the largest) in
+// columns of their own.  Products of such operands are exact in the float32
+// accumulator.
+//
+// Tiles are 16 rows of W.  A warp keeps two batches of loads (8 KB) in flight
+// through all of its tiles, so the memory never waits for a tile's end.  The
+// eight warps of a CTA share a tile's contraction or take tiles of their own,
+// and the CTAs of a cluster share it too where the tiles are few or x is too
+// large for one CTA's shared memory; sums are joined in the order of the shares,
+// through distributed shared memory between CTAs.
 #include <algorithm>
 
 #include "q4.cuh"
@@ -26,13 +35,17 @@ int num_sms();
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 16 * kWarps;
-constexpr int kBatch = 4;                    // chunks that a warp loads together, while it works on as many
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kBatch = 4;                    // chunks that a warp loads together
+
+constexpr int kMostShared = 225 * 1024;       // bytes of a CTA
 
 struct MatParams {
     int m, n, k;
     int tokens, terms;                       // rows of x a pass, columns each of them takes
-    int chunks, per, panel;                  // of the contraction; a share's; those whose x is held at once
+    int chunks, per;                         // of the contraction; a CTA's share of them
+    int split;                               // warps that share a tile (1, 2, 4 or 8)
+    int blocks, held;                        // blocks of 8 / split tiles; those whose sums wait for a join
     dion_x_type xt;
     const void* x; long long ldx;
     const uint8_t* sx; long long ldsx;
@@ -43,20 +56,30 @@ struct MatParams {
     void* y; long long ldy; int y_f32;
 };
 
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+// d = A B, or d + A B.
+template <bool ADD>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (ADD)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Pairs (columns 2 i, 2 i + 1) of a held word as bfloat16.
-template <int I>
-__device__ __forceinline__ uint32_t weights2(uint32_t w)
+// Pairs (columns 0 and 1, 2 and 3) of the low bytes of a held word's halves as float16.
+__device__ __forceinline__ void weights4(uint32_t w, uint32_t& p0, uint32_t& p1)
 {
-    uint32_t v = ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u, r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));   // 128 + 8
-    return r;
+    uint32_t a, b;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(a) : "r"(w), "r"(0x000f000fu), "r"(0x64006400u));   // (w & mask) | 1024
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(b) : "r"(w), "r"(0x00f000f0u), "r"(0x64006400u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p0) : "r"(a), "r"(0x64086408u));                          // 1024 + 8
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p1) : "r"(b), "r"(0x2c002c00u), "r"(0xd480d480u));    // / 16, - (64 + 8)
 }
 
 // Weights are read once: they pass L1 by.
@@ -92,71 +115,137 @@ __device__ __forceinline__ float power_of(uint32_t byte)
     return byte == 255u ? __uint_as_float(0x7fc00000u) : byte ? __uint_as_float(byte << 23) : 0x1p-127f;
 }
 
-// Eight columns of x from col on as bfloat16 (three terms of float32), zeros past k.
-__device__ __forceinline__ void load_x(const MatParams& p, int row, int col, uint4 (&out)[3])
+// Eight columns of x, as loaded, zeros past k (and zeros, with scale byte 127, beyond).
+template <int XT>
+struct RawX {
+    uint32_t w[XT == DION_X_F32 ? 8 : XT == DION_X_BF16 ? 4 : 2];
+    uint32_t scale;
+};
+template <int XT>
+__device__ __forceinline__ void load_x(const MatParams& p, int row, int col, RawX<XT>& r)
 {
-    float2 f[4];
-    const bool whole = p.x_wide && col + 8 <= p.k;
-    if (p.xt == DION_X_BF16) {
-        const bf16* r = (const bf16*)p.x + row * p.ldx + col;
-        if (whole) {
-            out[0] = *reinterpret_cast<const uint4*>(r);
-            return;
-        }
+    constexpr int W = sizeof(r.w) / 4, E = 8 / W;                  // words, elements a word
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = make_float2(col + 2 * i < p.k ? to_f(r[2 * i]) : 0.f, col + 2 * i + 1 < p.k ? to_f(r[2 * i + 1]) : 0.f);
-    } else if (p.xt == DION_X_F32) {
-        const float* r = (const float*)p.x + row * p.ldx + col;
-        if (whole) {
-            q8::Raw8<float> v;
-            v.u[0] = reinterpret_cast<const uint4*>(r)[0];
-            v.u[1] = reinterpret_cast<const uint4*>(r)[1];
-            q8::unpack8(v, f);
+    for (int i = 0; i < W; ++i) r.w[i] = 0;
+    r.scale = 127;
+    const int left = p.k - col;
+    if (left <= 0) return;
+    const uint8_t* at = (const uint8_t*)p.x + (row * p.ldx + col) * (W / 2);
+    if (W == 2) r.scale = p.sx[row * p.ldsx + col / 128];
+    if (left >= 8 && (W == 2 || p.x_wide)) {                       // (8-bit rows are aligned)
+        if constexpr (W == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
+            r.w[0] = v.x;
+            r.w[1] = v.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = make_float2(col + 2 * i < p.k ? r[2 * i] : 0.f, col + 2 * i + 1 < p.k ? r[2 * i + 1] : 0.f);
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(at)[i];
+                r.w[4 * i] = v.x;
+                r.w[4 * i + 1] = v.y;
+                r.w[4 * i + 2] = v.z;
+                r.w[4 * i + 3] = v.w;
+            }
         }
     } else {
-        const uint8_t* r = (const uint8_t*)p.x + row * p.ldx + col;
-        uint32_t w[2] = {0, 0};
-        if (col + 8 <= p.k) {                // (8-bit rows are aligned)
-            const uint2 v = *reinterpret_cast<const uint2*>(r);
-            w[0] = v.x;
-            w[1] = v.y;
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < p.k) w[i >> 2] |= (uint32_t)r[i] << (8 * (i & 3));
-        }
-        const float s = col < p.k ? power_of(p.sx[row * p.ldsx + col / 128]) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint16_t b = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-            uint32_t h;
-            if (p.xt == DION_X_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
-            else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(b));
-            float2 v;
-            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-                : "=f"(v.x), "=f"(v.y)
-                : "r"(h));
-            f[i] = q8::mul2(v, make_float2(s, s));
-        }
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                r.w[i / E] |= (E == 1   ? reinterpret_cast<const uint32_t*>(at)[i]
+                               : E == 2 ? (uint32_t) reinterpret_cast<const uint16_t*>(at)[i]
+                                        : (uint32_t)at[i])
+                              << (32 / E * (i % E));
     }
-    q8::Raw8<bf16> t;
-#pragma unroll
-    for (int e = 0; e < 3; ++e) {
-        q8::pack8(t, f);
-        out[e] = t.u[0];
-        if (p.terms == 1) break;
-        float2 h[4];
-        q8::unpack8(t, h);
-        // what the term leaves (an infinity or NaN leaves nothing)
+}
+
+__device__ __forceinline__ uint32_t half2_of(float2 v)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+    return r;
+}
+__device__ __forceinline__ float2 floats_of(uint32_t h)
+{
+    float2 v;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(h));
+    return v;
+}
+
+// As float16, to the columns' places (`pitch` bytes apart); returns the power
+// of two that they are to be multiplied by.  The 16 lanes of a half-warp hold
+// the same row's 128 columns.
+template <int XT>
+__device__ __forceinline__ float store_x(const RawX<XT>& r, uint8_t* to, int pitch)
+{
+    if constexpr (XT == DION_X_E4M3 || XT == DION_X_E5M2) {
+        uint32_t h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[i].x = q8::mag_bits(h[i].x) < q8::kInfBits ? f[i].x - h[i].x : 0.f;
-            f[i].y = q8::mag_bits(h[i].y) < q8::kInfBits ? f[i].y - h[i].y : 0.f;
+            const uint16_t b = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
+            if (XT == DION_X_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(b));
+            else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h[i]) : "h"(b));
+        }
+        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+        return power_of(r.scale);
+    } else {
+        float2 f[4];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = XT == DION_X_BF16 ? q8::unpack2(r.w[i % (sizeof(r.w) / 4)])
+                                     : make_float2(__uint_as_float(r.w[2 * i % (sizeof(r.w) / 4)]),
+                                                   __uint_as_float(r.w[(2 * i + 1) % (sizeof(r.w) / 4)]));
+            amax = max(amax, max(q8::finite_mag_bits(f[i].x), q8::finite_mag_bits(f[i].y)));
+        }
+        const uint32_t half = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) amax = max(amax, __shfl_xor_sync(half, amax, o));
+        // 2^-e takes amax into [2^14, 2^15); for amax below 2^-98 it stays 2^112
+        const uint32_t e = max(amax >> 23, 29u);                   // biased: e - 14 + 127 is e's
+        const float down = __uint_as_float((268u - e) << 23), up = __uint_as_float((e - 14u) << 23);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = q8::mul2(f[i], make_float2(down, down));
+            h[i] = half2_of(v);
+            if (XT == DION_X_F32) {
+                const float2 a = floats_of(h[i]);
+                // what the first term leaves (an infinity or NaN leaves nothing)
+                l[i] = half2_of(make_float2(q8::mag_bits(a.x) < q8::kInfBits ? v.x - a.x : 0.f,
+                                            q8::mag_bits(a.y) < q8::kInfBits ? v.y - a.y : 0.f));
+            }
+        }
+        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (XT == DION_X_F32) *reinterpret_cast<uint4*>(to + pitch) = make_uint4(l[0], l[1], l[2], l[3]);
+        return up;
+    }
+}
+
+// x's rows token0 .. and chunks c0 .. c1 - 1 of them, to shared memory: the
+// columns (`xpitch` bytes apart) and their powers [chunk][column].
+template <int XT, int N>
+__device__ __forceinline__ void stage_x(const MatParams& p, int token0, int tokens, int c0, int c1, uint8_t* xs, int xpitch,
+                                        float* powers, int columns)
+{
+    constexpr int TERMS = XT == DION_X_F32 ? 2 : 1;
+    const int units = 16 * (c1 - c0), all = tokens * units;        // of eight columns
+    const uint32_t magic = 0xffffffffu / units + 1;                // quotients by a product: exact, as all * units < 2^32
+    for (int i0 = threadIdx.x; i0 < all; i0 += N * kThreads) {
+        RawX<XT> r[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = i0 + e * kThreads, row = (int)__umulhi(i, magic);
+            if (i < all) load_x<XT>(p, token0 + row, 128 * c0 + 8 * (i - row * units), r[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = i0 + e * kThreads, row = (int)__umulhi(i, magic), u = i - row * units;
+            if (i < all) {                   // (whole half-warps)
+                const float up = store_x<XT>(r[e], xs + row * TERMS * xpitch + 16 * u, xpitch);
+                if (u % 16 < TERMS) powers[u / 16 * columns + row * TERMS + u % 16] = up;
+            }
         }
     }
 }
@@ -169,195 +258,303 @@ struct Batch {
     uint32_t s[2][kBatch * S / 2];           // two scales a word
 };
 
+// Where a warp loads next: its lanes' places in rows g and g + 8 of a tile.
+struct Place {
+    const uint8_t* q[2];
+    const bf16* s[2];
+};
 template <int GROUP>
-__device__ __forceinline__ void load_batch(const MatParams& p, Batch<GROUP>& b, const uint8_t* const (&q)[2],
-                                           const bf16* const (&s)[2], int c, int end)
+__device__ __forceinline__ void load_batch(const MatParams& p, Batch<GROUP>& b, const Place& at, int c, int end)
 {
     constexpr int S = 128 / GROUP;
+    const bool whole = c + kBatch <= end;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-        if (c + u < end) {
-            b.w[u][0] = load_once(q[0] + 64ll * (c + u));
-            b.w[u][1] = load_once(q[1] + 64ll * (c + u));
+        if (whole || c + u < end) {
+            b.w[u][0] = load_once(at.q[0] + 64 * u);
+            b.w[u][1] = load_once(at.q[1] + 64 * u);
         }
+    if (p.s_wide && (c + kBatch) * S <= p.groups) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const bf16* at = s[r] + (long long)c * S;
-        if (p.s_wide && (c + kBatch) * S <= p.groups) {
+        for (int r = 0; r < 2; ++r) {
             if constexpr (S == 1) {
-                const uint2 v = *reinterpret_cast<const uint2*>(at);
+                const uint2 v = *reinterpret_cast<const uint2*>(at.s[r]);
                 b.s[r][0] = v.x;
                 b.s[r][1] = v.y;
             } else {
 #pragma unroll
                 for (int i = 0; i < S / 2; ++i) {
-                    const uint4 v = reinterpret_cast<const uint4*>(at)[i];
+                    const uint4 v = reinterpret_cast<const uint4*>(at.s[r])[i];
                     b.s[r][4 * i] = v.x;
                     b.s[r][4 * i + 1] = v.y;
                     b.s[r][4 * i + 2] = v.z;
                     b.s[r][4 * i + 3] = v.w;
                 }
             }
-        } else {
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < kBatch * S / 2; ++i) {
-                const uint16_t* u = reinterpret_cast<const uint16_t*>(at) + 2 * i;
+                const uint16_t* u = reinterpret_cast<const uint16_t*>(at.s[r]) + 2 * i;
                 const int left = p.groups - c * S - 2 * i;
                 b.s[r][i] = (left > 0 ? u[0] : 0u) | (left > 1 ? (uint32_t)u[1] << 16 : 0u);
             }
-        }
     }
 }
 
+// acc += the products of a chunk; xs: the lane's place in the chunk's columns, powers: in its powers of two.
 template <int MB, int GROUP>
-__device__ __forceinline__ void chunk_products(const Batch<GROUP>& b, int u, const uint8_t* xs, int xpitch, const bool (&has)[MB],
-                                               float (&acc)[MB][4])
+__device__ __forceinline__ void chunk_products(const Batch<GROUP>& b, int u, const uint8_t* xs, int xpitch, const float* powers,
+                                               const bool (&has)[MB], float (&acc)[MB][4])
 {
     constexpr int S = 128 / GROUP;
-    float sum[MB][4];
+    float sum[MB][4], scaled[MB][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint32_t w0 = j == 0 ? b.w[u][0].x : j == 1 ? b.w[u][0].y : j == 2 ? b.w[u][0].z : b.w[u][0].w;
         const uint32_t w1 = j == 0 ? b.w[u][1].x : j == 1 ? b.w[u][1].y : j == 2 ? b.w[u][1].z : b.w[u][1].w;
-        const uint32_t a0[4] = {weights2<0>(w0), weights2<1>(w0), weights2<2>(w0), weights2<3>(w0)};
-        const uint32_t a1[4] = {weights2<0>(w1), weights2<1>(w1), weights2<2>(w1), weights2<3>(w1)};
+        uint32_t a[2][4];                    // rows g and g + 8, columns 0 1 and 2 3; then 4 5 and 6 7
+        weights4(w0, a[0][0], a[0][2]);
+        weights4(w1, a[0][1], a[0][3]);
+        weights4(w0 >> 8, a[1][0], a[1][2]);
+        weights4(w1 >> 8, a[1][1], a[1][3]);
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            if (j * 32 % GROUP == 0) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
             uint4 x = make_uint4(0, 0, 0, 0);
             if (has[i]) x = *reinterpret_cast<const uint4*>(xs + 8 * i * xpitch + 64 * j);
-            mma(sum[i], a0[0], a1[0], a0[1], a1[1], x.x, x.y);
-            mma(sum[i], a0[2], a1[2], a0[3], a1[3], x.z, x.w);
+            if (j * 32 % GROUP == 0) mma<false>(sum[i], a[0], x.x, x.y);
+            else mma<true>(sum[i], a[0], x.x, x.y);
+            mma<true>(sum[i], a[1], x.z, x.w);
             if ((j + 1) * 32 % GROUP == 0) {
                 const int e = u * S + j * 32 / GROUP;
                 const uint32_t v0 = b.s[0][e / 2], v1 = b.s[1][e / 2];
                 const float s0 = __uint_as_float(e & 1 ? v0 & 0xffff0000u : v0 << 16);
                 const float s1 = __uint_as_float(e & 1 ? v1 & 0xffff0000u : v1 << 16);
-                acc[i][0] = fmaf(s0, sum[i][0], acc[i][0]);
-                acc[i][1] = fmaf(s0, sum[i][1], acc[i][1]);
-                acc[i][2] = fmaf(s1, sum[i][2], acc[i][2]);
-                acc[i][3] = fmaf(s1, sum[i][3], acc[i][3]);
-            }
-        }
-    }
-}
-
-template <int MB, int GROUP>
-__global__ void __launch_bounds__(kThreads) q4_matmul_kernel(const MatParams p, const int shares)
-{
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int share = shares > 1 ? (int)cluster_rank() : 0;
-    const int row0 = (int)(blockIdx.x / shares) * kRows, token0 = blockIdx.y * p.tokens;
-    const int tokens = min(p.tokens, p.m - token0), cols = tokens * p.terms;
-    const int xpitch = 256 * p.panel + 64;   // bytes; eight rows' 16-byte words then meet no bank twice
-    float* sums = (float*)(smem + p.tokens * p.terms * xpitch);   // [column][row of W]
-    const int c0 = share * p.per, c1 = min(c0 + p.per, p.chunks);
-    const bool active = row0 + 16 * warp < p.n;
-    const int r0 = min(row0 + 16 * warp + g, p.n - 1), r1 = min(row0 + 16 * warp + g + 8, p.n - 1);
-    const uint8_t* const q[2] = {p.q + r0 * p.ldq + 16 * t, p.q + r1 * p.ldq + 16 * t};
-    const bf16* const s[2] = {p.s + r0 * p.lds, p.s + r1 * p.lds};
-    bool has[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) has[i] = 8 * i + g < cols;
-    float acc[MB][4] = {};
-    wait_previous();
-    allow_next();
-    for (int pc = c0; pc < c1; pc += p.panel) {
-        const int pe = min(pc + p.panel, c1);
-        Batch<GROUP> b[2];
-        if (active) load_batch(p, b[0], q, s, pc, pe);
-        if (pc > c0) __syncthreads();        // the last panel's x has been read
-        const int units = 16 * (pe - pc);    // of eight columns
-        for (int i = threadIdx.x; i < tokens * units; i += kThreads) {
-            const int row = i / units, u = i - row * units;
-            uint4 v[3];
-            load_x(p, token0 + row, 128 * pc + 8 * u, v);
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-                if (e < p.terms) *reinterpret_cast<uint4*>(smem + (row * p.terms + e) * xpitch + 16 * u) = v[e];
-        }
-        __syncthreads();
-        if (active) {
-            const uint8_t* xs = smem + g * xpitch + 16 * t;
-#pragma unroll 1
-            for (int c = pc; c < pe; c += 2 * kBatch) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int at = c + h * kBatch;
-                    if (at >= pe) break;
-                    if (at + kBatch < pe) load_batch(p, b[h ^ 1], q, s, at + kBatch, pe);
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        if (at + u >= pe) break;
-                        chunk_products<MB, GROUP>(b[h], u, xs + 256 * (at + u - pc), xpitch, has, acc);
-                    }
+                if (j * 32 < GROUP) {
+                    scaled[i][0] = s0 * sum[i][0];
+                    scaled[i][1] = s0 * sum[i][1];
+                    scaled[i][2] = s1 * sum[i][2];
+                    scaled[i][3] = s1 * sum[i][3];
+                } else {
+                    scaled[i][0] = fmaf(s0, sum[i][0], scaled[i][0]);
+                    scaled[i][1] = fmaf(s0, sum[i][1], scaled[i][1]);
+                    scaled[i][2] = fmaf(s1, sum[i][2], scaled[i][2]);
+                    scaled[i][3] = fmaf(s1, sum[i][3], scaled[i][3]);
                 }
             }
         }
     }
-    if (active) {
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = 8 * i + 2 * t + (e & 1);
-                if (col < cols) sums[col * kRows + 16 * warp + g + 8 * (e >> 1)] = acc[i][e];
-            }
+    for (int i = 0; i < MB; ++i) {
+        const float2 up = *reinterpret_cast<const float2*>(powers + 8 * i);
+        acc[i][0] = fmaf(up.x, scaled[i][0], acc[i][0]);
+        acc[i][1] = fmaf(up.y, scaled[i][1], acc[i][1]);
+        acc[i][2] = fmaf(up.x, scaled[i][2], acc[i][2]);
+        acc[i][3] = fmaf(up.y, scaled[i][3], acc[i][3]);
     }
-    if (shares > 1) cluster_sync();
-    else __syncthreads();
-    for (int i = share * kThreads + threadIdx.x; i < tokens * kRows; i += shares * kThreads) {
-        const int row = i / kRows, r = i % kRows;
-        if (row0 + r >= p.n) continue;
+}
+
+// Sums of a cluster's held blocks, to y: CTA `share` adds its part of them.
+__device__ __forceinline__ void join(const MatParams& p, const float* hold, int first, int step, int count, int shares, int share,
+                                     int token0, int tokens)
+{
+    const int tiles = kWarps / p.split, cols = p.tokens * p.terms;
+    cluster_sync();
+    for (int i = share * kThreads + threadIdx.x; i < count * tiles * tokens * 16; i += shares * kThreads) {
+        const int r = i & 15, token = i / 16 % tokens, tile = i / 16 / tokens;      // tile: of all held ones
+        const int row = ((first + tile / tiles * step) * tiles + tile % tiles) * 16 + r;
+        if (row >= p.n) continue;
         float v = 0.f;
-        for (int e = 0; e < p.terms; ++e) {
-            const float* at = sums + (row * p.terms + e) * kRows + r;
-            if (shares == 1) v += *at;
-            else
-                for (int h = 0; h < shares; ++h) v += load_remote(at, h);
-        }
-        const long long o = (token0 + row) * p.ldy + row0 + r;
+        for (int e = 0; e < p.terms; ++e)
+            for (int h = 0; h < shares; ++h) v += load_remote(hold + (tile * cols + token * p.terms + e) * 16 + r, h);
+        const long long o = (token0 + token) * p.ldy + row;
         if (p.y_f32) ((float*)p.y)[o] = v;
         else ((bf16*)p.y)[o] = __float2bfloat16_rn(v);
     }
-    if (shares > 1) cluster_sync();          // the others have read this CTA's sums
+    cluster_sync();                          // the others have read this CTA's sums
 }
-
-// Shares of the contraction (CTAs of a cluster): as many as it takes for three
-// CTAs an SM, each with whole batches of chunks.
-int shares_of(long long row_blocks, int chunks, int& per)
-{
-    int s = (int)std::min<long long>(8, cdiv(3ll * num_sms(), row_blocks));
-    s = std::max(1, std::min(s, (int)cdiv(chunks, kBatch)));
-    per = (int)(cdiv(cdiv(chunks, s), kBatch) * kBatch);
-    return (int)cdiv(chunks, per);
-}
-
-constexpr int kPanelBytes = 65536;           // of x held at once
 
 template <int MB, int GROUP>
-cudaError_t go(MatParams& p, int shares, cudaStream_t st)
+__global__ void __launch_bounds__(kThreads, MB == 1 ? 2 : 1) q4_matmul_kernel(const MatParams p, const int shares)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int share = shares > 1 ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / shares, step = gridDim.x / shares, token0 = blockIdx.y * p.tokens;
+    const int tokens = min(p.tokens, p.m - token0), cols = tokens * p.terms, most = p.tokens * p.terms;
+    const int xpitch = 256 * p.per + 64;     // bytes; eight rows' 16-byte words then meet no bank twice
+    float* powers = (float*)(smem + most * xpitch);              // [chunk][8 MB columns]
+    float* parts = powers + p.per * 8 * MB;                      // [2][warp][column][16]: a warp's sums of a tile
+    float* hold = parts + 2 * kWarps * most * 16;                // [held][tile of the block][column][16]
+    const int c0 = share * p.per, c1 = min(c0 + p.per, p.chunks);
+    // this warp's tile of a block, and its share of the CTA's chunks in whole batches (it may have none)
+    const int tiles = kWarps / p.split, mine = warp / p.split, part = warp % p.split;
+    const int each = (c1 - c0 + p.split * kBatch - 1) / (p.split * kBatch) * kBatch;
+    const int w0 = min(c0 + part * each, c1), w1 = min(w0 + each, c1);
+    const int batches = max(1, (w1 - w0 + kBatch - 1) / kBatch);
+    bool has[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) has[i] = 8 * i + g < cols;
+    wait_previous();
+    allow_next();
+
+    Batch<GROUP> b[2];
+    int lb = first, li = 0;                  // block and batch that are loaded next
+    Place at;
+    auto load_next = [&](Batch<GROUP>& to) {
+        if (lb >= p.blocks) return;
+        if (li == 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = min(16 * (lb * tiles + mine) + g + 8 * r, p.n - 1);
+                at.q[r] = p.q + row * p.ldq + 64ll * w0 + 16 * t;
+                at.s[r] = p.s + row * p.lds + (long long)w0 * (128 / GROUP);
+            }
+        }
+        load_batch(p, to, at, w0 + li * kBatch, w1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            at.q[r] += 64 * kBatch;
+            at.s[r] += kBatch * (128 / GROUP);
+        }
+        if (++li == batches) {
+            li = 0;
+            lb += step;
+        }
+    };
+    load_next(b[0]);
+    load_next(b[1]);
+
+    if (p.xt == DION_X_BF16) stage_x<DION_X_BF16, 4>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
+    else if (p.xt == DION_X_F32) stage_x<DION_X_F32, 2>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
+    else if (p.xt == DION_X_E4M3) stage_x<DION_X_E4M3, 8>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
+    else stage_x<DION_X_E5M2, 8>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
+    __syncthreads();
+
+    const uint8_t* xs = smem + g * xpitch + 16 * t + 256 * (w0 - c0);
+    const float* ups = powers + (w0 - c0) * 8 * MB + 2 * t;
+    float acc[MB][4] = {};
+    int cb = first, ci = 0, turn = 0, held = 0;
+    while (cb < p.blocks) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (cb >= p.blocks) break;
+            const int c = ci * kBatch;
+            if (w0 + c + kBatch <= w1) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    chunk_products<MB, GROUP>(b[h], u, xs + 256 * (c + u), xpitch, ups + (c + u) * 8 * MB, has, acc);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kBatch - 1; ++u) {
+                    if (w0 + c + u >= w1) break;
+                    chunk_products<MB, GROUP>(b[h], u, xs + 256 * (c + u), xpitch, ups + (c + u) * 8 * MB, has, acc);
+                }
+            }
+            load_next(b[h]);
+            if (++ci < batches) continue;
+            // the tile's end: the sums of the warps that share it
+            float* to = parts + ((turn * kWarps + warp) * most) * 16;
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = 8 * i + 2 * t + (e & 1);
+                    if (col < cols) to[col * 16 + g + 8 * (e >> 1)] = acc[i][e];
+                    acc[i][e] = 0.f;
+                }
+            if (p.split == 1) __syncwarp();
+            else asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "r"(32 * p.split) : "memory");
+            const float* from = parts + ((turn * kWarps + mine * p.split) * most) * 16;
+            const int row0 = (cb * tiles + mine) * 16;
+            if (shares == 1) {
+                for (int i = part * 32 + lane; i < tokens * 16; i += 32 * p.split) {
+                    const int r = i & 15, token = i >> 4;
+                    float v = 0.f;
+                    for (int e = 0; e < p.terms; ++e)
+                        for (int w = 0; w < p.split; ++w) v += from[(w * most + token * p.terms + e) * 16 + r];
+                    if (row0 + r < p.n) {
+                        const long long o = (token0 + token) * p.ldy + row0 + r;
+                        if (p.y_f32) ((float*)p.y)[o] = v;
+                        else ((bf16*)p.y)[o] = __float2bfloat16_rn(v);
+                    }
+                }
+            } else {
+                float* kept = hold + (held * tiles + mine) * most * 16;
+                for (int i = part * 32 + lane; i < cols * 16; i += 32 * p.split) {
+                    float v = 0.f;
+                    for (int w = 0; w < p.split; ++w) v += from[w * most * 16 + i];
+                    kept[i] = v;
+                }
+                if (++held == p.held || cb + step >= p.blocks) {
+                    join(p, hold, cb - (held - 1) * step, step, held, shares, share, token0, tokens);
+                    held = 0;
+                }
+            }
+            // (two turns: who writes a turn's sums again has passed the other's barrier, so all have read them)
+            turn ^= 1;
+            ci = 0;
+            cb += step;
+        }
+    }
+}
+
+// CTAs of a cluster of `shares` that run at once (whole clusters lie in a group of SMs).
+int clusters_at_once(int shares)
+{
+    constexpr int at_once[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    return at_once[shares] * num_sms() / 152;
+}
+
+template <int MB, int GROUP>
+cudaError_t go(MatParams& p, int shares, size_t smem, cudaStream_t st)
 {
     static std::atomic<unsigned long long> attr{0};
-    const int cols = p.tokens * p.terms;
-    const size_t smem = (size_t)cols * (256 * p.panel + 64) + (size_t)cols * kRows * sizeof(float);
-    cudaError_t e = smem_attr_once((const void*)q4_matmul_kernel<MB, GROUP>, 2 * kPanelBytes, attr);
+    cudaError_t e = smem_attr_once((const void*)q4_matmul_kernel<MB, GROUP>, kMostShared, attr);
     if (e != cudaSuccess) return e;
-    return launch_cluster("q4_matmul", q4_matmul_kernel<MB, GROUP>,
-                          dim3((unsigned)(cdiv(p.n, kRows) * shares), (unsigned)cdiv(p.m, p.tokens)), dim3(kThreads), shares, smem, st, p,
-                          shares);
+    const int per_sm = MB == 1 && smem <= kMostShared / 2 ? 2 : 1;
+    const int clusters = std::min(p.blocks, std::max(1, per_sm * clusters_at_once(shares)));
+    return launch_cluster("q4_matmul", q4_matmul_kernel<MB, GROUP>, dim3((unsigned)(clusters * shares), (unsigned)cdiv(p.m, p.tokens)),
+                          dim3(kThreads), shares, smem, st, p, shares);
 }
 
 template <int GROUP>
-cudaError_t pick(MatParams& p, cudaStream_t st)
+cudaError_t pick(MatParams& p, int shares, size_t smem, cudaStream_t st)
 {
-    const int shares = shares_of(cdiv(p.n, kRows), p.chunks, p.per);
     const int cols = p.tokens * p.terms;
-    p.panel = std::min(p.per, std::max(kBatch, kPanelBytes / (256 * cols) / kBatch * kBatch));
-    if (cols <= 8) return go<1, GROUP>(p, shares, st);
-    if (cols <= 16) return go<2, GROUP>(p, shares, st);
-    return go<4, GROUP>(p, shares, st);
+    // (the columns that `cut` reckoned with)
+    if (cols <= 8) return go<1, GROUP>(p, shares, smem, st);
+    if (cols <= 16) return go<2, GROUP>(p, shares, smem, st);
+    return go<4, GROUP>(p, shares, smem, st);
+}
+
+// How the work is cut, for p.m rows of p.chunks chunks: rows of x a pass, CTAs
+// that share the contraction (returned), warps that share a tile.
+int cut(MatParams& p, size_t& smem)
+{
+    const int tiles = (int)cdiv(p.n, 16), sms = num_sms();
+    p.tokens = std::min(p.m, 32 / p.terms);
+    const int wide = p.tokens * p.terms <= 8 ? 8 : p.tokens * p.terms <= 16 ? 16 : 32;      // columns of a pass's kernel
+    auto share = [&](int s) { return (int)(cdiv(cdiv(p.chunks, s), kBatch) * kBatch); };
+    // x, its powers of two, the warps' sums (1 KB a column) and those that wait for a join (16 KB)
+    auto bytes = [&](int s) { return (size_t)p.tokens * p.terms * (256 * share(s) + 64 + 1024) + 4 * wide * share(s) + 16384; };
+    while (p.tokens > 1 && bytes(8) > kMostShared) --p.tokens;
+    int s = 1;
+    while (s < 8 && bytes(s) > kMostShared) ++s;
+    // few tiles: more CTAs, as long as each of a CTA's warps has a batch
+    while (s < 8 && (long long)tiles * s * 2 <= sms && cdiv(p.chunks, s + 1) >= kWarps * kBatch) ++s;
+    p.per = share(s);
+    s = (int)cdiv(p.chunks, p.per);
+    // warps share a tile down to two batches each, or one where tiles are few
+    p.split = kWarps;
+    while (p.split > 1 && p.per < p.split * kBatch * (tiles * s > 2 * sms * (kWarps / p.split) ? 2 : 1)) p.split /= 2;
+    p.blocks = (int)cdiv(tiles, kWarps / p.split);
+    const int cols = p.tokens * p.terms, block = kWarps / p.split * cols * 64;
+    p.held = std::max(1, 16384 / block);
+    smem = (size_t)cols * (256 * p.per + 64 + 1024) + (size_t)4 * wide * p.per + (s > 1 ? (size_t)p.held * block : 0);
+    return s;
 }
 
 }  // namespace
@@ -371,8 +568,7 @@ cudaError_t q4_matmul(const Q4MatArgs& a, cudaStream_t st)
     }
     MatParams p{};
     p.m = a.m; p.n = a.w.rows; p.k = a.w.cols;
-    p.terms = a.xt == DION_X_F32 ? 3 : 1;
-    p.tokens = std::min(a.m, 32 / p.terms);
+    p.terms = a.xt == DION_X_F32 ? 2 : 1;
     p.chunks = (int)cdiv(p.k, 128);
     p.xt = a.xt; p.x = a.x; p.ldx = a.ldx; p.sx = a.sx; p.ldsx = a.ldsx;
     p.x_wide = (uintptr_t)a.x % 16 == 0 && a.ldx * (a.xt == DION_X_F32 ? 4 : 2) % 16 == 0;
@@ -382,7 +578,10 @@ cudaError_t q4_matmul(const Q4MatArgs& a, cudaStream_t st)
     const int wide = std::min(16, 8 * 128 / a.w.group);            // bytes of a batch's scales that are loaded at once
     p.s_wide = (uintptr_t)a.w.s % wide == 0 && a.w.lds * 2 % wide == 0;
     p.y = a.y; p.ldy = a.ldy; p.y_f32 = a.ydt == DION_F32;
-    return a.w.group == 32 ? pick<32>(p, st) : a.w.group == 64 ? pick<64>(p, st) : pick<128>(p, st);
+    size_t smem = 0;
+    const int shares = cut(p, smem);
+    return a.w.group == 32 ? pick<32>(p, shares, smem, st) : a.w.group == 64 ? pick<64>(p, shares, smem, st)
+                                                                           : pick<128>(p, shares, smem, st);
 }
 
 }  // namespace dion

@@ -110,15 +110,16 @@ def x_values(x):
 
 
 def check(y, x, w):
-    """Products are exact (float32 x: up to 2^-24 of each, three terms of 8 bits).  A chain of sums is
-    at most the share's products of the tensor cores (16 terms each, truncated: 2^-23), its groups, the
-    shares and the terms; the result is rounded once."""
+    """Products are exact but for x's own part (float32: 2^-24 of a value; values far below the largest of a
+    row's 128 columns: 2^-39 of that).  A chain of sums is at most the share's products of the tensor cores (16
+    terms each, truncated: 2^-23), its groups, chunks, the shares and the terms; the result is rounded once."""
     xv, wv = x_values(x), values(w)
     want = xv @ wv.t()
     size = xv.abs() @ wv.abs().t()
     k = w.cols
-    chain = k / 16 + k / w.group + 8 + 8
-    slack = (chain * 2.0 ** -23 + 2.0 ** -24) * size + (2.0 ** -8 * want.abs() if y.dtype is BF16 else 2.0 ** -24 * want.abs())
+    chain = k / 16 + k / w.group + k / 128 + 8 + 8
+    far = 2.0 ** -39 * k * xv.nan_to_num().abs().amax(1, keepdim=True) * wv.nan_to_num().abs().amax(1)
+    slack = (chain * 2.0 ** -23 + 2.0 ** -24) * size + far + (2.0 ** -8 * want.abs() if y.dtype is BF16 else 2.0 ** -24 * want.abs())
     got = y.double().reshape(want.shape)
     assert torch.all((got - want).abs() <= slack)
     if y.dtype is F32 and want.numel() >= 64:

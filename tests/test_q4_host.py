@@ -70,7 +70,8 @@ def test_matmul_refuses(lib, kw):
 
 def test_matmul_empty_and_too_large(lib):
     assert matmul(lib, m=0) == OK and matmul(lib, n=0) == OK
-    assert matmul(lib, m=32 * 65535 + 1) == UNSUPPORTED and matmul(lib, xt=0, m=10 * 65535 + 1) == UNSUPPORTED
+    assert matmul(lib, m=65536) == UNSUPPORTED
+    assert matmul(lib, k=262145, ldx=262145, ldq=64 * 2049, lds=2049) == UNSUPPORTED
     assert matmul(lib, n=0x7fffffff, ldy=0x7fffffff) == UNSUPPORTED
 
 
