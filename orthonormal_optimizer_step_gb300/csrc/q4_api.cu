@@ -52,7 +52,7 @@ extern "C" dion_status dion_q4_matmul(int m, int n, int k, dion_x_type xt, const
     if (m == 0 || n == 0) return DION_OK;
     if (!matrix_ok(y, ydt, n, ldy)) return DION_ERR_INVALID_ARG;
     // a row's share of eight CTAs in shared memory; the grid's passes over the weights
-    if (k > 1 << 18 || m > 65535) return DION_ERR_UNSUPPORTED;
+    if (k > 1 << 17 || m > 65535) return DION_ERR_UNSUPPORTED;
     const Q4Side w{n, k, group, (uint8_t*)q, ldq, (bf16*)s, lds};
     if (k > 0) {
         const bool q8 = xt == DION_X_E4M3 || xt == DION_X_E5M2;

@@ -19,12 +19,14 @@
 // columns of their own.  Products of such operands are exact in the float32
 // accumulator.
 //
-// Tiles are 16 rows of W.  A warp keeps two batches of loads (8 KB) in flight
-// through all of its tiles, so the memory never waits for a tile's end.  The
-// eight warps of a CTA share a tile's contraction or take tiles of their own,
-// and the CTAs of a cluster share it too where the tiles are few or x is too
-// large for one CTA's shared memory; sums are joined in the order of the shares,
-// through distributed shared memory between CTAs.
+// Tiles are 16 rows of W.  Weights and scales go to shared memory by
+// asynchronous copies, each lane its own 16 bytes, two batches of four chunks
+// (8 KB a warp) ahead through all of a warp's tiles: no register waits for them
+// and no barrier hands them over.  The eight warps of a CTA share a tile's
+// contraction or take tiles of their own, and the CTAs of a cluster share it too
+// where the tiles are few or x is too large for one CTA's shared memory; sums
+// are joined in the order of the shares, through distributed shared memory
+// between CTAs.
 #include <algorithm>
 
 #include "q4.cuh"
@@ -36,7 +38,8 @@ int num_sms();
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kBatch = 4;                    // chunks that a warp loads together
+constexpr int kBatch = 4;                    // chunks that a warp copies together
+constexpr int kAhead = 2;                    // batches in flight
 
 constexpr int kMostShared = 225 * 1024;       // bytes of a CTA
 
@@ -52,7 +55,7 @@ struct MatParams {
     int x_wide;                              // x's rows start on 16-byte boundaries
     const uint8_t* q; long long ldq;
     const bf16* s; long long lds;
-    int groups, s_wide;                      // scale rows start on boundaries of a batch's scales
+    int group, groups, s_wide;               // scale rows start on 4-byte boundaries
     void* y; long long ldy; int y_f32;
 };
 
@@ -82,13 +85,17 @@ __device__ __forceinline__ void weights4(uint32_t w, uint32_t& p0, uint32_t& p1)
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p1) : "r"(b), "r"(0x2c002c00u), "r"(0xd480d480u));    // / 16, - (64 + 8)
 }
 
-// Weights are read once: they pass L1 by.
-__device__ __forceinline__ uint4 load_once(const uint8_t* p)
+// Asynchronous copies to shared memory (weights are read once and pass L1 by).
+__device__ __forceinline__ void copy16(uint32_t to, const void* from)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -250,71 +257,86 @@ __device__ __forceinline__ void stage_x(const MatParams& p, int token0, int toke
     }
 }
 
-// What a warp loads together: weights of rows g and g + 8 and their scales.
+// A batch in shared memory: [chunk][row g or g + 8][lane] 16 bytes of weights,
+// then [row of the tile] the batch's scales.
 template <int GROUP>
 struct Batch {
-    static constexpr int S = 128 / GROUP;    // scales of a chunk
-    uint4 w[kBatch][2];
-    uint32_t s[2][kBatch * S / 2];           // two scales a word
+    static constexpr int S = 128 / GROUP;                          // scales of a chunk
+    static constexpr int ROW = kBatch * S * 2;                     // bytes of a row's scales
+    // a row's distance: eight rows' scales then lie in different banks
+    static constexpr int PITCH = ROW + (GROUP == 32 ? 8 : 4);
+    static constexpr int WEIGHTS = kBatch * 1024, BYTES = WEIGHTS + 16 * PITCH;
 };
+static_assert(Batch<128>::BYTES % 16 == 0 && Batch<64>::BYTES % 16 == 0 && Batch<32>::BYTES % 16 == 0, "16-byte copies");
 
-// Where a warp loads next: its lanes' places in rows g and g + 8 of a tile.
+// Where a warp copies from next: its lanes' places in rows g and g + 8 of a tile.
 struct Place {
     const uint8_t* q[2];
     const bf16* s[2];
 };
+// to: the batch's place; c: its first chunk, of which those before `end` exist.
 template <int GROUP>
-__device__ __forceinline__ void load_batch(const MatParams& p, Batch<GROUP>& b, const Place& at, int c, int end)
+__device__ __forceinline__ void copy_batch(const MatParams& p, uint8_t* to, const Place& at, int c, int end, int lane)
 {
-    constexpr int S = 128 / GROUP;
+    using B = Batch<GROUP>;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t w = (uint32_t)__cvta_generic_to_shared(to) + 16 * lane;
     const bool whole = c + kBatch <= end;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
         if (whole || c + u < end) {
-            b.w[u][0] = load_once(at.q[0] + 64 * u);
-            b.w[u][1] = load_once(at.q[1] + 64 * u);
+            copy16(w + 1024 * u, at.q[0] + 64 * u);
+            copy16(w + 1024 * u + 512, at.q[1] + 64 * u);
         }
-    if (p.s_wide && (c + kBatch) * S <= p.groups) {
+    uint8_t* s = to + B::WEIGHTS + g * B::PITCH;
+    constexpr int WORDS = B::ROW / 4;                              // of two scales: 2, 4 or 8
+    if (p.s_wide && (c + kBatch) * B::S <= p.groups) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if constexpr (S == 1) {
-                const uint2 v = *reinterpret_cast<const uint2*>(at.s[r]);
-                b.s[r][0] = v.x;
-                b.s[r][1] = v.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < S / 2; ++i) {
-                    const uint4 v = reinterpret_cast<const uint4*>(at.s[r])[i];
-                    b.s[r][4 * i] = v.x;
-                    b.s[r][4 * i + 1] = v.y;
-                    b.s[r][4 * i + 2] = v.z;
-                    b.s[r][4 * i + 3] = v.w;
-                }
+        for (int i = 0; i < (WORDS + 3) / 4; ++i)
+            if (WORDS >= 4 || t < WORDS) {
+                const uint32_t d = (uint32_t)__cvta_generic_to_shared(s) + 4 * t + 16 * i;
+                copy4(d, (const uint8_t*)at.s[0] + 4 * t + 16 * i);
+                copy4(d + 8 * B::PITCH, (const uint8_t*)at.s[1] + 4 * t + 16 * i);
             }
-        }
     } else {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < (WORDS + 3) / 4; ++i)
 #pragma unroll
-            for (int i = 0; i < kBatch * S / 2; ++i) {
-                const uint16_t* u = reinterpret_cast<const uint16_t*>(at.s[r]) + 2 * i;
-                const int left = p.groups - c * S - 2 * i;
-                b.s[r][i] = (left > 0 ? u[0] : 0u) | (left > 1 ? (uint32_t)u[1] << 16 : 0u);
+            for (int r = 0; r < 2; ++r) {
+                const int e = 2 * t + 8 * i, left = p.groups - c * B::S - e;
+                const uint16_t* u = reinterpret_cast<const uint16_t*>(at.s[r]) + e;
+                const uint32_t v = (left > 0 ? u[0] : 0u) | (left > 1 ? (uint32_t)u[1] << 16 : 0u);
+                if (WORDS >= 4 || t < WORDS) *reinterpret_cast<uint32_t*>(s + 8 * r * B::PITCH + 2 * e) = v;
             }
     }
 }
 
-// acc += the products of a chunk; xs: the lane's place in the chunk's columns, powers: in its powers of two.
+// acc += the products of a chunk.  w: the lane's 16 bytes of row g, those of row g + 8 512 bytes on; s: row g's
+// scales of the chunk, row g + 8's eight rows on; xs: the lane's place in the chunk, columns: of its columns,
+// powers: in its powers of two.
 template <int MB, int GROUP>
-__device__ __forceinline__ void chunk_products(const Batch<GROUP>& b, int u, const uint8_t* xs, int xpitch, const float* powers,
-                                               const bool (&has)[MB], float (&acc)[MB][4])
+__device__ __forceinline__ void chunk_products(const uint8_t* w, const uint8_t* s, const uint8_t* xs, const int (&columns)[MB],
+                                               const float* powers, float (&acc)[MB][4])
 {
-    constexpr int S = 128 / GROUP;
+    using B = Batch<GROUP>;
+    const uint4 q0 = *reinterpret_cast<const uint4*>(w), q1 = *reinterpret_cast<const uint4*>(w + 512);
+    uint32_t sw[2][(B::S + 1) / 2];                                // two scales a word
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const uint8_t* at = s + 8 * r * B::PITCH;
+        if constexpr (B::S == 1) sw[r][0] = *reinterpret_cast<const uint16_t*>(at);
+        else if constexpr (B::S == 2) sw[r][0] = *reinterpret_cast<const uint32_t*>(at);
+        else {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
+            sw[r][0] = v.x;
+            sw[r][1] = v.y;
+        }
+    }
     float sum[MB][4], scaled[MB][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint32_t w0 = j == 0 ? b.w[u][0].x : j == 1 ? b.w[u][0].y : j == 2 ? b.w[u][0].z : b.w[u][0].w;
-        const uint32_t w1 = j == 0 ? b.w[u][1].x : j == 1 ? b.w[u][1].y : j == 2 ? b.w[u][1].z : b.w[u][1].w;
+        const uint32_t w0 = j == 0 ? q0.x : j == 1 ? q0.y : j == 2 ? q0.z : q0.w;
+        const uint32_t w1 = j == 0 ? q1.x : j == 1 ? q1.y : j == 2 ? q1.z : q1.w;
         uint32_t a[2][4];                    // rows g and g + 8, columns 0 1 and 2 3; then 4 5 and 6 7
         weights4(w0, a[0][0], a[0][2]);
         weights4(w1, a[0][1], a[0][3]);
@@ -322,14 +344,14 @@ __device__ __forceinline__ void chunk_products(const Batch<GROUP>& b, int u, con
         weights4(w1 >> 8, a[1][1], a[1][3]);
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (has[i]) x = *reinterpret_cast<const uint4*>(xs + 8 * i * xpitch + 64 * j);
+            const uint4 x = *reinterpret_cast<const uint4*>(xs + columns[i] + 64 * j);
             if (j * 32 % GROUP == 0) mma<false>(sum[i], a[0], x.x, x.y);
             else mma<true>(sum[i], a[0], x.x, x.y);
             mma<true>(sum[i], a[1], x.z, x.w);
             if ((j + 1) * 32 % GROUP == 0) {
-                const int e = u * S + j * 32 / GROUP;
-                const uint32_t v0 = b.s[0][e / 2], v1 = b.s[1][e / 2];
+                constexpr int PER = GROUP / 32;
+                const int e = j / PER;
+                const uint32_t v0 = sw[0][e / 2], v1 = sw[1][e / 2];
                 const float s0 = __uint_as_float(e & 1 ? v0 & 0xffff0000u : v0 << 16);
                 const float s1 = __uint_as_float(e & 1 ? v1 & 0xffff0000u : v1 << 16);
                 if (j * 32 < GROUP) {
@@ -377,7 +399,7 @@ __device__ __forceinline__ void join(const MatParams& p, const float* hold, int 
 }
 
 template <int MB, int GROUP>
-__global__ void __launch_bounds__(kThreads, MB == 1 ? 2 : 1) q4_matmul_kernel(const MatParams p, const int shares)
+__global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_matmul_kernel(const MatParams p, const int shares)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -385,7 +407,10 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 2 : 1) q4_matmul_kernel(co
     const int first = blockIdx.x / shares, step = gridDim.x / shares, token0 = blockIdx.y * p.tokens;
     const int tokens = min(p.tokens, p.m - token0), cols = tokens * p.terms, most = p.tokens * p.terms;
     const int xpitch = 256 * p.per + 64;     // bytes; eight rows' 16-byte words then meet no bank twice
-    float* powers = (float*)(smem + most * xpitch);              // [chunk][8 MB columns]
+    using B = Batch<GROUP>;
+    uint8_t* ring = smem + warp * (kAhead * B::BYTES);           // [batch in flight], this warp's
+    uint8_t* xall = smem + kWarps * kAhead * B::BYTES;           // [column][xpitch]
+    float* powers = (float*)(xall + most * xpitch);              // [chunk][8 MB columns]
     float* parts = powers + p.per * 8 * MB;                      // [2][warp][column][16]: a warp's sums of a tile
     float* hold = parts + 2 * kWarps * most * 16;                // [held][tile of the block][column][16]
     const int c0 = share * p.per, c1 = min(c0 + p.per, p.chunks);
@@ -394,67 +419,70 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 2 : 1) q4_matmul_kernel(co
     const int each = (c1 - c0 + p.split * kBatch - 1) / (p.split * kBatch) * kBatch;
     const int w0 = min(c0 + part * each, c1), w1 = min(w0 + each, c1);
     const int batches = max(1, (w1 - w0 + kBatch - 1) / kBatch);
-    bool has[MB];
+    // this lane's columns (past the last one, that one again: nothing reads their sums)
+    int columns[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) has[i] = 8 * i + g < cols;
+    for (int i = 0; i < MB; ++i) columns[i] = min(8 * i + g, cols - 1) * xpitch;
     wait_previous();
     allow_next();
 
-    Batch<GROUP> b[2];
-    int lb = first, li = 0;                  // block and batch that are loaded next
+    int lb = first, li = 0;                  // block and batch that are copied next
     Place at;
-    auto load_next = [&](Batch<GROUP>& to) {
-        if (lb >= p.blocks) return;
-        if (li == 0) {
+    auto copy_next = [&](int slot) {
+        if (lb < p.blocks) {
+            if (li == 0) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = min(16 * (lb * tiles + mine) + g + 8 * r, p.n - 1);
-                at.q[r] = p.q + row * p.ldq + 64ll * w0 + 16 * t;
-                at.s[r] = p.s + row * p.lds + (long long)w0 * (128 / GROUP);
-            }
-        }
-        load_batch(p, to, at, w0 + li * kBatch, w1);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            at.q[r] += 64 * kBatch;
-            at.s[r] += kBatch * (128 / GROUP);
-        }
-        if (++li == batches) {
-            li = 0;
-            lb += step;
-        }
-    };
-    load_next(b[0]);
-    load_next(b[1]);
-
-    if (p.xt == DION_X_BF16) stage_x<DION_X_BF16, 4>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
-    else if (p.xt == DION_X_F32) stage_x<DION_X_F32, 2>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
-    else if (p.xt == DION_X_E4M3) stage_x<DION_X_E4M3, 8>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
-    else stage_x<DION_X_E5M2, 8>(p, token0, tokens, c0, c1, smem, xpitch, powers, 8 * MB);
-    __syncthreads();
-
-    const uint8_t* xs = smem + g * xpitch + 16 * t + 256 * (w0 - c0);
-    const float* ups = powers + (w0 - c0) * 8 * MB + 2 * t;
-    float acc[MB][4] = {};
-    int cb = first, ci = 0, turn = 0, held = 0;
-    while (cb < p.blocks) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (cb >= p.blocks) break;
-            const int c = ci * kBatch;
-            if (w0 + c + kBatch <= w1) {
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    chunk_products<MB, GROUP>(b[h], u, xs + 256 * (c + u), xpitch, ups + (c + u) * 8 * MB, has, acc);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kBatch - 1; ++u) {
-                    if (w0 + c + u >= w1) break;
-                    chunk_products<MB, GROUP>(b[h], u, xs + 256 * (c + u), xpitch, ups + (c + u) * 8 * MB, has, acc);
+                for (int r = 0; r < 2; ++r) {
+                    const int row = min(16 * (lb * tiles + mine) + g + 8 * r, p.n - 1);
+                    at.q[r] = p.q + row * p.ldq + 64ll * w0 + 16 * t;
+                    at.s[r] = p.s + row * p.lds + (long long)w0 * B::S;
                 }
             }
-            load_next(b[h]);
-            if (++ci < batches) continue;
+            copy_batch<GROUP>(p, ring + slot * B::BYTES, at, w0 + li * kBatch, w1, lane);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                at.q[r] += 64 * kBatch;
+                at.s[r] += kBatch * B::S;
+            }
+            if (++li == batches) {
+                li = 0;
+                lb += step;
+            }
+        }
+        copies_end();                        // (an empty group keeps the count)
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) copy_next(i);
+
+    if (p.xt == DION_X_BF16) stage_x<DION_X_BF16, 8>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
+    else if (p.xt == DION_X_F32) stage_x<DION_X_F32, 4>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
+    else if (p.xt == DION_X_E4M3) stage_x<DION_X_E4M3, 8>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
+    else stage_x<DION_X_E5M2, 8>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
+    __syncthreads();
+
+    const uint8_t* xs = xall + 16 * t + 256 * (w0 - c0);
+    const float* ups = powers + (w0 - c0) * 8 * MB + 2 * t;
+    float acc[MB][4] = {};
+    int cb = first, ci = 0, turn = 0, held = 0, slot = 0;
+    while (cb < p.blocks) {
+        copies_wait();
+        __syncwarp();                        // the other lanes' scales
+        const uint8_t* wq = ring + slot * B::BYTES + 16 * lane;
+        const uint8_t* ws = ring + slot * B::BYTES + B::WEIGHTS + g * B::PITCH;
+        const int c = ci * kBatch;
+        if (w0 + c + kBatch <= w1) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                chunk_products<MB, GROUP>(wq + 1024 * u, ws + 2 * B::S * u, xs + 256 * (c + u), columns, ups + (c + u) * 8 * MB, acc);
+        } else {
+#pragma unroll 1
+            for (int u = 0; w0 + c + u < w1; ++u)
+                chunk_products<MB, GROUP>(wq + 1024 * u, ws + 2 * B::S * u, xs + 256 * (c + u), columns, ups + (c + u) * 8 * MB, acc);
+        }
+        __syncwarp();                        // all lanes have read the scales
+        copy_next(slot);
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
+        if (++ci == batches) {
             // the tile's end: the sums of the warps that share it
             float* to = parts + ((turn * kWarps + warp) * most) * 16;
 #pragma unroll
@@ -514,7 +542,7 @@ cudaError_t go(MatParams& p, int shares, size_t smem, cudaStream_t st)
     static std::atomic<unsigned long long> attr{0};
     cudaError_t e = smem_attr_once((const void*)q4_matmul_kernel<MB, GROUP>, kMostShared, attr);
     if (e != cudaSuccess) return e;
-    const int per_sm = MB == 1 && smem <= kMostShared / 2 ? 2 : 1;
+    const int per_sm = std::min(MB == 1 ? 3 : MB == 2 ? 2 : 1, (int)(228 * 1024 / (smem + 1024)));
     const int clusters = std::min(p.blocks, std::max(1, per_sm * clusters_at_once(shares)));
     return launch_cluster("q4_matmul", q4_matmul_kernel<MB, GROUP>, dim3((unsigned)(clusters * shares), (unsigned)cdiv(p.m, p.tokens)),
                           dim3(kThreads), shares, smem, st, p, shares);
@@ -538,8 +566,9 @@ int cut(MatParams& p, size_t& smem)
     p.tokens = std::min(p.m, 32 / p.terms);
     const int wide = p.tokens * p.terms <= 8 ? 8 : p.tokens * p.terms <= 16 ? 16 : 32;      // columns of a pass's kernel
     auto share = [&](int s) { return (int)(cdiv(cdiv(p.chunks, s), kBatch) * kBatch); };
-    // x, its powers of two, the warps' sums (1 KB a column) and those that wait for a join (16 KB)
-    auto bytes = [&](int s) { return (size_t)p.tokens * p.terms * (256 * share(s) + 64 + 1024) + 4 * wide * share(s) + 16384; };
+    // the batches in flight, x, its powers of two, the warps' sums (1 KB a column) and those that wait for a join (16 KB)
+    const size_t ring = (size_t)kWarps * kAhead * (p.group == 32 ? Batch<32>::BYTES : p.group == 64 ? Batch<64>::BYTES : Batch<128>::BYTES);
+    auto bytes = [&](int s) { return ring + (size_t)p.tokens * p.terms * (256 * share(s) + 64 + 1024) + 4 * wide * share(s) + 16384; };
     while (p.tokens > 1 && bytes(8) > kMostShared) --p.tokens;
     int s = 1;
     while (s < 8 && bytes(s) > kMostShared) ++s;
@@ -553,7 +582,7 @@ int cut(MatParams& p, size_t& smem)
     p.blocks = (int)cdiv(tiles, kWarps / p.split);
     const int cols = p.tokens * p.terms, block = kWarps / p.split * cols * 64;
     p.held = std::max(1, 16384 / block);
-    smem = (size_t)cols * (256 * p.per + 64 + 1024) + (size_t)4 * wide * p.per + (s > 1 ? (size_t)p.held * block : 0);
+    smem = ring + (size_t)cols * (256 * p.per + 64 + 1024) + (size_t)4 * wide * p.per + (s > 1 ? (size_t)p.held * block : 0);
     return s;
 }
 
@@ -575,8 +604,8 @@ cudaError_t q4_matmul(const Q4MatArgs& a, cudaStream_t st)
     p.q = a.w.q; p.ldq = a.w.ldq;
     p.s = a.w.s; p.lds = a.w.lds;
     p.groups = (int)cdiv(p.k, a.w.group);
-    const int wide = std::min(16, 8 * 128 / a.w.group);            // bytes of a batch's scales that are loaded at once
-    p.s_wide = (uintptr_t)a.w.s % wide == 0 && a.w.lds * 2 % wide == 0;
+    p.group = a.w.group;
+    p.s_wide = (uintptr_t)a.w.s % 4 == 0 && a.w.lds % 2 == 0;
     p.y = a.y; p.ldy = a.ldy; p.y_f32 = a.ydt == DION_F32;
     size_t smem = 0;
     const int shares = cut(p, smem);

@@ -71,7 +71,7 @@ def test_matmul_refuses(lib, kw):
 def test_matmul_empty_and_too_large(lib):
     assert matmul(lib, m=0) == OK and matmul(lib, n=0) == OK
     assert matmul(lib, m=65536) == UNSUPPORTED
-    assert matmul(lib, k=262145, ldx=262145, ldq=64 * 2049, lds=2049) == UNSUPPORTED
+    assert matmul(lib, k=131073, ldx=131073, ldq=64 * 1025, lds=1025) == UNSUPPORTED
     assert matmul(lib, n=0x7fffffff, ldy=0x7fffffff) == UNSUPPORTED
 
 
