@@ -301,20 +301,85 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&r)[4
         rw[i] = (code[4 * i] + code[4 * i + 1] * 256u) + (code[4 * i + 2] + code[4 * i + 3] * 256u) * 65536u;
 }
 
+// Whole chunks of 8-bit tensors come through shared memory, each thread copying
+// what it will read itself (and a warp's first two lanes the block's scales), so
+// that two chunks are in flight and no register waits for them.  [p | g][half][thread]
+// 16 bytes, [m | r][thread] 8 bytes, [m | r][warp] scales.
+constexpr int kAhead = 2;
+struct Stage {
+    uint4 value[2][2][kThreads];
+    uint2 state[2][kThreads];
+    float scale[2][kThreads / 32];
+};
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+    else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
+}
+
+// Whether a chunk of a tensor comes that way.
+__device__ __forceinline__ bool staged(uint32_t flags, long long n, uint32_t chunk_of_tensor)
+{
+    return (flags & (kState8 | kWide)) == (kState8 | kWide) && n - (long long)chunk_of_tensor * kChunk >= kChunk;
+}
+__device__ __forceinline__ void stage_values(uint4 (&to)[2][kThreads], const void* from, long long at, bool half)
+{
+    const uint4* p = (const uint4*)((const uint8_t*)from + at * (half ? 2 : 4));
+    copy_async(&to[0][threadIdx.x], p, 16);
+    if (!half) copy_async(&to[1][threadIdx.x], p + 1, 16);
+}
+__device__ __forceinline__ void staged_values(const uint4 (&from)[2][kThreads], bool half, float2 (&f)[4])
+{
+    if (half) {
+        Raw8<bf16> r;
+        r.u[0] = from[0][threadIdx.x];
+        unpack8(r, f);
+    } else {
+        Raw8<float> r;
+        r.u[0] = from[0][threadIdx.x];
+        r.u[1] = from[1][threadIdx.x];
+        unpack8(r, f);
+    }
+}
+
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const Constants given, const Constants* dev, const float* scale,
                  const uint32_t per)
 {
+    __shared__ Stage stages[kAhead];
     wait_previous();
     allow_next();
     const float f = scale ? *scale : 1.f;
     if (f != f) return;
     const Constants c = dev ? *dev : given;
     const int lane = threadIdx.x & 31;
-    uint32_t chunk = blockIdx.x * per;
+    uint32_t chunk = blockIdx.x * per, ahead = chunk;
     const uint32_t end = min(chunk + per, t.chunks);
-    for (int i = tensor_of(t, chunk); chunk < end; ++i) {
+    int i = tensor_of(t, chunk), ai = i;             // the tensors of `chunk` and of `ahead`
+    auto copy_next = [&](Stage& to) {
+        if (ahead < end) {
+            while (ai + 1 < t.count && t.first[ai + 1] <= ahead) ++ai;
+            const Entry& e = t.e[ai];
+            const uint32_t own = ahead - t.first[ai];
+            if (staged(e.flags, e.n, own)) {
+                const long long at = (long long)own * kChunk + threadIdx.x * kPer;
+                stage_values(to.value[0], e.p, at, e.flags & kParamBf16);
+                stage_values(to.value[1], e.g, at, e.flags & kGradBf16);
+                copy_async(&to.state[0][threadIdx.x], (const uint8_t*)e.m + at, 8);
+                copy_async(&to.state[1][threadIdx.x], (const uint8_t*)e.v + at, 8);
+                if (lane < 2) copy_async(&to.scale[lane][threadIdx.x >> 5], (lane ? e.vs : e.ms) + at / DION_ADAMW_BLOCK, 4);
+            }
+            ++ahead;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");       // (an empty group keeps the count)
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) copy_next(stages[k]);
+    int slot = 0;
+    for (; chunk < end; ++i) {
         const Entry& e = t.e[i];
         const uint32_t first = t.first[i], stop = i + 1 < t.count ? min(end, t.first[i + 1]) : end;
         const uint32_t flags = e.flags;
@@ -322,56 +387,80 @@ __global__ void __launch_bounds__(kThreads)
         const float rate = c.rate * e.lr_factor, keep = 1.f - c.decay * e.lr_factor * e.decay_factor;
         const uint32_t key = mix(c.key ^ e.index);
         for (; chunk < stop; ++chunk) {
+            Stage& stage = stages[slot];
+            slot ^= 1;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            __syncwarp();                            // the other lanes' copies of the scales
             const long long at = (long long)(chunk - first) * kChunk + threadIdx.x * kPer;
             const long long left = e.n - at;
-            // (of the last chunk whole warps may have nothing; a warp stays together)
-            if (left + lane * kPer <= 0) continue;
             const int k = (int)max(0ll, min(left, 8ll));
-            Values x;
-            float2 r[4];
-            if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
-            else load_values((const float*)e.p + at, wide, k, x.p);
-            if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
-            else load_values((const float*)e.g + at, wide, k, x.g);
-            if (flags & kState8) {
-                const long long block = at / DION_ADAMW_BLOCK;
-                const uint2 mb = load_bytes((const uint8_t*)e.m + at, wide, k), rb = load_bytes((const uint8_t*)e.v + at, wide, k);
-                e4m3_values(mb, e.ms[block], x.m);
-                e4m3_values(rb, e.vs[block], x.v);
+            // (of the last chunk whole warps may have nothing; a warp stays together)
+            if (left + lane * kPer > 0) {
+                Values x;
+                float2 r[4];
+                if (flags & kState8) {
+                    const long long block = at / DION_ADAMW_BLOCK;
+                    uint2 mb, rb;
+                    float ms, rs;
+                    if (staged(flags, e.n, chunk - first)) {
+                        staged_values(stage.value[0], flags & kParamBf16, x.p);
+                        staged_values(stage.value[1], flags & kGradBf16, x.g);
+                        mb = stage.state[0][threadIdx.x];
+                        rb = stage.state[1][threadIdx.x];
+                        ms = stage.scale[0][threadIdx.x >> 5];
+                        rs = stage.scale[1][threadIdx.x >> 5];
+                    } else {
+                        if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
+                        else load_values((const float*)e.p + at, wide, k, x.p);
+                        if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
+                        else load_values((const float*)e.g + at, wide, k, x.g);
+                        mb = load_bytes((const uint8_t*)e.m + at, wide, k);
+                        rb = load_bytes((const uint8_t*)e.v + at, wide, k);
+                        ms = e.ms[block];
+                        rs = e.vs[block];
+                    }
+                    e4m3_values(mb, ms, x.m);
+                    e4m3_values(rb, rs, x.v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
-                moments(x, c, f);
+                    for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
+                    moments(x, c, f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = make_float2(__fsqrt_rn(x.v[j].x), __fsqrt_rn(x.v[j].y));
-                float ms, rs;
-                uint32_t mw[2], rw[2];
-                encode(x.m, r, Dither(at, key), ms, rs, mw, rw);
-                __syncwarp();                        // all lanes have read the block's scales
-                if (lane == 0) {
-                    e.ms[block] = ms;
-                    e.vs[block] = rs;
+                    for (int j = 0; j < 4; ++j) r[j] = make_float2(__fsqrt_rn(x.v[j].x), __fsqrt_rn(x.v[j].y));
+                    uint32_t mw[2], rw[2];
+                    encode(x.m, r, Dither(at, key), ms, rs, mw, rw);
+                    __syncwarp();                    // all lanes have read the block's scales
+                    if (lane == 0) {
+                        e.ms[block] = ms;
+                        e.vs[block] = rs;
+                    }
+                    store_bytes((uint8_t*)e.m + at, wide, k, mw);
+                    store_bytes((uint8_t*)e.v + at, wide, k, rw);
+                } else {
+                    if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
+                    else load_values((const float*)e.p + at, wide, k, x.p);
+                    if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
+                    else load_values((const float*)e.g + at, wide, k, x.g);
+                    load_values((const float*)e.m + at, wide, k, x.m);
+                    load_values((const float*)e.v + at, wide, k, x.v);
+                    moments(x, c, f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
+                        asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
+                    }
+                    store_values((float*)e.m + at, wide, k, x.m);
+                    store_values((float*)e.v + at, wide, k, x.v);
                 }
-                store_bytes((uint8_t*)e.m + at, wide, k, mw);
-                store_bytes((uint8_t*)e.v + at, wide, k, rw);
-            } else {
-                load_values((const float*)e.m + at, wide, k, x.m);
-                load_values((const float*)e.v + at, wide, k, x.v);
-                moments(x, c, f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
-                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
+                parameters(x, r, c, rate, keep);
+                if (flags & kParamBf16) {
+                    store_values((bf16*)e.p + at, wide, k, x.p);
+                } else {
+                    store_values((float*)e.p + at, wide, k, x.p);
+                    if (e.copy) store_values(e.copy + at, wide, k, x.p);
                 }
-                store_values((float*)e.m + at, wide, k, x.m);
-                store_values((float*)e.v + at, wide, k, x.v);
             }
-            parameters(x, r, c, rate, keep);
-            if (flags & kParamBf16) {
-                store_values((bf16*)e.p + at, wide, k, x.p);
-            } else {
-                store_values((float*)e.p + at, wide, k, x.p);
-                if (e.copy) store_values(e.copy + at, wide, k, x.p);
-            }
+            __syncwarp();                            // all lanes have read the stage's scales
+            copy_next(stage);
         }
     }
 }
@@ -544,7 +633,7 @@ int fill(Table<CAP>& t, int i, int count, const dion_adamw_tensor* tensors, bool
 // ragged by little, and otherwise few searches.
 uint32_t chunks_per_cta(uint32_t chunks)
 {
-    return (uint32_t)std::min<long long>(8, std::max<long long>(1, chunks / (32ll * num_sms())));
+    return (uint32_t)std::min<long long>(32, std::max<long long>(1, chunks / (16ll * num_sms())));
 }
 
 template <int CAP>
