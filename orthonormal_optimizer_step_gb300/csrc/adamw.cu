@@ -54,6 +54,7 @@ struct Constants {
     float b1, c1, b2, c2;          // c = 1 - b
     float rate, root, eps, decay;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), eps, lr * weight_decay
     uint32_t key;                  // of the dither
+    float one;                     // 1, where the compiler does not see it (add_apart)
 };
 
 // A hash of a 32-bit word: two rounds of shift, exclusive or and product.
@@ -77,6 +78,7 @@ __host__ __device__ inline Constants constants(double lr, double b1, double b2, 
     c.eps = (float)eps;
     c.decay = (float)(lr * wd);
     c.key = mix(seed * 0x632BE5ABu + (uint32_t)step);
+    c.one = 1.f;
     return c;
 }
 
@@ -212,10 +214,11 @@ struct Values {
     float2 p[4], g[4], m[4], v[4];
 };
 
-// a + b, rounded by itself: in packed form the compiler joins the addition with
+// a + b, rounded by itself.  In packed form the compiler joins an addition with
 // the product before it, explicit rounding or not (measured: a quarter of the
-// sums had the bits of a fused operation).
-__device__ __forceinline__ float2 add_apart(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+// sums had the bits of a fused operation); a multiply-add with a one that it does
+// not know cannot be joined.
+__device__ __forceinline__ float2 add_apart(float2 a, float2 b, float one) { return fma2(a, make_float2(one, one), b); }
 
 // Moments after the step.  Each operation is rounded once (none is fused with
 // another), so that the bits of 8-bit states follow from the formula alone.
@@ -224,8 +227,8 @@ __device__ __forceinline__ void moments(Values& x, const Constants& c, float f)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 g = mul2(x.g[j], make_float2(f, f));
-        x.m[j] = add_apart(mul2(x.m[j], make_float2(c.b1, c.b1)), mul2(g, make_float2(c.c1, c.c1)));
-        x.v[j] = add_apart(mul2(x.v[j], make_float2(c.b2, c.b2)), mul2(mul2(g, g), make_float2(c.c2, c.c2)));
+        x.m[j] = add_apart(mul2(x.m[j], make_float2(c.b1, c.b1)), mul2(g, make_float2(c.c1, c.c1)), c.one);
+        x.v[j] = add_apart(mul2(x.v[j], make_float2(c.b2, c.b2)), mul2(mul2(g, g), make_float2(c.c2, c.c2)), c.one);
     }
 }
 
@@ -246,33 +249,55 @@ __device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], cons
 
 __device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b, uint32_t c) { return max(max(a, b), c); }
 
-// The 8-bit states of a warp's block of 256, for moments m and roots r.
-__device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&r)[4], const Dither& dither, float& ms, float& rs,
-                                       uint32_t (&mw)[2], uint32_t (&rw)[2])
+// Square roots of v >= 0, finite, and one more of the warp's largest: Newton's step
+// on s = v / sqrt(v) with the residual v - s^2 formed exactly, from a reciprocal
+// root within 2^-22.  The result is off the real root by 2^-43 of it before its one
+// rounding, so it is the nearest float32 but for a few v in a million (whose root
+// lies that close to half-way between two).  A third of the instructions of the
+// function that has no such exceptions.
+__device__ __forceinline__ float2 roots(float2 v)
 {
-    // infinities reach the maxima, and an r that is NaN; a NaN of m does not, and has its own byte in the conversion
+    float2 y;                                        // (of zero: finite, and the product with it zero)
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1e-38f)));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1e-38f)));
+    const float2 s = mul2(v, y);
+    const float2 residual = fma2(make_float2(-s.x, -s.y), s, v);
+    return fma2(residual, mul2(y, make_float2(0.5f, 0.5f)), s);
+}
+
+// The roots r of second moments v, and the 8-bit states of a warp's block of 256.
+__device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4], float2 (&r)[4], const Dither& dither, float& ms,
+                                       float& rs, uint32_t (&mw)[2], uint32_t (&rw)[2])
+{
+    // infinities reach the maxima, and a v that is NaN; a NaN of m does not, and has its own byte in the conversion
     float mmax = 0.f;
-    uint32_t rmax = 0;
+    uint32_t vmax = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         mmax = fmaxf(mmax, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
-        rmax = max3(rmax, __float_as_uint(r[j].x), __float_as_uint(r[j].y));
+        vmax = max3(vmax, __float_as_uint(v[j].x), __float_as_uint(v[j].y));
     }
     uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(mmax));
-    rmax = __reduce_max_sync(0xffffffffu, rmax);
-    const bool finite = mbits < kInfBits && rmax < kInfBits;       // the same in all lanes
-    if (!finite) {
-        mbits = rmax = 0;
+    vmax = __reduce_max_sync(0xffffffffu, vmax);
+    float rmax;
+    const bool finite = mbits < kInfBits && vmax < kInfBits;       // the same in all lanes
+    if (finite) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = roots(v[j]);
+        rmax = roots(make_float2(__uint_as_float(vmax), 0.f)).x;
+    } else {
+        uint32_t rbits = mbits = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            r[j] = make_float2(__fsqrt_rn(v[j].x), __fsqrt_rn(v[j].y));
             mbits = max3(mbits, finite_mag_bits(m[j].x), finite_mag_bits(m[j].y));
-            rmax = max3(rmax, finite_mag_bits(r[j].x), finite_mag_bits(r[j].y));
+            rbits = max3(rbits, finite_mag_bits(r[j].x), finite_mag_bits(r[j].y));
         }
         mbits = __reduce_max_sync(0xffffffffu, mbits);
-        rmax = __reduce_max_sync(0xffffffffu, rmax);
+        rmax = __uint_as_float(__reduce_max_sync(0xffffffffu, rbits));
     }
     ms = block_scale(__uint_as_float(mbits));
-    rs = block_scale(__uint_as_float(rmax));
+    rs = block_scale(rmax);
     const float mi = __frcp_rn(ms), ri = __frcp_rn(rs);
     uint32_t code[8], least = 0xffffffffu;
     float2 x[4];
@@ -301,51 +326,123 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&r)[4
         rw[i] = (code[4 * i] + code[4 * i + 1] * 256u) + (code[4 * i + 2] + code[4 * i + 3] * 256u) * 65536u;
 }
 
-// Whole chunks of 8-bit tensors come through shared memory, each thread copying
-// what it will read itself (and a warp's first two lanes the block's scales), so
-// that two chunks are in flight and no register waits for them.  [p | g][half][thread]
-// 16 bytes, [m | r][thread] 8 bytes, [m | r][warp] scales.
-constexpr int kAhead = 2;
-struct Stage {
-    uint4 value[2][2][kThreads];
-    uint2 state[2][kThreads];
-    float scale[2][kThreads / 32];
-};
-__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes)
+// A step with 8-bit states on what a thread holds; encodes them into mw and rw, with the block's new scales in ms and rs.
+__device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, float& rs, const Constants& c, float f, float rate,
+                                      float keep, const Dither& dither, uint32_t (&mw)[2], uint32_t (&rw)[2])
 {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
-    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
-    else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(from) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
+    float2 r[4];
+    e4m3_values(mb, ms, x.m);
+    e4m3_values(rb, rs, x.v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
+    moments(x, c, f);
+    encode(x.m, x.v, r, dither, ms, rs, mw, rw);
+    parameters(x, r, c, rate, keep);
 }
 
-// Whether a chunk of a tensor comes that way.
-__device__ __forceinline__ bool staged(uint32_t flags, long long n, uint32_t chunk_of_tensor)
+// Whole chunks of an 8-bit tensor with aligned addresses come through shared
+// memory, each warp copying what it will read itself, 16 bytes a lane side by side,
+// so that two chunks are in flight and no register waits for them.  The instructions around a chunk's eight values a thread count (81 a value
+// with the general loop's branches and addresses took 655 us for the listed 262
+// million values), so types are fixed and addresses are kept.
+constexpr int kAhead = 2;
+struct Stage {
+    uint4 value[2][2 * kThreads];                    // [p | g] in the memory's order, a warp's 1 KB (512 bytes) together
+    uint2 state[2][kThreads];                        // [m | r][thread]
+    float scale[2][kThreads / 32];                   // [m | r][warp]
+};
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from)
 {
-    return (flags & (kState8 | kWide)) == (kState8 | kWide) && n - (long long)chunk_of_tensor * kChunk >= kChunk;
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(from), "n"(BYTES) : "memory");
 }
-__device__ __forceinline__ void stage_values(uint4 (&to)[2][kThreads], const void* from, long long at, bool half)
+template <typename P, typename G>
+__device__ __forceinline__ void whole_chunks8(const Entry& e, long long at, int chunks, const Constants& c, float f, float rate,
+                                              float keep, uint32_t key, Stage (&stages)[kAhead])
 {
-    const uint4* p = (const uint4*)((const uint8_t*)from + at * (half ? 2 : 4));
-    copy_async(&to[0][threadIdx.x], p, 16);
-    if (!half) copy_async(&to[1][threadIdx.x], p + 1, 16);
-}
-__device__ __forceinline__ void staged_values(const uint4 (&from)[2][kThreads], bool half, float2 (&f)[4])
-{
-    if (half) {
-        Raw8<bf16> r;
-        r.u[0] = from[0][threadIdx.x];
-        unpack8(r, f);
-    } else {
-        Raw8<float> r;
-        r.u[0] = from[0][threadIdx.x];
-        r.u[1] = from[1][threadIdx.x];
-        unpack8(r, f);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    P* p = (P*)e.p + at;
+    const G* g = (const G*)e.g + at;                 // (this thread's eight values; as are the next)
+    uint8_t* m = (uint8_t*)e.m + at;
+    uint8_t* v = (uint8_t*)e.v + at;
+    float* ms = e.ms + at / DION_ADAMW_BLOCK;
+    float* vs = e.vs + at / DION_ADAMW_BLOCK;
+    bf16* copy = sizeof(P) == 4 && e.copy ? e.copy + at : nullptr;
+    int left = chunks;                               // of them from p, g, m and v on
+    // of a warp's values, 16-byte word i of lane l is word 32 i + l (float32 words of a thread lie side by side)
+    constexpr int PW = sizeof(P) / 2, GW = sizeof(G) / 2;
+    const uint4* pw = (const uint4*)p - (PW - 1) * lane;
+    const uint4* gw = (const uint4*)g - (GW - 1) * lane;
+    constexpr int PC = kChunk * (int)sizeof(P) / 16, GC = kChunk * (int)sizeof(G) / 16;      // words of a chunk
+    auto fetch = [&](Stage& to, int d) {             // chunk d from there
+        if (d < left) {
+#pragma unroll
+            for (int i = 0; i < PW; ++i) copy_async<16>(&to.value[0][warp * 32 * PW + 32 * i + lane], pw + d * PC + 32 * i);
+#pragma unroll
+            for (int i = 0; i < GW; ++i) copy_async<16>(&to.value[1][warp * 32 * GW + 32 * i + lane], gw + d * GC + 32 * i);
+            copy_async<8>(&to.state[0][threadIdx.x], m + d * kChunk);
+            copy_async<8>(&to.state[1][threadIdx.x], v + d * kChunk);
+            if (lane < 2) copy_async<4>(&to.scale[lane][warp], (lane ? vs : ms) + d * (kChunk / DION_ADAMW_BLOCK));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");       // (an empty group keeps the count)
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(stages[i], i);
+#pragma unroll 1
+    for (int n = 0; n < chunks; n += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (n + i >= chunks) break;
+            Stage& from = stages[i];
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            __syncwarp();                            // the other lanes' copies
+            Values x;
+            Raw8<P> rp;
+            Raw8<G> rg;
+#pragma unroll
+            for (int k = 0; k < PW; ++k) rp.u[k] = from.value[0][threadIdx.x * PW + k];
+#pragma unroll
+            for (int k = 0; k < GW; ++k) rg.u[k] = from.value[1][threadIdx.x * GW + k];
+            unpack8(rp, x.p);
+            unpack8(rg, x.g);
+            const uint2 mb = from.state[0][threadIdx.x], rb = from.state[1][threadIdx.x];
+            float s0 = from.scale[0][warp], s1 = from.scale[1][warp];
+            __syncwarp();                            // all lanes have read theirs
+            fetch(from, kAhead);
+            uint32_t mw[2], rw[2];
+            step8(x, mb, rb, s0, s1, c, f, rate, keep, Dither(at, key), mw, rw);
+            pack8(rp, x.p);
+#pragma unroll
+            for (int k = 0; k < PW; ++k) reinterpret_cast<uint4*>(p)[k] = rp.u[k];
+            if (sizeof(P) == 4 && copy) {
+                Raw8<bf16> rc;
+                pack8(rc, x.p);
+                *reinterpret_cast<uint4*>(copy) = rc.u[0];
+                copy += kChunk;
+            }
+            *reinterpret_cast<uint2*>(m) = make_uint2(mw[0], mw[1]);
+            *reinterpret_cast<uint2*>(v) = make_uint2(rw[0], rw[1]);
+            if (lane == 0) {
+                *ms = s0;
+                *vs = s1;
+            }
+            at += kChunk;
+            p += kChunk;
+            pw += PC;
+            gw += GC;
+            m += kChunk;
+            v += kChunk;
+            ms += kChunk / DION_ADAMW_BLOCK;
+            vs += kChunk / DION_ADAMW_BLOCK;
+            --left;
+        }
     }
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const Constants given, const Constants* dev, const float* scale,
                  const uint32_t per)
 {
@@ -356,111 +453,73 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (f != f) return;
     const Constants c = dev ? *dev : given;
     const int lane = threadIdx.x & 31;
-    uint32_t chunk = blockIdx.x * per, ahead = chunk;
+    uint32_t chunk = blockIdx.x * per;
     const uint32_t end = min(chunk + per, t.chunks);
-    int i = tensor_of(t, chunk), ai = i;             // the tensors of `chunk` and of `ahead`
-    auto copy_next = [&](Stage& to) {
-        if (ahead < end) {
-            while (ai + 1 < t.count && t.first[ai + 1] <= ahead) ++ai;
-            const Entry& e = t.e[ai];
-            const uint32_t own = ahead - t.first[ai];
-            if (staged(e.flags, e.n, own)) {
-                const long long at = (long long)own * kChunk + threadIdx.x * kPer;
-                stage_values(to.value[0], e.p, at, e.flags & kParamBf16);
-                stage_values(to.value[1], e.g, at, e.flags & kGradBf16);
-                copy_async(&to.state[0][threadIdx.x], (const uint8_t*)e.m + at, 8);
-                copy_async(&to.state[1][threadIdx.x], (const uint8_t*)e.v + at, 8);
-                if (lane < 2) copy_async(&to.scale[lane][threadIdx.x >> 5], (lane ? e.vs : e.ms) + at / DION_ADAMW_BLOCK, 4);
-            }
-            ++ahead;
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");       // (an empty group keeps the count)
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) copy_next(stages[k]);
-    int slot = 0;
-    for (; chunk < end; ++i) {
+    for (int i = tensor_of(t, chunk); chunk < end; ++i) {
         const Entry& e = t.e[i];
         const uint32_t first = t.first[i], stop = i + 1 < t.count ? min(end, t.first[i + 1]) : end;
         const uint32_t flags = e.flags;
         const bool wide = flags & kWide;
         const float rate = c.rate * e.lr_factor, keep = 1.f - c.decay * e.lr_factor * e.decay_factor;
         const uint32_t key = mix(c.key ^ e.index);
+        if ((flags & (kState8 | kWide)) == (kState8 | kWide)) {
+            const long long at = (long long)(chunk - first) * kChunk + threadIdx.x * kPer;
+            const int whole = (int)min((long long)(stop - chunk), e.n / kChunk - (long long)(chunk - first));
+            if (whole > 0) {
+                if (flags & kParamBf16) {
+                    if (flags & kGradBf16) whole_chunks8<bf16, bf16>(e, at, whole, c, f, rate, keep, key, stages);
+                    else whole_chunks8<bf16, float>(e, at, whole, c, f, rate, keep, key, stages);
+                } else {
+                    if (flags & kGradBf16) whole_chunks8<float, bf16>(e, at, whole, c, f, rate, keep, key, stages);
+                    else whole_chunks8<float, float>(e, at, whole, c, f, rate, keep, key, stages);
+                }
+                chunk += whole;
+            }
+        }
         for (; chunk < stop; ++chunk) {
-            Stage& stage = stages[slot];
-            slot ^= 1;
-            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-            __syncwarp();                            // the other lanes' copies of the scales
             const long long at = (long long)(chunk - first) * kChunk + threadIdx.x * kPer;
             const long long left = e.n - at;
-            const int k = (int)max(0ll, min(left, 8ll));
             // (of the last chunk whole warps may have nothing; a warp stays together)
-            if (left + lane * kPer > 0) {
-                Values x;
+            if (left + lane * kPer <= 0) continue;
+            const int k = (int)max(0ll, min(left, 8ll));
+            Values x;
+            if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
+            else load_values((const float*)e.p + at, wide, k, x.p);
+            if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
+            else load_values((const float*)e.g + at, wide, k, x.g);
+            if (flags & kState8) {
+                const long long block = at / DION_ADAMW_BLOCK;
+                const uint2 mb = load_bytes((const uint8_t*)e.m + at, wide, k), rb = load_bytes((const uint8_t*)e.v + at, wide, k);
+                float ms = e.ms[block], rs = e.vs[block];
+                uint32_t mw[2], rw[2];
+                step8(x, mb, rb, ms, rs, c, f, rate, keep, Dither(at, key), mw, rw);
+                __syncwarp();                        // all lanes have read the block's scales
+                if (lane == 0) {
+                    e.ms[block] = ms;
+                    e.vs[block] = rs;
+                }
+                store_bytes((uint8_t*)e.m + at, wide, k, mw);
+                store_bytes((uint8_t*)e.v + at, wide, k, rw);
+            } else {
                 float2 r[4];
-                if (flags & kState8) {
-                    const long long block = at / DION_ADAMW_BLOCK;
-                    uint2 mb, rb;
-                    float ms, rs;
-                    if (staged(flags, e.n, chunk - first)) {
-                        staged_values(stage.value[0], flags & kParamBf16, x.p);
-                        staged_values(stage.value[1], flags & kGradBf16, x.g);
-                        mb = stage.state[0][threadIdx.x];
-                        rb = stage.state[1][threadIdx.x];
-                        ms = stage.scale[0][threadIdx.x >> 5];
-                        rs = stage.scale[1][threadIdx.x >> 5];
-                    } else {
-                        if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
-                        else load_values((const float*)e.p + at, wide, k, x.p);
-                        if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
-                        else load_values((const float*)e.g + at, wide, k, x.g);
-                        mb = load_bytes((const uint8_t*)e.m + at, wide, k);
-                        rb = load_bytes((const uint8_t*)e.v + at, wide, k);
-                        ms = e.ms[block];
-                        rs = e.vs[block];
-                    }
-                    e4m3_values(mb, ms, x.m);
-                    e4m3_values(rb, rs, x.v);
+                load_values((const float*)e.m + at, wide, k, x.m);
+                load_values((const float*)e.v + at, wide, k, x.v);
+                moments(x, c, f);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
-                    moments(x, c, f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) r[j] = make_float2(__fsqrt_rn(x.v[j].x), __fsqrt_rn(x.v[j].y));
-                    uint32_t mw[2], rw[2];
-                    encode(x.m, r, Dither(at, key), ms, rs, mw, rw);
-                    __syncwarp();                    // all lanes have read the block's scales
-                    if (lane == 0) {
-                        e.ms[block] = ms;
-                        e.vs[block] = rs;
-                    }
-                    store_bytes((uint8_t*)e.m + at, wide, k, mw);
-                    store_bytes((uint8_t*)e.v + at, wide, k, rw);
-                } else {
-                    if (flags & kParamBf16) load_values((const bf16*)e.p + at, wide, k, x.p);
-                    else load_values((const float*)e.p + at, wide, k, x.p);
-                    if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
-                    else load_values((const float*)e.g + at, wide, k, x.g);
-                    load_values((const float*)e.m + at, wide, k, x.m);
-                    load_values((const float*)e.v + at, wide, k, x.v);
-                    moments(x, c, f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
-                        asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
-                    }
-                    store_values((float*)e.m + at, wide, k, x.m);
-                    store_values((float*)e.v + at, wide, k, x.v);
+                for (int j = 0; j < 4; ++j) {
+                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
+                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
                 }
                 parameters(x, r, c, rate, keep);
-                if (flags & kParamBf16) {
-                    store_values((bf16*)e.p + at, wide, k, x.p);
-                } else {
-                    store_values((float*)e.p + at, wide, k, x.p);
-                    if (e.copy) store_values(e.copy + at, wide, k, x.p);
-                }
+                store_values((float*)e.m + at, wide, k, x.m);
+                store_values((float*)e.v + at, wide, k, x.v);
             }
-            __syncwarp();                            // all lanes have read the stage's scales
-            copy_next(stage);
+            if (flags & kParamBf16) {
+                store_values((bf16*)e.p + at, wide, k, x.p);
+            } else {
+                store_values((float*)e.p + at, wide, k, x.p);
+                if (e.copy) store_values(e.copy + at, wide, k, x.p);
+            }
         }
     }
 }
@@ -502,23 +561,30 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const __grid_constant__ Table<CAP> t, double* part)
 {
-    constexpr int N = 4;                             // chunks in flight
+    constexpr int N = 4;                             // chunks of float32 in flight, twice as many of bfloat16
     __shared__ double sums[kThreads / 32];
     wait_previous();
     allow_next();
     uint32_t chunk = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
     const uint32_t end = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
-    double sum = 0;                                  // of at most 32 float32 squares at a time
+    double sum = 0;                                  // of 64 float32 squares at a time
     for (int i = tensor_of(t, chunk); chunk < end; ++i) {
         const Entry& e = t.e[i];
         const uint32_t stop = i + 1 < t.count ? min(end, t.first[i + 1]) : end;
         const uint32_t flags = e.flags;
         long long at = (long long)(chunk - t.first[i]) * kChunk + threadIdx.x * kPer;
         while (chunk < stop) {
-            if ((flags & kWide) && chunk + N <= stop && at + (N - 1) * kChunk + (kThreads - threadIdx.x) * kPer <= e.n) {
-                sum += (double)(flags & kGradBf16 ? squares<N>((const bf16*)e.g + at) : squares<N>((const float*)e.g + at));
-                chunk += N;
-                at += N * kChunk;
+            if ((flags & kWide) && chunk + 2 * N <= stop && at + (2 * N - 1) * kChunk + (kThreads - threadIdx.x) * kPer <= e.n) {
+                float part;
+                if (flags & kGradBf16) {
+                    part = squares<2 * N>((const bf16*)e.g + at);
+                } else {
+                    part = squares<N>((const float*)e.g + at);
+                    part += squares<N>((const float*)e.g + at + N * kChunk);
+                }
+                sum += (double)part;
+                chunk += 2 * N;
+                at += 2 * N * kChunk;
             } else {
                 const int k = (int)max(0ll, min(e.n - at, 8ll));
                 float2 g[4], acc = make_float2(0.f, 0.f);
@@ -664,13 +730,14 @@ cudaError_t norm_some(int& i, int count, const dion_adamw_tensor* tensors, doubl
     Table<CAP> t;
     i = fill(t, i, count, tensors, false);
     if (t.chunks == 0) return cudaSuccess;
-    const int grid = (int)std::min<long long>(t.chunks, most);
+    const int grid = (int)std::min<long long>(t.chunks < 2048 ? t.chunks : cdiv(t.chunks, 16), most);
     double* at = part + parts;
     parts += grid;
     return launch_overlapped("grad_norm", grad_norm_kernel<CAP>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, at);
 }
 
-int norm_ctas() { return 8 * num_sms(); }
+// Partial sums of a launch: as many CTAs as run at once several times over, so that none ends much later than the others.
+int norm_ctas() { return 32 * num_sms(); }
 // Launches of a list: by tensors, and by the chunks that a table counts (a
 // tensor of kMostValues has 2^27, so one takes 15 at least).
 long long norm_launches(int count) { return cdiv(count, kLarge) + cdiv(count, 15); }

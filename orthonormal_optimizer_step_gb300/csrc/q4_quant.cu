@@ -46,14 +46,32 @@ __global__ void __launch_bounds__(kThreads)
         const bool finite = amax < kInfBits;
         const bf16 s = finite ? from_f<bf16>(__fdiv_rn(__uint_as_float(amax), 7.f)) : from_f<bf16>(__uint_as_float(0x7fc00000u));
         const float by = to_f(s);
-        uint32_t word = 0x88888888u;
-        if (finite && by > 0.f) {
+        uint32_t word;
+        if (finite && by >= 0x1p-100f) {
+            // Quotients by the scale's reciprocal and Markstein's correction, whose remainder is exact: the division's
+            // own results, ties among them.  1.5 * 2^23 + 8 rounds them to whole numbers, plus eight, in the low bits
+            // (a scale is bf16(amax / 7), so they lie in -7 .. 7).
+            const float inv = __frcp_rn(by);
             word = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = __fdiv_rn(i & 1 ? f[i >> 1].y : f[i >> 1].x, by);
-                const int q = min(max(__float2int_rn(v), -8), 7) + 8;
-                word |= (uint32_t)q << (4 * (i >> 1) + 16 * (i & 1));
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = mul2(f[i], make_float2(inv, inv));
+                const float2 rest = fma2(make_float2(-v.x, -v.y), make_float2(by, by), f[i]);
+                const float2 w = fma2(rest, make_float2(inv, inv), v);
+                const float2 q = add2(w, make_float2(12582920.f, 12582920.f));
+                // columns 2 i and 2 i + 1: four bits of each half
+                word += __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x5410) << (4 * i);
+            }
+        } else {
+            word = 0x88888888u;
+            if (finite && by > 0.f) {
+                word = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float v = __fdiv_rn(i & 1 ? f[i >> 1].y : f[i >> 1].x, by);
+                    const int q = min(max(__float2int_rn(v), -8), 7) + 8;
+                    word |= (uint32_t)q << (4 * (i >> 1) + 16 * (i & 1));
+                }
             }
         }
         const int col = 128 * (int)chunk[u] + 8 * l;
@@ -88,9 +106,13 @@ __global__ void __launch_bounds__(kThreads)
         if ((blockIdx.x * kUnits + u) * kHalves + half >= units) break;
         float2 f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = make_float2((float)((int)((word[u] >> (4 * i)) & 15u) - 8) * s[u],
-                               (float)((int)((word[u] >> (4 * i + 16)) & 15u) - 8) * s[u]);
+        for (int i = 0; i < 4; ++i) {
+            // four bits in a float's low ones are 2^23 + q + 8
+            const uint32_t w = (word[u] >> (4 * i)) & 0x000f000fu;
+            const float2 q = add2(make_float2(__uint_as_float(w & 15u | 0x4b000000u), __uint_as_float(w >> 16 | 0x4b000000u)),
+                                  make_float2(-8388616.f, -8388616.f));
+            f[i] = mul2(q, make_float2(s[u], s[u]));
+        }
         T* r = y + row[u] * ldy;
         const int c0 = 128 * (int)chunk[u];
         if (aligned && c0 + 8 * l + 8 <= w.cols) {

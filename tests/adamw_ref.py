@@ -55,23 +55,29 @@ def scales(x):
     return (full.view(-1, BLOCK).amax(1) / 448).clamp(min=2.0 ** -100)
 
 
-def check8(state, want, rounded_up=None):
+def check8(state, want, rounded_up=None, terms=None):
     """A State8 against its float64 moment (or root).
 
-    The moments are right to 3 roundings each, the root and the division by the scale
-    to as many more: 8 half steps of float32, 2^-21, are granted to what is rounded.
-    `rounded_up`: the dither; else to nearest."""
+    The second moment is right to 6 roundings (its terms are positive), the root and the
+    division by the scale to two more each: 8 half steps of float32, 2^-21, are granted to
+    what is rounded.  A first moment is a sum of two terms, each right to two roundings,
+    that may cancel: 4 half steps of `terms`, the sum of their magnitudes, are granted to it
+    besides.  `rounded_up`: the dither; else to nearest."""
     n = want.numel()
     s = scales(want)
     got_s = state.scale.double()
-    assert torch.all((got_s - s).abs() <= 2.0 ** -21 * s)
+    off = torch.zeros_like(want) if terms is None else 2.0 ** -22 * terms
+    most = torch.zeros(s.numel() * BLOCK, dtype=torch.float64, device=want.device)
+    most[:n] = off.nan_to_num(posinf=0.0)
+    assert torch.all((got_s - s).abs() <= 2.0 ** -21 * s + most.view(-1, BLOCK).amax(1) / 448)
+    off = off / got_s.repeat_interleave(BLOCK)[:n]
     y = want / got_s.repeat_interleave(BLOCK)[:n]
     got = state.data.flatten().double()
     ok = torch.isfinite(want)
     assert torch.all(torch.isnan(got[~ok]))
-    y, got = y[ok], got[ok]
+    y, got, off = y[ok], got[ok], off[ok]
     step = spacing(y.abs())
-    slack = 2.0 ** -21 * y.abs() + 2.0 ** -29              # (below 2^-6 float32's own subnormals count)
+    slack = 2.0 ** -21 * y.abs() + 2.0 ** -29 + off        # (below 2^-6 float32's own subnormals count)
     if rounded_up is None:
         # half the distance to a neighbour; at a power of two the distance below is half of that above
         assert torch.all((got - y).abs() <= step / 2 + slack)
