@@ -37,9 +37,16 @@ int num_sms();
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kBatch = 4;                    // chunks that a warp copies together
-constexpr int kAhead = 2;                    // batches in flight
+constexpr int kUnit = 4;                     // shares of the contraction are multiples of these chunks
+
+// How a kernel of 8 MB columns is laid out.
+template <int MB>
+struct Cfg {
+    static constexpr int WARPS = 8, THREADS = 32 * WARPS;
+    static constexpr int CTAS = MB == 1 ? 2 : 1;                   // an SM
+    static constexpr int BATCH = MB == 1 ? 4 : 2;                  // chunks that a warp copies together
+    static constexpr int AHEAD = 2;          // batches in flight
+};
 
 constexpr int kMostShared = 225 * 1024;       // bytes of a CTA
 
@@ -47,15 +54,15 @@ struct MatParams {
     int m, n, k;
     int tokens, terms;                       // rows of x a pass, columns each of them takes
     int chunks, per;                         // of the contraction; a CTA's share of them
-    int split;                               // warps that share a tile (1, 2, 4 or 8)
-    int blocks, held;                        // blocks of 8 / split tiles; those whose sums wait for a join
+    int split;                               // warps that share a tile (a power of two)
+    int blocks, held;                        // blocks of warps / split tiles; those whose sums wait for a join
     dion_x_type xt;
     const void* x; long long ldx;
     const uint8_t* sx; long long ldsx;
     int x_wide;                              // x's rows start on 16-byte boundaries
     const uint8_t* q; long long ldq;
     const bf16* s; long long lds;
-    int group, groups, s_wide;               // scale rows start on 4-byte boundaries
+    int groups, s_wide;               // scale rows start on 4-byte boundaries
     void* y; long long ldy; int y_f32;
 };
 
@@ -90,12 +97,18 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy8(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t to, const void* from)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+// Until all but the last `LEFT` groups are here.
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -122,46 +135,38 @@ __device__ __forceinline__ float power_of(uint32_t byte)
     return byte == 255u ? __uint_as_float(0x7fc00000u) : byte ? __uint_as_float(byte << 23) : 0x1p-127f;
 }
 
-// Eight columns of x, as loaded, zeros past k (and zeros, with scale byte 127, beyond).
-template <int XT>
-struct RawX {
-    uint32_t w[XT == DION_X_F32 ? 8 : XT == DION_X_BF16 ? 4 : 2];
-    uint32_t scale;
-};
-template <int XT>
-__device__ __forceinline__ void load_x(const MatParams& p, int row, int col, RawX<XT>& r)
+// x comes in two steps, a thread doing both for its units of eight columns:
+// copied as it is to the place of its float16 (8, 16 or, in two terms' places, 32
+// bytes), then converted there.  All copies are issued before the first weights:
+// behind the weights in flight a load of x takes as long as they do (8 rows of
+// 14336x4096 took 4 us longer than one).
+template <int XT, int THREADS>
+__device__ __forceinline__ void copy_x(const MatParams& p, int token0, int tokens, int c0, int c1, uint8_t* xs, int xpitch,
+                                       uint32_t magic)
 {
-    constexpr int W = sizeof(r.w) / 4, E = 8 / W;                  // words, elements a word
+    constexpr int TERMS = XT == DION_X_F32 ? 2 : 1, BYTES = XT == DION_X_F32 ? 32 : XT == DION_X_BF16 ? 16 : 8;
+    const int units = 16 * (c1 - c0), all = tokens * units;
+    for (int i = threadIdx.x; i < all; i += THREADS) {
+        const int row = (int)__umulhi(i, magic), u = i - row * units, col = 128 * c0 + 8 * u, left = p.k - col;
+        uint8_t* to = xs + row * TERMS * xpitch + 16 * u;
+        const uint8_t* from = (const uint8_t*)p.x + ((token0 + row) * p.ldx + col) * (BYTES / 8);
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+        if (left >= 8 && (BYTES == 8 || p.x_wide)) {               // (8-bit rows are aligned)
+            if (BYTES == 8) {
+                copy8(d, from);
+            } else {
+                copy16(d, from);
+                if (BYTES == 32) copy16(d + xpitch, from + 16);
+            }
+        } else {                                                   // zeros past k
 #pragma unroll
-    for (int i = 0; i < W; ++i) r.w[i] = 0;
-    r.scale = 127;
-    const int left = p.k - col;
-    if (left <= 0) return;
-    const uint8_t* at = (const uint8_t*)p.x + (row * p.ldx + col) * (W / 2);
-    if (W == 2) r.scale = p.sx[row * p.ldsx + col / 128];
-    if (left >= 8 && (W == 2 || p.x_wide)) {                       // (8-bit rows are aligned)
-        if constexpr (W == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(at);
-            r.w[0] = v.x;
-            r.w[1] = v.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < W / 4; ++i) {
-                const uint4 v = reinterpret_cast<const uint4*>(at)[i];
-                r.w[4 * i] = v.x;
-                r.w[4 * i + 1] = v.y;
-                r.w[4 * i + 2] = v.z;
-                r.w[4 * i + 3] = v.w;
+            for (int e = 0; e < 8; ++e) {
+                uint8_t* at = to + (BYTES == 32 ? (e >> 2) * xpitch + 4 * (e & 3) : BYTES / 8 * e);
+                if (BYTES == 32) *reinterpret_cast<uint32_t*>(at) = e < left ? reinterpret_cast<const uint32_t*>(from)[e] : 0u;
+                else if (BYTES == 16) *reinterpret_cast<uint16_t*>(at) = e < left ? reinterpret_cast<const uint16_t*>(from)[e] : 0;
+                else *at = e < left ? from[e] : 0;
             }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left)
-                r.w[i / E] |= (E == 1   ? reinterpret_cast<const uint32_t*>(at)[i]
-                               : E == 2 ? (uint32_t) reinterpret_cast<const uint16_t*>(at)[i]
-                                        : (uint32_t)at[i])
-                              << (32 / E * (i % E));
     }
 }
 
@@ -180,94 +185,95 @@ __device__ __forceinline__ float2 floats_of(uint32_t h)
     return v;
 }
 
-// As float16, to the columns' places (`pitch` bytes apart); returns the power
-// of two that they are to be multiplied by.  The 16 lanes of a half-warp hold
-// the same row's 128 columns.
+// A unit of plain x to float16, in place; returns the power of two that it is to
+// be multiplied by.  The 16 lanes of a half-warp hold a row's 128 columns.
 template <int XT>
-__device__ __forceinline__ float store_x(const RawX<XT>& r, uint8_t* to, int pitch)
+__device__ __forceinline__ float convert_x(uint8_t* at, int pitch)
 {
-    if constexpr (XT == DION_X_E4M3 || XT == DION_X_E5M2) {
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint16_t b = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
-            if (XT == DION_X_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(b));
-            else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h[i]) : "h"(b));
-        }
-        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-        return power_of(r.scale);
+    float2 f[4];
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    if constexpr (XT == DION_X_BF16) {
+        f[0] = q8::unpack2(v.x);
+        f[1] = q8::unpack2(v.y);
+        f[2] = q8::unpack2(v.z);
+        f[3] = q8::unpack2(v.w);
     } else {
-        float2 f[4];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = XT == DION_X_BF16 ? q8::unpack2(r.w[i % (sizeof(r.w) / 4)])
-                                     : make_float2(__uint_as_float(r.w[2 * i % (sizeof(r.w) / 4)]),
-                                                   __uint_as_float(r.w[(2 * i + 1) % (sizeof(r.w) / 4)]));
-            amax = max(amax, max(q8::finite_mag_bits(f[i].x), q8::finite_mag_bits(f[i].y)));
-        }
-        const uint32_t half = 0xffffu << (threadIdx.x & 16);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) amax = max(amax, __shfl_xor_sync(half, amax, o));
-        // 2^-e takes amax into [2^14, 2^15); for amax below 2^-98 it stays 2^112
-        const uint32_t e = max(amax >> 23, 29u);                   // biased: e - 14 + 127 is e's
-        const float down = __uint_as_float((268u - e) << 23), up = __uint_as_float((e - 14u) << 23);
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = q8::mul2(f[i], make_float2(down, down));
-            h[i] = half2_of(v);
-            if (XT == DION_X_F32) {
-                const float2 a = floats_of(h[i]);
-                // what the first term leaves (an infinity or NaN leaves nothing)
-                l[i] = half2_of(make_float2(q8::mag_bits(a.x) < q8::kInfBits ? v.x - a.x : 0.f,
-                                            q8::mag_bits(a.y) < q8::kInfBits ? v.y - a.y : 0.f));
-            }
-        }
-        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (XT == DION_X_F32) *reinterpret_cast<uint4*>(to + pitch) = make_uint4(l[0], l[1], l[2], l[3]);
-        return up;
+        q8::Raw8<float> r;
+        r.u[0] = v;
+        r.u[1] = *reinterpret_cast<const uint4*>(at + pitch);
+        q8::unpack8(r, f);
     }
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = max(amax, max(q8::finite_mag_bits(f[i].x), q8::finite_mag_bits(f[i].y)));
+    const uint32_t half = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) amax = max(amax, __shfl_xor_sync(half, amax, o));
+    // 2^-e takes amax into [2^14, 2^15); for amax below 2^-98 it stays 2^112
+    const uint32_t e = max(amax >> 23, 29u);                       // biased: e - 14 + 127 is e's
+    const float down = __uint_as_float((268u - e) << 23), up = __uint_as_float((e - 14u) << 23);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 w = q8::mul2(f[i], make_float2(down, down));
+        h[i] = half2_of(w);
+        if (XT == DION_X_F32) {
+            const float2 a = floats_of(h[i]);
+            // what the first term leaves (an infinity or NaN leaves nothing)
+            l[i] = half2_of(make_float2(q8::mag_bits(a.x) < q8::kInfBits ? w.x - a.x : 0.f,
+                                        q8::mag_bits(a.y) < q8::kInfBits ? w.y - a.y : 0.f));
+        }
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (XT == DION_X_F32) *reinterpret_cast<uint4*>(at + pitch) = make_uint4(l[0], l[1], l[2], l[3]);
+    return up;
+}
+// A unit of 8-bit x.
+template <int XT>
+__device__ __forceinline__ void widen_x(uint8_t* at)
+{
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t b = (uint16_t)((i < 2 ? v.x : v.y) >> (16 * (i & 1)));
+        if (XT == DION_X_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(b));
+        else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h[i]) : "h"(b));
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// x's rows token0 .. and chunks c0 .. c1 - 1 of them, to shared memory: the
-// columns (`xpitch` bytes apart) and their powers [chunk][column].
-template <int XT, int N>
-__device__ __forceinline__ void stage_x(const MatParams& p, int token0, int tokens, int c0, int c1, uint8_t* xs, int xpitch,
-                                        float* powers, int columns)
+// What copy_x brought, converted by the threads that copied it; powers: [chunk][column].
+template <int XT, int THREADS>
+__device__ __forceinline__ void convert_all(int tokens, int c0, int c1, uint8_t* xs, int xpitch, float* powers, int columns,
+                                            uint32_t magic)
 {
     constexpr int TERMS = XT == DION_X_F32 ? 2 : 1;
-    const int units = 16 * (c1 - c0), all = tokens * units;        // of eight columns
-    const uint32_t magic = 0xffffffffu / units + 1;                // quotients by a product: exact, as all * units < 2^32
-    for (int i0 = threadIdx.x; i0 < all; i0 += N * kThreads) {
-        RawX<XT> r[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int i = i0 + e * kThreads, row = (int)__umulhi(i, magic);
-            if (i < all) load_x<XT>(p, token0 + row, 128 * c0 + 8 * (i - row * units), r[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int i = i0 + e * kThreads, row = (int)__umulhi(i, magic), u = i - row * units;
-            if (i < all) {                   // (whole half-warps)
-                const float up = store_x<XT>(r[e], xs + row * TERMS * xpitch + 16 * u, xpitch);
-                if (u % 16 < TERMS) powers[u / 16 * columns + row * TERMS + u % 16] = up;
-            }
+    const int units = 16 * (c1 - c0), all = tokens * units;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < all; i += THREADS) {             // (whole half-warps)
+        const int row = (int)__umulhi(i, magic), u = i - row * units;
+        uint8_t* at = xs + row * TERMS * xpitch + 16 * u;
+        if constexpr (XT == DION_X_F32 || XT == DION_X_BF16) {
+            const float up = convert_x<XT>(at, xpitch);
+            if (u % 16 < TERMS) powers[u / 16 * columns + row * TERMS + u % 16] = up;
+        } else {
+            widen_x<XT>(at);
         }
     }
 }
 
 // A batch in shared memory: [chunk][row g or g + 8][lane] 16 bytes of weights,
 // then [row of the tile] the batch's scales.
-template <int GROUP>
+template <int GROUP, int BATCH>
 struct Batch {
     static constexpr int S = 128 / GROUP;                          // scales of a chunk
-    static constexpr int ROW = kBatch * S * 2;                     // bytes of a row's scales
+    static constexpr int ROW = BATCH * S * 2;                     // bytes of a row's scales
     // a row's distance: eight rows' scales then lie in different banks
     static constexpr int PITCH = ROW + (GROUP == 32 ? 8 : 4);
-    static constexpr int WEIGHTS = kBatch * 1024, BYTES = WEIGHTS + 16 * PITCH;
+    static constexpr int WEIGHTS = BATCH * 1024, BYTES = WEIGHTS + 16 * PITCH;
+    static_assert(BYTES % 16 == 0 && ROW % 4 == 0, "whole words");
 };
-static_assert(Batch<128>::BYTES % 16 == 0 && Batch<64>::BYTES % 16 == 0 && Batch<32>::BYTES % 16 == 0, "16-byte copies");
 
 // Where a warp copies from next: its lanes' places in rows g and g + 8 of a tile.
 struct Place {
@@ -275,22 +281,22 @@ struct Place {
     const bf16* s[2];
 };
 // to: the batch's place; c: its first chunk, of which those before `end` exist.
-template <int GROUP>
+template <int GROUP, int BATCH>
 __device__ __forceinline__ void copy_batch(const MatParams& p, uint8_t* to, const Place& at, int c, int end, int lane)
 {
-    using B = Batch<GROUP>;
+    using B = Batch<GROUP, BATCH>;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t w = (uint32_t)__cvta_generic_to_shared(to) + 16 * lane;
-    const bool whole = c + kBatch <= end;
+    const bool whole = c + BATCH <= end;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
+    for (int u = 0; u < BATCH; ++u)
         if (whole || c + u < end) {
             copy16(w + 1024 * u, at.q[0] + 64 * u);
             copy16(w + 1024 * u + 512, at.q[1] + 64 * u);
         }
     uint8_t* s = to + B::WEIGHTS + g * B::PITCH;
-    constexpr int WORDS = B::ROW / 4;                              // of two scales: 2, 4 or 8
-    if (p.s_wide && (c + kBatch) * B::S <= p.groups) {
+    constexpr int WORDS = B::ROW / 4;                              // of two scales: 1 to 8
+    if (p.s_wide && (c + BATCH) * B::S <= p.groups) {
 #pragma unroll
         for (int i = 0; i < (WORDS + 3) / 4; ++i)
             if (WORDS >= 4 || t < WORDS) {
@@ -314,11 +320,10 @@ __device__ __forceinline__ void copy_batch(const MatParams& p, uint8_t* to, cons
 // acc += the products of a chunk.  w: the lane's 16 bytes of row g, those of row g + 8 512 bytes on; s: row g's
 // scales of the chunk, row g + 8's eight rows on; xs: the lane's place in the chunk, columns: of its columns,
 // powers: in its powers of two.
-template <int MB, int GROUP>
+template <int MB, int GROUP, class B>
 __device__ __forceinline__ void chunk_products(const uint8_t* w, const uint8_t* s, const uint8_t* xs, const int (&columns)[MB],
                                                const float* powers, float (&acc)[MB][4])
 {
-    using B = Batch<GROUP>;
     const uint4 q0 = *reinterpret_cast<const uint4*>(w), q1 = *reinterpret_cast<const uint4*>(w + 512);
     uint32_t sw[2][(B::S + 1) / 2];                                // two scales a word
 #pragma unroll
@@ -379,12 +384,13 @@ __device__ __forceinline__ void chunk_products(const uint8_t* w, const uint8_t* 
 }
 
 // Sums of a cluster's held blocks, to y: CTA `share` adds its part of them.
+template <int THREADS>
 __device__ __forceinline__ void join(const MatParams& p, const float* hold, int first, int step, int count, int shares, int share,
                                      int token0, int tokens)
 {
-    const int tiles = kWarps / p.split, cols = p.tokens * p.terms;
+    const int tiles = THREADS / 32 / p.split, cols = p.tokens * p.terms;
     cluster_sync();
-    for (int i = share * kThreads + threadIdx.x; i < count * tiles * tokens * 16; i += shares * kThreads) {
+    for (int i = share * THREADS + threadIdx.x; i < count * tiles * tokens * 16; i += shares * THREADS) {
         const int r = i & 15, token = i / 16 % tokens, tile = i / 16 / tokens;      // tile: of all held ones
         const int row = ((first + tile / tiles * step) * tiles + tile % tiles) * 16 + r;
         if (row >= p.n) continue;
@@ -399,7 +405,7 @@ __device__ __forceinline__ void join(const MatParams& p, const float* hold, int 
 }
 
 template <int MB, int GROUP>
-__global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_matmul_kernel(const MatParams p, const int shares)
+__global__ void __launch_bounds__(Cfg<MB>::THREADS, Cfg<MB>::CTAS) q4_matmul_kernel(const MatParams p, const int shares)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -407,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_ma
     const int first = blockIdx.x / shares, step = gridDim.x / shares, token0 = blockIdx.y * p.tokens;
     const int tokens = min(p.tokens, p.m - token0), cols = tokens * p.terms, most = p.tokens * p.terms;
     const int xpitch = 256 * p.per + 64;     // bytes; eight rows' 16-byte words then meet no bank twice
-    using B = Batch<GROUP>;
+    constexpr int kWarps = Cfg<MB>::WARPS, kBatch = Cfg<MB>::BATCH, kAhead = Cfg<MB>::AHEAD, kThreads = Cfg<MB>::THREADS;
+    using B = Batch<GROUP, kBatch>;
     uint8_t* ring = smem + warp * (kAhead * B::BYTES);           // [batch in flight], this warp's
     uint8_t* xall = smem + kWarps * kAhead * B::BYTES;           // [column][xpitch]
     float* powers = (float*)(xall + most * xpitch);              // [chunk][8 MB columns]
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_ma
                     at.s[r] = p.s + row * p.lds + (long long)w0 * B::S;
                 }
             }
-            copy_batch<GROUP>(p, ring + slot * B::BYTES, at, w0 + li * kBatch, w1, lane);
+            copy_batch<GROUP, kBatch>(p, ring + slot * B::BYTES, at, w0 + li * kBatch, w1, lane);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 at.q[r] += 64 * kBatch;
@@ -451,13 +458,24 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_ma
         }
         copies_end();                        // (an empty group keeps the count)
     };
+    const uint32_t magic = 0xffffffffu / (16 * (c1 - c0)) + 1;     // quotients by a row's units as products: exact below 2^32 / units
+    if (p.xt == DION_X_BF16) copy_x<DION_X_BF16, kThreads>(p, token0, tokens, c0, c1, xall, xpitch, magic);
+    else if (p.xt == DION_X_F32) copy_x<DION_X_F32, kThreads>(p, token0, tokens, c0, c1, xall, xpitch, magic);
+    else {
+        copy_x<DION_X_E4M3, kThreads>(p, token0, tokens, c0, c1, xall, xpitch, magic);
+        for (int i = threadIdx.x; i < tokens * (c1 - c0); i += kThreads) {
+            const int row = i / (c1 - c0), c = i - row * (c1 - c0);
+            powers[c * 8 * MB + row] = power_of(p.sx[(token0 + row) * p.ldsx + c0 + c]);
+        }
+    }
+    copies_end();
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) copy_next(i);
-
-    if (p.xt == DION_X_BF16) stage_x<DION_X_BF16, 8>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
-    else if (p.xt == DION_X_F32) stage_x<DION_X_F32, 4>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
-    else if (p.xt == DION_X_E4M3) stage_x<DION_X_E4M3, 8>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
-    else stage_x<DION_X_E5M2, 8>(p, token0, tokens, c0, c1, xall, xpitch, powers, 8 * MB);
+    copies_wait<kAhead>();                   // x is here
+    if (p.xt == DION_X_BF16) convert_all<DION_X_BF16, kThreads>(tokens, c0, c1, xall, xpitch, powers, 8 * MB, magic);
+    else if (p.xt == DION_X_F32) convert_all<DION_X_F32, kThreads>(tokens, c0, c1, xall, xpitch, powers, 8 * MB, magic);
+    else if (p.xt == DION_X_E4M3) convert_all<DION_X_E4M3, kThreads>(tokens, c0, c1, xall, xpitch, powers, 8 * MB, magic);
+    else convert_all<DION_X_E5M2, kThreads>(tokens, c0, c1, xall, xpitch, powers, 8 * MB, magic);
     __syncthreads();
 
     const uint8_t* xs = xall + 16 * t + 256 * (w0 - c0);
@@ -465,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_ma
     float acc[MB][4] = {};
     int cb = first, ci = 0, turn = 0, held = 0, slot = 0;
     while (cb < p.blocks) {
-        copies_wait();
+        copies_wait<kAhead - 1>();
         __syncwarp();                        // the other lanes' scales
         const uint8_t* wq = ring + slot * B::BYTES + 16 * lane;
         const uint8_t* ws = ring + slot * B::BYTES + B::WEIGHTS + g * B::PITCH;
@@ -473,11 +491,11 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_ma
         if (w0 + c + kBatch <= w1) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
-                chunk_products<MB, GROUP>(wq + 1024 * u, ws + 2 * B::S * u, xs + 256 * (c + u), columns, ups + (c + u) * 8 * MB, acc);
+                chunk_products<MB, GROUP, B>(wq + 1024 * u, ws + 2 * B::S * u, xs + 256 * (c + u), columns, ups + (c + u) * 8 * MB, acc);
         } else {
 #pragma unroll 1
             for (int u = 0; w0 + c + u < w1; ++u)
-                chunk_products<MB, GROUP>(wq + 1024 * u, ws + 2 * B::S * u, xs + 256 * (c + u), columns, ups + (c + u) * 8 * MB, acc);
+                chunk_products<MB, GROUP, B>(wq + 1024 * u, ws + 2 * B::S * u, xs + 256 * (c + u), columns, ups + (c + u) * 8 * MB, acc);
         }
         __syncwarp();                        // all lanes have read the scales
         copy_next(slot);
@@ -517,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 3 : MB == 2 ? 2 : 1) q4_ma
                     kept[i] = v;
                 }
                 if (++held == p.held || cb + step >= p.blocks) {
-                    join(p, hold, cb - (held - 1) * step, step, held, shares, share, token0, tokens);
+                    join<kThreads>(p, hold, cb - (held - 1) * step, step, held, shares, share, token0, tokens);
                     held = 0;
                 }
             }
@@ -536,54 +554,60 @@ int clusters_at_once(int shares)
     return at_once[shares] * num_sms() / 152;
 }
 
+// How the work is cut, for p.m rows of p.chunks chunks: rows of x a pass (fixed
+// before), CTAs that share the contraction (returned; 0: x does not fit), warps
+// that share a tile, and a CTA's shared memory.
 template <int MB, int GROUP>
-cudaError_t go(MatParams& p, int shares, size_t smem, cudaStream_t st)
+int cut(MatParams& p, size_t& smem)
 {
+    using C = Cfg<MB>;
+    constexpr size_t ring = (size_t)C::WARPS * C::AHEAD * Batch<GROUP, C::BATCH>::BYTES;
+    const int tiles = (int)cdiv(p.n, 16), sms = num_sms(), cols = p.tokens * p.terms;
+    auto share = [&](int s) { return (int)(cdiv(cdiv(p.chunks, s), kUnit) * kUnit); };
+    // the batches in flight, x, its powers of two, and the warps' sums
+    auto bytes = [&](int s) { return ring + (size_t)cols * (256 * share(s) + 64 + 128 * C::WARPS) + 32 * MB * share(s); };
+    constexpr size_t hold = std::max(16384, C::WARPS * 8 * MB * 64);         // sums that wait for a join: a block's at least
+    int s = 1;
+    while (s < 8 && bytes(s) + (s > 1 ? hold : 0) > kMostShared) ++s;
+    if (bytes(s) + (s > 1 ? hold : 0) > kMostShared) return 0;
+    // few tiles: more CTAs, as long as each of a CTA's warps has a batch
+    while (s < 8 && (long long)tiles * s * 2 <= sms && cdiv(p.chunks, s + 1) >= C::WARPS * C::BATCH) ++s;
+    p.per = share(s);
+    s = (int)cdiv(p.chunks, p.per);
+    // warps share a tile down to four batches each, or one where tiles are few
+    p.split = C::WARPS;
+    while (p.split > 1 && p.per < p.split * C::BATCH * ((long long)tiles * s > 2 * sms * (C::WARPS / p.split) ? 4 : 1)) p.split /= 2;
+    p.blocks = (int)cdiv(tiles, C::WARPS / p.split);
+    const int block = C::WARPS / p.split * cols * 64;
+    p.held = std::max(1, (int)hold / block);
+    smem = bytes(s) + (s > 1 ? (size_t)p.held * block : 0);
+    return s;
+}
+
+template <int MB, int GROUP>
+cudaError_t go(MatParams& p, cudaStream_t st)
+{
+    using C = Cfg<MB>;
     static std::atomic<unsigned long long> attr{0};
     cudaError_t e = smem_attr_once((const void*)q4_matmul_kernel<MB, GROUP>, kMostShared, attr);
     if (e != cudaSuccess) return e;
-    const int per_sm = std::min(MB == 1 ? 3 : MB == 2 ? 2 : 1, (int)(228 * 1024 / (smem + 1024)));
+    size_t smem = 0;
+    int shares = cut<MB, GROUP>(p, smem);
+    for (; !shares && p.tokens > 1; shares = cut<MB, GROUP>(p, smem)) --p.tokens;     // (fewer rows a pass)
+    if (!shares) return cudaErrorInvalidValue;
+    const int per_sm = std::min(C::CTAS, (int)(228 * 1024 / (smem + 1024)));
     const int clusters = std::min(p.blocks, std::max(1, per_sm * clusters_at_once(shares)));
     return launch_cluster("q4_matmul", q4_matmul_kernel<MB, GROUP>, dim3((unsigned)(clusters * shares), (unsigned)cdiv(p.m, p.tokens)),
-                          dim3(kThreads), shares, smem, st, p, shares);
+                          dim3(C::THREADS), shares, smem, st, p, shares);
 }
 
 template <int GROUP>
-cudaError_t pick(MatParams& p, int shares, size_t smem, cudaStream_t st)
+cudaError_t pick(MatParams& p, cudaStream_t st)
 {
     const int cols = p.tokens * p.terms;
-    // (the columns that `cut` reckoned with)
-    if (cols <= 8) return go<1, GROUP>(p, shares, smem, st);
-    if (cols <= 16) return go<2, GROUP>(p, shares, smem, st);
-    return go<4, GROUP>(p, shares, smem, st);
-}
-
-// How the work is cut, for p.m rows of p.chunks chunks: rows of x a pass, CTAs
-// that share the contraction (returned), warps that share a tile.
-int cut(MatParams& p, size_t& smem)
-{
-    const int tiles = (int)cdiv(p.n, 16), sms = num_sms();
-    p.tokens = std::min(p.m, 32 / p.terms);
-    const int wide = p.tokens * p.terms <= 8 ? 8 : p.tokens * p.terms <= 16 ? 16 : 32;      // columns of a pass's kernel
-    auto share = [&](int s) { return (int)(cdiv(cdiv(p.chunks, s), kBatch) * kBatch); };
-    // the batches in flight, x, its powers of two, the warps' sums (1 KB a column) and those that wait for a join (16 KB)
-    const size_t ring = (size_t)kWarps * kAhead * (p.group == 32 ? Batch<32>::BYTES : p.group == 64 ? Batch<64>::BYTES : Batch<128>::BYTES);
-    auto bytes = [&](int s) { return ring + (size_t)p.tokens * p.terms * (256 * share(s) + 64 + 1024) + 4 * wide * share(s) + 16384; };
-    while (p.tokens > 1 && bytes(8) > kMostShared) --p.tokens;
-    int s = 1;
-    while (s < 8 && bytes(s) > kMostShared) ++s;
-    // few tiles: more CTAs, as long as each of a CTA's warps has a batch
-    while (s < 8 && (long long)tiles * s * 2 <= sms && cdiv(p.chunks, s + 1) >= kWarps * kBatch) ++s;
-    p.per = share(s);
-    s = (int)cdiv(p.chunks, p.per);
-    // warps share a tile down to two batches each, or one where tiles are few
-    p.split = kWarps;
-    while (p.split > 1 && p.per < p.split * kBatch * (tiles * s > 2 * sms * (kWarps / p.split) ? 2 : 1)) p.split /= 2;
-    p.blocks = (int)cdiv(tiles, kWarps / p.split);
-    const int cols = p.tokens * p.terms, block = kWarps / p.split * cols * 64;
-    p.held = std::max(1, 16384 / block);
-    smem = ring + (size_t)cols * (256 * p.per + 64 + 1024) + (size_t)4 * wide * p.per + (s > 1 ? (size_t)p.held * block : 0);
-    return s;
+    if (cols <= 8) return go<1, GROUP>(p, st);
+    if (cols <= 16) return go<2, GROUP>(p, st);
+    return go<4, GROUP>(p, st);
 }
 
 }  // namespace
@@ -604,13 +628,10 @@ cudaError_t q4_matmul(const Q4MatArgs& a, cudaStream_t st)
     p.q = a.w.q; p.ldq = a.w.ldq;
     p.s = a.w.s; p.lds = a.w.lds;
     p.groups = (int)cdiv(p.k, a.w.group);
-    p.group = a.w.group;
     p.s_wide = (uintptr_t)a.w.s % 4 == 0 && a.w.lds % 2 == 0;
     p.y = a.y; p.ldy = a.ldy; p.y_f32 = a.ydt == DION_F32;
-    size_t smem = 0;
-    const int shares = cut(p, smem);
-    return a.w.group == 32 ? pick<32>(p, shares, smem, st) : a.w.group == 64 ? pick<64>(p, shares, smem, st)
-                                                                           : pick<128>(p, shares, smem, st);
+    p.tokens = std::min(p.m, 32 / p.terms);
+    return a.w.group == 32 ? pick<32>(p, st) : a.w.group == 64 ? pick<64>(p, st) : pick<128>(p, st);
 }
 
 }  // namespace dion
