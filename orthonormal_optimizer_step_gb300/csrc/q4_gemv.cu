@@ -42,7 +42,7 @@ constexpr int kUnit = 4;                     // shares of the contraction are mu
 // How a kernel of 8 MB columns is laid out.
 template <int MB>
 struct Cfg {
-    static constexpr int WARPS = 8, THREADS = 32 * WARPS;
+    static constexpr int WARPS = MB == 2 ? 12 : 8, THREADS = 32 * WARPS;
     static constexpr int CTAS = MB == 1 ? 2 : 1;                   // an SM
     static constexpr int BATCH = MB == 1 ? 4 : 2;                  // chunks that a warp copies together
     static constexpr int AHEAD = 2;          // batches in flight
@@ -54,7 +54,7 @@ struct MatParams {
     int m, n, k;
     int tokens, terms;                       // rows of x a pass, columns each of them takes
     int chunks, per;                         // of the contraction; a CTA's share of them
-    int split;                               // warps that share a tile (a power of two)
+    int split;                               // warps that share a tile
     int blocks, held;                        // blocks of warps / split tiles; those whose sums wait for a join
     dion_x_type xt;
     const void* x; long long ldx;
@@ -71,12 +71,12 @@ template <bool ADD>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     if (ADD)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -551,37 +551,62 @@ __global__ void __launch_bounds__(Cfg<MB>::THREADS, Cfg<MB>::CTAS) q4_matmul_ker
 int clusters_at_once(int shares)
 {
     constexpr int at_once[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-    return at_once[shares] * num_sms() / 152;
+    return std::max(1, at_once[shares] * num_sms() / 152);
 }
 
-// How the work is cut, for p.m rows of p.chunks chunks: rows of x a pass (fixed
-// before), CTAs that share the contraction (returned; 0: x does not fit), warps
-// that share a tile, and a CTA's shared memory.
+// CTAs an SM, for their shared memory.
+template <class C>
+int ctas_of(size_t bytes) { return std::min(C::CTAS, (int)(228 * 1024 / (bytes + 1024))); }
+
+// How the work is cut, for p.tokens rows a pass: CTAs that share the contraction
+// (returned; 0: x does not fit), warps that share a tile, and a CTA's shared
+// memory.  The cut with the least estimate of an SM's time is taken, in the time
+// that its warps need for a chunk each (about 0.2 us): its blocks one after the
+// other (one of two CTAs an SM that runs alone takes 1.3 of its time beside the
+// other, not half of two), whose warps work on whole batches and need two chunks'
+// time for a tile's end; x, 0.55 for a thread's unit of eight columns; a join, 7.
+// us with every number of warps that share a tile, from all down to one, and the
+// estimates:
+//   1 x 53248 x 16384 (g128)   79.9  76.3  84.2 106.3     405  393  405  438
+//   1 x  4096 x 14336          12.5  10.8  16.8  29.0      44   43   79  152
+//   1 x 53248 x  4096          25.9  24.1  24.2  29.7     134  115  110  114
+//   1 x 32768 x  1024          11.7   8.8   7.6   7.2      85   44   25   21
+//   16 x 4096 x 14336 (q8, 4 shares)  22.3 19.4 17.5 22.8  65   49   41   47
 template <int MB, int GROUP>
 int cut(MatParams& p, size_t& smem)
 {
     using C = Cfg<MB>;
     constexpr size_t ring = (size_t)C::WARPS * C::AHEAD * Batch<GROUP, C::BATCH>::BYTES;
-    const int tiles = (int)cdiv(p.n, 16), sms = num_sms(), cols = p.tokens * p.terms;
-    auto share = [&](int s) { return (int)(cdiv(cdiv(p.chunks, s), kUnit) * kUnit); };
-    // the batches in flight, x, its powers of two, and the warps' sums
-    auto bytes = [&](int s) { return ring + (size_t)cols * (256 * share(s) + 64 + 128 * C::WARPS) + 32 * MB * share(s); };
     constexpr size_t hold = std::max(16384, C::WARPS * 8 * MB * 64);         // sums that wait for a join: a block's at least
-    int s = 1;
-    while (s < 8 && bytes(s) + (s > 1 ? hold : 0) > kMostShared) ++s;
-    if (bytes(s) + (s > 1 ? hold : 0) > kMostShared) return 0;
-    // few tiles: more CTAs, as long as each of a CTA's warps has a batch
-    while (s < 8 && (long long)tiles * s * 2 <= sms && cdiv(p.chunks, s + 1) >= C::WARPS * C::BATCH) ++s;
-    p.per = share(s);
-    s = (int)cdiv(p.chunks, p.per);
-    // warps share a tile down to four batches each, or one where tiles are few
-    p.split = C::WARPS;
-    while (p.split > 1 && p.per < p.split * C::BATCH * ((long long)tiles * s > 2 * sms * (C::WARPS / p.split) ? 4 : 1)) p.split /= 2;
-    p.blocks = (int)cdiv(tiles, C::WARPS / p.split);
-    const int block = C::WARPS / p.split * cols * 64;
-    p.held = std::max(1, (int)hold / block);
-    smem = bytes(s) + (s > 1 ? (size_t)p.held * block : 0);
-    return s;
+    const int tiles = (int)cdiv(p.n, 16), cols = p.tokens * p.terms;
+    float least = 0.f;
+    int best = 0;
+    for (int s = 1; s <= 8 && (best == 0 || cdiv(p.chunks, s) >= C::BATCH); ++s) {
+        const int per = (int)(cdiv(cdiv(p.chunks, s), kUnit) * kUnit);
+        if (s > 1 && cdiv(p.chunks, per) != s) continue;           // (a share would be empty)
+        // the batches in flight, x, its powers of two, and the warps' sums
+        const size_t bytes = ring + (size_t)cols * (256 * per + 64 + 128 * C::WARPS) + 32 * MB * per + (s > 1 ? hold : 0);
+        if (bytes > kMostShared) continue;
+        const int at_once = clusters_at_once(s), per_sm = ctas_of<C>(bytes);
+        const float x = 0.55f * 16 / C::THREADS * p.tokens * per, join = s > 1 ? 7.f : 0.f;
+        for (int split = C::WARPS; split; split /= 2) {
+            const int blocks = (int)cdiv(tiles, C::WARPS / split), rest = blocks % (per_sm * at_once);
+            const float full = (float)(blocks / (per_sm * at_once) * per_sm);
+            const float rounds = full + (rest == 0 ? 0.f : rest > at_once ? 2.f : per_sm == 2 ? 1.3f : 1.f);
+            const float t = rounds * (float)(cdiv(per, split * C::BATCH) * C::BATCH + 2) + (blocks > at_once ? per_sm : 1) * x + join;
+            if (best && t >= least) continue;
+            least = t;
+            best = s;
+            p.per = per;
+            p.split = split;
+            p.blocks = blocks;
+            const int block = C::WARPS / split * cols * 64;
+            p.held = std::max(1, (int)hold / block);
+            smem = bytes;
+        }
+        if (best == s && (long long)tiles * C::BATCH > 8ll * C::WARPS * at_once) break;    // tiles enough: no more shares
+    }
+    return best;
 }
 
 template <int MB, int GROUP>
@@ -595,8 +620,7 @@ cudaError_t go(MatParams& p, cudaStream_t st)
     int shares = cut<MB, GROUP>(p, smem);
     for (; !shares && p.tokens > 1; shares = cut<MB, GROUP>(p, smem)) --p.tokens;     // (fewer rows a pass)
     if (!shares) return cudaErrorInvalidValue;
-    const int per_sm = std::min(C::CTAS, (int)(228 * 1024 / (smem + 1024)));
-    const int clusters = std::min(p.blocks, std::max(1, per_sm * clusters_at_once(shares)));
+    const int clusters = std::min(p.blocks, ctas_of<C>(smem) * clusters_at_once(shares));
     return launch_cluster("q4_matmul", q4_matmul_kernel<MB, GROUP>, dim3((unsigned)(clusters * shares), (unsigned)cdiv(p.m, p.tokens)),
                           dim3(C::THREADS), shares, smem, st, p, shares);
 }
