@@ -89,7 +89,9 @@ dion_status dion_grad_norm_workspace_size(int count, size_t* bytes);
  * skips).  Of the list, n, g and g_type are read.  Squares are float32 (a
  * gradient beyond 1.8e19 makes the norm infinite), their sums float64 from a
  * few hundred values on, in a fixed order (the same bits every time).
- * max_norm > 0 may be infinite.  workspace: 8-byte aligned.
+ * max_norm > 0 may be infinite.  workspace: 8-byte aligned; none is used, and
+ * it may be NULL, for up to 256 tensors of 2^20 values in all, each counted up to
+ * a multiple of 2048.
  */
 dion_status dion_grad_norm(int count, const dion_adamw_tensor* tensors, double max_norm, float* out, void* workspace,
                            size_t workspace_bytes, void* cuda_stream);

@@ -71,7 +71,13 @@ class GradList:
         self.device = None
         for i, g in enumerate(grads):
             self._gradient(i, g, g.numel())
-        self._workspace_bytes = None
+        self._workspace_bytes = self._needs()
+
+    def _needs(self):
+        """Workspace bytes of the norm: 0 where the library uses none (should its limit be lower, its answer says so)."""
+        if self.count <= 256 and sum(e.n + 2047 >> 11 for e in self.table) <= 512:
+            return 0
+        return dion_grad_norm_workspace_size(self.count)
 
     def _gradient(self, i, g, n):
         e = self.table[i]
@@ -236,15 +242,17 @@ def dion_grad_norm(grads, *, max_norm=math.inf, out=None, workspace=None, stream
         if out.dtype is not _F32 or out.shape != (2,) or not out.is_contiguous():
             raise ValueError("out must be a contiguous float32 tensor of 2")
         _same_device(dev, out=out)
-    if workspace is None:
-        nbytes = grads._workspace_bytes
-        if nbytes is None:
-            nbytes = grads._workspace_bytes = dion_grad_norm_workspace_size(grads.count)
-        workspace = empty((nbytes,), dtype=torch.uint8, device=device)
-    else:
+    wsptr, nbytes = None, grads._workspace_bytes
+    if workspace is not None:
         _same_device(dev, workspace=workspace)
-        nbytes = workspace.numel() * workspace.element_size()
-    code = _od.lib().dion_grad_norm(grads.count, table, max_norm, out.data_ptr(), workspace.data_ptr(), nbytes, _raw_stream(dev))
+        wsptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif nbytes:
+        workspace = empty((nbytes,), dtype=torch.uint8, device=device)
+        wsptr = workspace.data_ptr()
+    code = _od.lib().dion_grad_norm(grads.count, table, max_norm, out.data_ptr(), wsptr, nbytes, _raw_stream(dev))
+    if code == _od.DION_ERR_WORKSPACE and workspace is None:
+        grads._workspace_bytes = dion_grad_norm_workspace_size(grads.count)
+        return dion_grad_norm(grads, max_norm=max_norm, out=out)
     if code:
         _od._check(code, "dion_grad_norm")
     return out

@@ -557,16 +557,11 @@ __device__ __forceinline__ float squares(const T* g)
     return (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
 }
 
+// Sum of the squares of chunks `chunk` .. `end` - 1, in thread 0.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
-    grad_norm_kernel(const __grid_constant__ Table<CAP> t, double* part)
+__device__ __forceinline__ double sum_squares(const Table<CAP>& t, uint32_t chunk, uint32_t end, double (&sums)[kThreads / 32])
 {
     constexpr int N = 4;                             // chunks of float32 in flight, twice as many of bfloat16
-    __shared__ double sums[kThreads / 32];
-    wait_previous();
-    allow_next();
-    uint32_t chunk = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
-    const uint32_t end = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
     double sum = 0;                                  // of 64 float32 squares at a time
     for (int i = tensor_of(t, chunk); chunk < end; ++i) {
         const Entry& e = t.e[i];
@@ -602,10 +597,28 @@ __global__ void __launch_bounds__(kThreads)
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0)
         for (int w = 1; w < kThreads / 32; ++w) sum += sums[w];
-        part[blockIdx.x] = sum;
-    }
+    return sum;
+}
+
+__device__ __forceinline__ void write_norm(double sum, double max_norm, float* out)
+{
+    const double norm = sqrt(sum);
+    out[0] = (float)norm;
+    out[1] = isfinite(norm) ? (float)fmin(1.0, max_norm / (norm + 1e-6)) : __int_as_float(0x7fffffff);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ Table<CAP> t, double* part)
+{
+    __shared__ double sums[kThreads / 32];
+    wait_previous();
+    allow_next();
+    const double sum = sum_squares(t, (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x),
+                                   (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x), sums);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* part, int parts, double max_norm, float* out)
@@ -621,11 +634,97 @@ __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* 
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < kThreads / 32; ++w) sum += sums[w];
-        const double norm = sqrt(sum);
-        out[0] = (float)norm;
-        out[1] = isfinite(norm) ? (float)fmin(1.0, max_norm / (norm + 1e-6)) : __int_as_float(0x7fffffff);
+        write_norm(sum, max_norm, out);
     }
 }
+
+// Few values: one cluster's CTAs, joined through distributed shared memory, so
+// that a call is one launch and has no workspace.  Lists of few values have many
+// small tensors, so 256 threads take single chunks, four of them together, whose
+// tensors are told by a table.
+constexpr int kCluster = 8, kFewThreads = 1024, kFewChunks = 512, kMedium = 256;
+struct TensorOf {
+    uint16_t chunk[kFewChunks];
+};
+template <int CAP>
+__global__ void __launch_bounds__(kFewThreads)
+    grad_norm_small_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ TensorOf of, const double max_norm, float* out)
+{
+    constexpr uint32_t GROUPS = kCluster * kFewThreads / kThreads, N = 4;
+    __shared__ double sums[kFewThreads / 32];
+    __shared__ double mine;
+    wait_previous();
+    allow_next();
+    double sum = 0;
+    for (uint32_t c = blockIdx.x * (kFewThreads / kThreads) + threadIdx.x / kThreads; c < t.chunks; c += N * GROUPS) {
+        // 16-byte words first, as they are (anything done to one would wait for it before the next is asked for);
+        // of a chunk without them, its squares
+        uint4 raw[N][2];
+        bool half[N];
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (uint32_t u = 0; u < N; ++u) {
+            const uint32_t chunk = c + u * GROUPS;
+            const int i = of.chunk[min(chunk, (uint32_t)kFewChunks - 1)];
+            const Entry& e = t.e[i];
+            const long long at = ((long long)chunk - t.first[i]) * kChunk + threadIdx.x % kThreads * kPer;
+            const int k = chunk < t.chunks ? (int)max(0ll, min(e.n - at, 8ll)) : 0;
+            raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+            half[u] = e.flags & kGradBf16;
+            if (k == 8 && (e.flags & kWide)) {
+                const uint4* w = (const uint4*)((const uint8_t*)e.g + at * (half[u] ? 2 : 4));
+                raw[u][0] = w[0];
+                if (!half[u]) raw[u][1] = w[1];
+            } else if (k > 0) {
+                float2 g[4];
+                if (half[u]) load_values((const bf16*)e.g + at, false, k, g);
+                else load_values((const float*)e.g + at, false, k, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc = fma2(g[j], g[j], acc);
+            }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < N; ++u) {
+            float2 g[4];
+            if (half[u]) {
+                Raw8<bf16> r;
+                r.u[0] = raw[u][0];
+                unpack8(r, g);
+            } else {
+                Raw8<float> r;
+                r.u[0] = raw[u][0];
+                r.u[1] = raw[u][1];
+                unpack8(r, g);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc = fma2(g[j], g[j], acc);
+        }
+        sum += (double)(acc.x + acc.y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        sum = sums[threadIdx.x];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (threadIdx.x == 0) mine = sum;
+    }
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        for (int r = 1; r < kCluster; ++r) {
+            uint32_t a;
+            double v;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(&mine)), "r"(r));
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
+            sum += v;
+        }
+        write_norm(sum, max_norm, out);
+    }
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");      // its sums have been read
+}
+static_assert(kFewThreads == 32 * 32, "one warp joins a CTA's warps");
 
 // ---------------------------------------------------------------------- host
 size_t bytes_of(dion_dtype t) { return t == DION_F32 ? 4 : 2; }
@@ -742,6 +841,33 @@ int norm_ctas() { return 6 * num_sms(); }
 // tensor of kMostValues has 2^27, so one takes 15 at least).
 long long norm_launches(int count) { return cdiv(count, kLarge) + cdiv(count, 15); }
 
+// Lists whose norm is one launch without a workspace: 867000 float32 values in 63
+// tensors take 11 us on the GPU so and 7 in two launches, but a call, host
+// included, takes 11 against 16.
+bool few_values(int count, const dion_adamw_tensor* tensors)
+{
+    if (count > kMedium) return false;
+    long long chunks = 0;
+    for (int i = 0; i < count && chunks <= kFewChunks; ++i) chunks += cdiv(tensors[i].n, kChunk);
+    return chunks <= kFewChunks;
+}
+template <int CAP>
+cudaError_t norm_few(int count, const dion_adamw_tensor* tensors, double max_norm, float* out, cudaStream_t st)
+{
+    Table<CAP> t;
+    TensorOf of;
+    fill(t, 0, count, tensors, false);
+    for (int i = 0; i < t.count; ++i)
+        for (uint32_t c = t.first[i]; c < (i + 1 < t.count ? t.first[i + 1] : t.chunks); ++c) of.chunk[c] = (uint16_t)i;
+    for (uint32_t c = t.chunks; c < kFewChunks; ++c) of.chunk[c] = 0;
+    if (t.count == 0) {                              // (an entry is read for chunks that do not exist as well)
+        t.first[0] = 0;
+        t.e[0] = Entry{};
+    }
+    return launch_cluster("grad_norm_small", grad_norm_small_kernel<CAP>, dim3(kCluster), dim3(kFewThreads), kCluster, 0, st, t, of,
+                          max_norm, out);
+}
+
 bool hyper_ok(double lr, double b1, double b2, double eps, double wd)
 {
     return std::isfinite(lr) && std::isfinite(wd) && std::isfinite(eps) && eps >= 0 && b1 >= 0 && b1 < 1 && b2 >= 0 && b2 < 1;
@@ -790,6 +916,11 @@ extern "C" dion_status dion_grad_norm(int count, const dion_adamw_tensor* tensor
     const dion_status ok = list_ok(count, tensors, false);
     if (ok != DION_OK) return ok;
     if (!(max_norm > 0) || !at_least(out, 4)) return DION_ERR_INVALID_ARG;
+    if (few_values(count, tensors)) {
+        const cudaStream_t s = (cudaStream_t)cuda_stream;
+        DION_TRY(count <= kSmall ? norm_few<kSmall>(count, tensors, max_norm, out, s) : norm_few<kMedium>(count, tensors, max_norm, out, s));
+        return DION_OK;
+    }
     size_t need = 0;
     dion_grad_norm_workspace_size(count, &need);
     if (need && (!at_least(workspace, 8) || workspace_bytes < need)) return DION_ERR_WORKSPACE;

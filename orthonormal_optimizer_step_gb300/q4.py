@@ -19,10 +19,10 @@ import torch
 from torch import empty
 
 import orthonormal_optimizer_step_gb300 as _od
-from orthonormal_optimizer_step_gb300.q8 import (Q8, _cuda, _matrix, _pitch, _q8, _raw_stream, _same_device, _type,
+from orthonormal_optimizer_step_gb300.q8 import (_TYPES, Q8, _cuda, _matrix, _pitch, _q8, _raw_stream, _same_device, _type,
                                                  _underived)
 
-_BF16 = torch.bfloat16
+_BF16, _U8 = torch.bfloat16, torch.uint8
 _GROUPS = (32, 64, 128)
 
 
@@ -48,9 +48,14 @@ def new_q4(rows, cols, *, group=128, device="cuda"):
 def _q4(w, what):
     """(rows, cols, group, data pointer, pitch, scale pointer, pitch) of a 4-bit matrix."""
     data, scale, cols, group = w
+    if data.dim() == 2 == scale.dim() and group in _GROUPS:       # all at once; what fails is found out below
+        (rows, width), (sr, sc), (ldq, one), (lds, sone), qptr = data.shape, scale.shape, data.stride(), scale.stride(), data.data_ptr()
+        if (one == 1 == sone and sr == rows and width == (cols + 127 >> 7) * 64 and sc * group - cols < group and sc * group >= cols > 0
+                and ldq >= width and lds >= sc and not (ldq | qptr) & 15 and data.dtype is _U8 and scale.dtype is _BF16):
+            return rows, cols, group, qptr, ldq, scale.data_ptr(), lds
     if group not in _GROUPS:
         raise ValueError(f"{what}: group must be 32, 64 or 128, got {group!r}")
-    if data.dtype is not torch.uint8 or scale.dtype is not _BF16:
+    if data.dtype is not _U8 or scale.dtype is not _BF16:
         raise TypeError(f"{what}: data must be uint8 and scales bfloat16, got {data.dtype} and {scale.dtype}")
     if data.dim() != 2 or scale.dim() != 2 or cols < 0:
         raise ValueError(f"{what}: expected [rows, bytes] data and [rows, groups] scales")
@@ -128,27 +133,38 @@ def dion_q4_matmul(x, w, *, out=None, out_dtype=_BF16, stream=None):
         if data.dim() != 2 or (square and m > 1):
             raise ValueError("x must be an 8-bit [rows, cols] matrix with a scale for each 128 values of a row")
         xt += 2
-        lead = (m,)
+        shape = m, n
     else:
-        data, scale = x, None
-        x2, ldx = _matrix(x, "x")
-        (m, k), lead = x2.shape, x.shape[:-1]
-        xt, xptr, sxptr, ldsx = _type(x.dtype, "x"), x2.data_ptr(), None, 0
+        data, scale, sxptr, ldsx, xt = x, None, None, 0, _TYPES.get(x.dtype)
+        if xt is None:
+            _type(x.dtype, "x")
+        if x.dim() == 2:
+            (m, k), (ldx, one) = x.shape, x.stride()
+            if one != 1 or ldx < k:
+                ldx = _pitch(m, k, ldx, one, "x")
+            shape, xptr = (m, n), x.data_ptr()
+        else:
+            x2, ldx = _matrix(x, "x")
+            (m, k), shape, xptr = x2.shape, (*x.shape[:-1], n), x2.data_ptr()
     if k != cols:
         raise ValueError(f"x has {k} columns, w {cols}")
     dev, given = _cuda(data, "x"), out
     if out is None:
-        yt, ldy = _type(out_dtype, "out_dtype"), n
-        out = empty((*lead, n), dtype=out_dtype, device=data.device)
+        yt, ldy = _TYPES.get(out_dtype), n
+        if yt is None:
+            _type(out_dtype, "out_dtype")
+        out = empty(shape, dtype=out_dtype, device=data.device)
         yptr = out.data_ptr()
     else:
-        if out.shape != (*lead, n):
-            raise ValueError(f"out must be {(*lead, n)}, got {tuple(out.shape)}")
+        if out.shape != shape:
+            raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
         yt = _type(out.dtype, "out")
         y2, ldy = _matrix(out, "out")
         yptr = y2.data_ptr()
-    if not dev == w[0].get_device() == w[1].get_device() == out.get_device() or scale is not None and scale.get_device() != dev:
-        _same_device(dev, w=w.data, w_scale=w.scale, out=out, x_scale=scale)
+        if out.get_device() != dev:
+            _same_device(dev, out=out)
+    if not dev == w[0].get_device() == w[1].get_device() or scale is not None and scale.get_device() != dev:
+        _same_device(dev, w=w.data, w_scale=w.scale, x_scale=scale)
     code = _od.lib().dion_q4_matmul(m, n, k, xt, xptr, ldx, sxptr, ldsx, group, qptr, ldq, sptr, lds, yt, yptr, ldy,
                                     _raw_stream(dev))
     if code:

@@ -269,7 +269,7 @@ def test_more_values_than_32_bits_count():
 # ------------------------------------------------------------------- norm
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("offset", [0, 1])
-@pytest.mark.parametrize("sizes", [[1], [5, 0, 2048], SIZES, [40] * 900, [3_000_001]])
+@pytest.mark.parametrize("sizes", [[1], [5, 0, 2048], SIZES, [40] * 256, [40] * 383, [40] * 900, [1 << 20], [(1 << 20) + 1], [3_000_001]])
 def test_norm(dtype, offset, sizes):
     """Squares and at most 32 sums of them in float32 (rounded the same way at worst): 33 half steps of the sum, half of that of its root."""
     grads = make(sizes, g=dtype, offset=offset)[1]
@@ -293,13 +293,16 @@ def test_norm_of_nothing_and_of_what_is_not_finite():
 def test_norm_into_given_memory_and_refusals():
     g = [torch.randn(1000, device="cuda")]
     grads = od.dion_grad_list(g)
+    large = od.dion_grad_list([torch.randn(1 << 21, device="cuda")])
     out, ws = torch.empty(2, device="cuda"), torch.empty(od.dion_grad_norm_workspace_size(1), dtype=torch.uint8, device="cuda")
     assert od.dion_grad_norm(grads, out=out, workspace=ws) is out
     assert torch.equal(out, od.dion_grad_norm(grads))
     with pytest.raises(ValueError, match="out"):
         od.dion_grad_norm(grads, out=torch.empty(3, device="cuda"))
     with pytest.raises(od.DionError):
-        od.dion_grad_norm(grads, workspace=ws[:8])
+        od.dion_grad_norm(large, workspace=ws[:8])
+    assert torch.equal(od.dion_grad_norm(large, workspace=torch.empty(od.dion_grad_norm_workspace_size(1), dtype=torch.uint8, device="cuda")),
+                       od.dion_grad_norm(large))
     with pytest.raises(od.DionError):
         od.dion_grad_norm(grads, max_norm=0.0)
 
