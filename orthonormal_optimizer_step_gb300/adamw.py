@@ -13,7 +13,9 @@ one when a call uses it.
     dion_adamw_step(plan, step=t, lr=1e-3, weight_decay=0.1, grad_scale=norm[1:])
 
 Parameters are updated in place, behind autograd's back: a plan's tensors carry
-no record of it, and a graph that holds an old value is not warned.
+no record of it, and a graph that holds an old value is not warned.  A plan goes
+with the memory that its tensors had when it was made, and keeps that memory: a
+parameter that is given other memory later (p.data = ...) needs a new plan.
 """
 from __future__ import annotations
 
@@ -67,7 +69,9 @@ class GradList:
         grads = list(grads)
         self.count = len(grads)
         self.table = (_Tensor * self.count)()
-        self.tensors = [grads]                     # kept alive, and nothing else
+        # the memory that the table points to is kept alive, and nothing else: aliases, since a tensor that a program
+        # gives other memory (p.data = ...) would let go of it
+        self.tensors = [[g.detach() for g in grads]]
         self.device = None
         for i, g in enumerate(grads):
             self._gradient(i, g, g.numel())
@@ -112,7 +116,9 @@ class AdamWPlan(GradList):
             if g.shape != p.shape:
                 raise ValueError(f"gradient {i} must have its parameter's shape")
         super().__init__(grads)
-        self.tensors += [params, first, second, copies]
+        self.tensors += [[t.detach() for t in params], *([State8(*(x.detach() for x in t)) if isinstance(t, State8) else t.detach()
+                                                          for t in moments] for moments in (first, second)),
+                         [t if t is None else t.detach() for t in copies]]
         written = []
         for i in range(count):
             p, m, v, c, e = params[i], first[i], second[i], copies[i], self.table[i]
@@ -182,7 +188,7 @@ class AdamWPlan(GradList):
                 pass
             self.tensors[0] = old
             raise
-        self.tensors[0] = grads
+        self.tensors[0] = [g.detach() for g in grads]
 
 
 def dion_grad_list(grads):

@@ -157,6 +157,24 @@ def test_plan_refuses_shared_memory(on_cpu):
     plan(p + [torch.zeros(4)], g + [g[0][:4]], m + [torch.zeros(4)], v + [torch.zeros(4)])   # gradients may be shared
 
 
+def test_plan_keeps_the_memory_that_it_writes(on_cpu):
+    """A tensor that is given other memory lets go of what the plan's table points to; the plan does not."""
+    p, g, m, v = parts(bits=8)
+    plan = od.dion_adamw_plan(p, g, m, v, copies=[torch.zeros(300, dtype=torch.bfloat16)])
+    later = [torch.zeros(300)]
+    for t in (p[0], g[0], m[0].data, m[0].scale, v[0].data, v[0].scale):
+        t.data = torch.ones_like(t)
+    e, (kept_g, kept_p, kept_m, kept_v, kept_c) = plan.table[0], [x[0] for x in plan.tensors]
+    assert (e.p, e.g, e.copy) == (kept_p.data_ptr(), kept_g.data_ptr(), kept_c.data_ptr())
+    assert (e.m, e.m_scale, e.v, e.v_scale) == (kept_m.data.data_ptr(), kept_m.scale.data_ptr(), kept_v.data.data_ptr(), kept_v.scale.data_ptr())
+    plan.set_gradients(later)
+    later[0].data = torch.ones(300)
+    assert e.g == plan.tensors[0][0].data_ptr() != later[0].data_ptr()
+    listed = od.dion_grad_list(later)
+    later[0].data = torch.zeros(300)
+    assert listed.table[0].g == listed.tensors[0][0].data_ptr() != later[0].data_ptr()
+
+
 def test_gradients_on_the_cpu_are_refused():
     with pytest.raises(ValueError, match="CUDA"):
         od.dion_grad_list([torch.zeros(4)])
