@@ -253,13 +253,14 @@ __device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b, uint32_t c) { r
 // on s = v / sqrt(v) with the residual v - s^2 formed exactly, from a reciprocal
 // root within 2^-22.  The result is off the real root by 2^-43 of it before its one
 // rounding, so it is the nearest float32 but for a few v in a million (whose root
-// lies that close to half-way between two).  A third of the instructions of the
-// function that has no such exceptions.
+// lies that close to half-way between two).  Below 2^-103 or so the residual is
+// rounded to float32's least distance, which takes it to s itself at worst, within
+// 2^-22.  A third of the instructions of the function that has no such exceptions.
 __device__ __forceinline__ float2 roots(float2 v)
 {
     float2 y;                                        // (of zero: finite, and the product with it zero)
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1e-38f)));
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1e-38f)));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 0x1p-149f)));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 0x1p-149f)));
     const float2 s = mul2(v, y);
     const float2 residual = fma2(make_float2(-s.x, -s.y), s, v);
     return fma2(residual, mul2(y, make_float2(0.5f, 0.5f)), s);

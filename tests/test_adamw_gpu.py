@@ -161,6 +161,19 @@ def test_no_root_above_zero_becomes_zero():
     assert not second[0].data.view(torch.uint8).any() and not z[0].any()
 
 
+def test_roots_of_subnormal_second_moments():
+    """Gradients of 3e-20 to 1e-17: second moments around and below float32's least normal number, 1.2e-38.
+
+    A v of 9e-43 or more is right to half of 2^-149, 8e-4 of it, and its root to half of that,
+    as is the block's largest; rounding up or down moves a value by less than a step, 2^-3 of it."""
+    g = torch.logspace(math.log10(3e-20), -17, 1 << 14, device="cuda")         # a block's values differ by 1.1 at most
+    p = [torch.zeros_like(g)]
+    first, second = od.dion_adamw_state(p, bits=8)
+    od.dion_adamw_step(od.dion_adamw_plan(p, [g], first, second), step=1, lr=1e-3)
+    want = math.sqrt(1e-3) * g.double()
+    assert torch.all((ref.values(second[0], g.numel()) - want).abs() <= (2.0 ** -3 + 2.0 ** -10) * want)
+
+
 def test_roots_follow_a_change_that_is_smaller_than_a_step():
     """With gradients of a tenth, r falls by 0.05 % a step; rounded to nearest it would stay where it was.
 
