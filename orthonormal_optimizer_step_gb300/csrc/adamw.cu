@@ -9,6 +9,7 @@
 // magnitude is one reduction over the warp.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "q8.cuh"
 #include "../../include/dion_adamw.h"
@@ -24,7 +25,7 @@ using namespace q8;
 constexpr int kThreads = 256, kPer = 8, kChunk = kThreads * kPer;
 static_assert(32 * kPer == DION_ADAMW_BLOCK, "a warp holds one block of an 8-bit state");
 
-enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kWide = 8 };   // kWide: 16-byte accesses
+enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kWide = 8, kWhole = 16 };   // 16-byte accesses; float32 values in 32 bytes
 
 struct Entry {
     void* p;
@@ -111,9 +112,13 @@ __device__ __forceinline__ void load_values(const T* p, bool wide, int k, float2
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_values(T* p, bool wide, int k, const float2 (&f)[4])
+__device__ __forceinline__ void store_values(T* p, bool wide, int k, const float2 (&f)[4], bool whole = false)
 {
-    if (wide && k >= 8) {
+    if (sizeof(T) == 4 && whole && k >= 8) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0].x), "f"(f[0].y), "f"(f[1].x),
+                     "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
+                     : "memory");
+    } else if (wide && k >= 8) {
         Raw8<T> r;
         pack8(r, f);
 #pragma unroll
@@ -169,15 +174,21 @@ __device__ __forceinline__ void e4m3_values(uint2 b, float scale, float2 (&f)[4]
     f[3] = mul2(e4m3_pair(b.y >> 16), s);
 }
 
-// A block's scale from its largest finite magnitude.  The division is a
-// product with the reciprocal of 448 and Markstein's correction, whose
-// remainder is exact, so that the quotient is rounded once; below 2^-100 only
-// the bound counts.
-__device__ __forceinline__ float block_scale(float amax)
+// The scales of a block's two states from their largest finite magnitudes, and the
+// scales' reciprocals.  The division is a product with the reciprocal of 448 and
+// Markstein's correction, whose remainder is exact, so that the quotient is rounded
+// once; below 2^-100 only the bound counts.  The reciprocal's correction is the
+// same, and rounds once but for a scale whose mantissa is all ones (a unit off).
+__device__ __forceinline__ void block_scales(float2 amax, float2& scale, float2& inverse)
 {
-    constexpr float inv = 1.f / 448.f;
-    const float q = __fmul_rn(amax, inv);
-    return fmaxf(__fmaf_rn(__fmaf_rn(-q, 448.f, amax), inv, q), 0x1p-100f);
+    const float2 by = make_float2(1.f / 448.f, 1.f / 448.f);
+    const float2 q = mul2(amax, by);
+    const float2 r = fma2(fma2(q, make_float2(-448.f, -448.f), amax), by, q);
+    scale = make_float2(fmaxf(r.x, 0x1p-100f), fmaxf(r.y, 0x1p-100f));
+    float2 y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(scale.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(scale.y));
+    inverse = fma2(fma2(make_float2(-scale.x, -scale.y), y, make_float2(1.f, 1.f)), y, y);
 }
 
 // Each element's dither, 20 bits, is the top of mix((at + j) ^ key) with at a
@@ -198,14 +209,18 @@ struct Dither {
     }
 };
 
-// E4M3 byte of x = r / scale >= 0 (finite), rounded up where the dither
+// E4M3 bytes of x = r / scale >= 0 (finite), rounded up where the dither
 // carries; 0 where an r above zero might have to be raised.  Times 2^-120 a
 // float's exponent is that of E4M3 (biases 127 and 7), its subnormals being
 // among the float's, and the 20 mantissa bits below E4M3's three are the place
-// between two values.  (x may exceed 448 by a rounding.)
-__device__ __forceinline__ uint32_t dithered(float x, uint32_t dither)
+// between two values.  x may exceed 448 by a rounding and is held to 448's code,
+// 126.  Four values are 7 instructions beside the additions: upper halves in
+// pairs, their minima, and the bytes at bit 4 of each.
+__device__ __forceinline__ uint32_t dithered4(float2 a, float2 b, const Dither& dither, int j)
 {
-    return min((__float_as_uint(x) + dither) >> 20, 126u);
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x) + dither(j), __float_as_uint(a.y) + dither(j + 1), 0x7632);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x) + dither(j + 2), __float_as_uint(b.y) + dither(j + 3), 0x7632);
+    return __byte_perm(__vminu2(lo, 0x07ef07efu) >> 4, __vminu2(hi, 0x07ef07efu) >> 4, 0x6420);
 }
 
 // What a thread holds of a chunk: eight values of each, of which k exist (the
@@ -232,13 +247,14 @@ __device__ __forceinline__ void moments(Values& x, const Constants& c, float f)
     }
 }
 
-// The parameters after the step, for r = sqrt(v).  The quotient is within two
+// The parameters after the step, for r = sqrt(v) times a power of two and root
+// divided by it.  The quotient is within two
 // units of the last place: an update is a thousandth of the parameter or less.
-__device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], const Constants& c, float rate, float keep)
+__device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], float root, float eps, float rate, float keep)
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 d = fma2(r[j], make_float2(c.root, c.root), make_float2(c.eps, c.eps));
+        const float2 d = fma2(r[j], make_float2(root, root), make_float2(eps, eps));
         float2 i;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.x) : "f"(d.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.y) : "f"(d.y));
@@ -249,24 +265,27 @@ __device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], cons
 
 __device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b, uint32_t c) { return max(max(a, b), c); }
 
-// Square roots of v >= 0, finite, and one more of the warp's largest: Newton's step
-// on s = v / sqrt(v) with the residual v - s^2 formed exactly, from a reciprocal
-// root within 2^-22.  The result is off the real root by 2^-43 of it before its one
-// rounding, so it is the nearest float32 but for a few v in a million (whose root
-// lies that close to half-way between two).  Below 2^-103 or so the residual is
-// rounded to float32's least distance, which takes it to s itself at worst, within
-// 2^-22.  A third of the instructions of the function that has no such exceptions.
+// 2^32 sqrt(v) for 0 <= v < 2^63: Newton's step on s = w / sqrt(w), w = 2^64 v, with
+// the residual w - s^2 formed exactly, from a reciprocal root within 2^-22.  The
+// result is off the real root by 2^-43 of it before its one rounding, so it is the
+// nearest float32 but for a few v in a million (whose root lies that close to
+// half-way between two).  A third of the instructions of the function that has no
+// such exceptions; w is a normal number for subnormal v too, which the reciprocal
+// root would need three more for.
+constexpr float kRootScale = 0x1p32f;
+constexpr uint32_t kRootBits = 0x5f000000;           // of 2^63
 __device__ __forceinline__ float2 roots(float2 v)
 {
+    const float2 w = mul2(v, make_float2(0x1p64f, 0x1p64f));
     float2 y;                                        // (of zero: finite, and the product with it zero)
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 0x1p-149f)));
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 0x1p-149f)));
-    const float2 s = mul2(v, y);
-    const float2 residual = fma2(make_float2(-s.x, -s.y), s, v);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(w.x, 0x1p-90f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(w.y, 0x1p-90f)));
+    const float2 s = mul2(w, y);
+    const float2 residual = fma2(make_float2(-s.x, -s.y), s, w);
     return fma2(residual, mul2(y, make_float2(0.5f, 0.5f)), s);
 }
 
-// The roots r of second moments v, and the 8-bit states of a warp's block of 256.
+// The roots of second moments v, times kRootScale, and the 8-bit states of a warp's block of 256.
 __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4], float2 (&r)[4], const Dither& dither, float& ms,
                                        float& rs, uint32_t (&mw)[2], uint32_t (&rw)[2])
 {
@@ -281,8 +300,8 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4
     uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(mmax));
     vmax = __reduce_max_sync(0xffffffffu, vmax);
     float rmax;
-    const bool finite = mbits < kInfBits && vmax < kInfBits;       // the same in all lanes
-    if (finite) {
+    const bool plain = mbits < kInfBits && vmax < kRootBits;       // the same in all lanes
+    if (plain) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[j] = roots(v[j]);
         rmax = roots(make_float2(__uint_as_float(vmax), 0.f)).x;
@@ -290,41 +309,40 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4
         uint32_t rbits = mbits = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            r[j] = make_float2(__fsqrt_rn(v[j].x), __fsqrt_rn(v[j].y));
+            r[j] = make_float2(__fsqrt_rn(v[j].x) * kRootScale, __fsqrt_rn(v[j].y) * kRootScale);
             mbits = max3(mbits, finite_mag_bits(m[j].x), finite_mag_bits(m[j].y));
             rbits = max3(rbits, finite_mag_bits(r[j].x), finite_mag_bits(r[j].y));
         }
         mbits = __reduce_max_sync(0xffffffffu, mbits);
         rmax = __uint_as_float(__reduce_max_sync(0xffffffffu, rbits));
     }
-    ms = block_scale(__uint_as_float(mbits));
-    rs = block_scale(rmax);
-    const float mi = __frcp_rn(ms), ri = __frcp_rn(rs);
-    uint32_t code[8], least = 0xffffffffu;
+    float2 scale, inverse;
+    block_scales(make_float2(__uint_as_float(mbits), rmax * (1.f / kRootScale)), scale, inverse);
+    ms = scale.x;
+    rs = scale.y;
+    const float mi = inverse.x, ri = inverse.y * (1.f / kRootScale);
+    uint32_t least = 0xffffffffu;
     float2 x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 y = mul2(m[j], make_float2(mi, mi));
-        const uint32_t w = finite ? cvt2<DION_E4M3>(y.x, y.y) : cvt2<DION_E4M3>(inf_to_nan(y.x), inf_to_nan(y.y));
+        const uint32_t w = plain ? cvt2<DION_E4M3>(y.x, y.y) : cvt2<DION_E4M3>(inf_to_nan(y.x), inf_to_nan(y.y));
         mw[j >> 1] = j & 1 ? mw[j >> 1] | (w << 16) : w;
         x[j] = mul2(mul2(r[j], make_float2(ri, ri)), make_float2(0x1p-120f, 0x1p-120f));
-        code[2 * j] = dithered(x[j].x, dither(2 * j));
-        code[2 * j + 1] = dithered(x[j].y, dither(2 * j + 1));
         least = min(min(least, __float_as_uint(x[j].x)), __float_as_uint(x[j].y));
     }
+    rw[0] = dithered4(x[0], x[1], dither, 0);
+    rw[1] = dithered4(x[2], x[3], dither, 4);
     if (least < 1u << 20) {                          // below E4M3's least value, 2^-9: may have become zero
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if ((j & 1 ? r[j >> 1].y : r[j >> 1].x) > 0.f) code[j] = max(code[j], 1u);
+            if ((j & 1 ? r[j >> 1].y : r[j >> 1].x) > 0.f && !(rw[j >> 2] >> (8 * (j & 3)) & 0xffu)) rw[j >> 2] |= 1u << (8 * (j & 3));
     }
-    if (!finite) {
+    if (!plain) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (mag_bits(j & 1 ? r[j >> 1].y : r[j >> 1].x) >= kInfBits) code[j] = 0x7fu;
+            if (mag_bits(j & 1 ? r[j >> 1].y : r[j >> 1].x) >= kInfBits) rw[j >> 2] |= 0x7fu << (8 * (j & 3));
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        rw[i] = (code[4 * i] + code[4 * i + 1] * 256u) + (code[4 * i + 2] + code[4 * i + 3] * 256u) * 65536u;
 }
 
 // A step with 8-bit states on what a thread holds; encodes them into mw and rw, with the block's new scales in ms and rs.
@@ -338,18 +356,32 @@ __device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, 
     for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
     moments(x, c, f);
     encode(x.m, x.v, r, dither, ms, rs, mw, rw);
-    parameters(x, r, c, rate, keep);
+    parameters(x, r, c.root * (1.f / kRootScale), c.eps, rate, keep);
 }
 
-// Whole chunks of an 8-bit tensor with aligned addresses come through shared
-// memory, each warp copying what it will read itself, 16 bytes a lane side by side,
-// so that two chunks are in flight and no register waits for them.  The instructions around a chunk's eight values a thread count (81 a value
-// with the general loop's branches and addresses took 655 us for the listed 262
-// million values), so types are fixed and addresses are kept.
+// A step with float32 states.
+__device__ __forceinline__ void step32(Values& x, const Constants& c, float f, float rate, float keep)
+{
+    float2 r[4];
+    moments(x, c, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
+    }
+    parameters(x, r, c.root, c.eps, rate, keep);
+}
+
+// Whole chunks of a tensor with aligned addresses come through shared memory, each
+// warp copying what it will read itself, 16 bytes a lane side by side, so that two
+// chunks are in flight and no register waits for them.  The instructions around a
+// chunk's eight values a thread count (81 a value with the general loop's branches
+// and addresses took 655 us for 262 million bfloat16 values with 8-bit states), so
+// types are fixed and addresses are kept.
 constexpr int kAhead = 2;
 struct Stage {
     uint4 value[2][2 * kThreads];                    // [p | g] in the memory's order, a warp's 1 KB (512 bytes) together
-    uint2 state[2][kThreads];                        // [m | r][thread]
+    uint4 state[2][2 * kThreads];                    // [m | v] likewise (8-bit: 256 bytes a warp)
     float scale[2][kThreads / 32];                   // [m | r][warp]
 };
 template <int BYTES>
@@ -359,33 +391,51 @@ __device__ __forceinline__ void copy_async(void* to, const void* from)
     if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(from), "n"(BYTES) : "memory");
 }
-template <typename P, typename G>
-__device__ __forceinline__ void whole_chunks8(const Entry& e, long long at, int chunks, long long step, const Constants& c, float f, float rate,
-                                              float keep, uint32_t key, Stage (&stages)[kAhead])
+// A lane's eight values' words of a warp's, copied side by side: word i of lane l is word 32 i + l there.
+template <int W>
+__device__ __forceinline__ void fetch_words(uint4* to, const uint4* from)
 {
+#pragma unroll
+    for (int i = 0; i < W; ++i) copy_async<16>(to + 32 * i, from + 32 * i);
+}
+template <typename T>
+__device__ __forceinline__ void read_words(const uint4* from, float2 (&f)[4])
+{
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = from[i];
+    unpack8(r, f);
+}
+template <typename P, typename G, bool EIGHT>
+__device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int chunks, long long step, const Constants& c, float f, float rate,
+                                             float keep, uint32_t key, Stage* stages)
+{
+    using S = typename std::conditional<EIGHT, uint8_t, float>::type;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     P* p = (P*)e.p + at;
     const G* g = (const G*)e.g + at;                 // (this thread's eight values; as are the next)
-    uint8_t* m = (uint8_t*)e.m + at;
-    uint8_t* v = (uint8_t*)e.v + at;
+    S* m = (S*)e.m + at;
+    S* v = (S*)e.v + at;
     float* ms = e.ms + at / DION_ADAMW_BLOCK;
     float* vs = e.vs + at / DION_ADAMW_BLOCK;
     bf16* copy = sizeof(P) == 4 && e.copy ? e.copy + at : nullptr;
     int left = chunks;                               // of them from p, g, m and v on
-    // of a warp's values, 16-byte word i of lane l is word 32 i + l (float32 words of a thread lie side by side)
-    constexpr int PW = sizeof(P) / 2, GW = sizeof(G) / 2;
+    constexpr int PW = sizeof(P) / 2, GW = sizeof(G) / 2;          // words of a thread
     const uint4* pw = (const uint4*)p - (PW - 1) * lane;
     const uint4* gw = (const uint4*)g - (GW - 1) * lane;
-    const long long pc = step * (sizeof(P) / 2) / 8, gc = step * (sizeof(G) / 2) / 8, sc = step / DION_ADAMW_BLOCK;   // words, scales of a step
+    const long long pc = step * PW / 8, gc = step * GW / 8, sc = step / DION_ADAMW_BLOCK;          // words, scales of a step
     auto fetch = [&](Stage& to, int d) {             // chunk d from there
         if (d < left) {
-#pragma unroll
-            for (int i = 0; i < PW; ++i) copy_async<16>(&to.value[0][warp * 32 * PW + 32 * i + lane], pw + d * pc + 32 * i);
-#pragma unroll
-            for (int i = 0; i < GW; ++i) copy_async<16>(&to.value[1][warp * 32 * GW + 32 * i + lane], gw + d * gc + 32 * i);
-            copy_async<8>(&to.state[0][threadIdx.x], m + d * step);
-            copy_async<8>(&to.state[1][threadIdx.x], v + d * step);
-            if (lane < 2) copy_async<4>(&to.scale[lane][warp], (lane ? vs : ms) + d * sc);
+            fetch_words<PW>(&to.value[0][warp * 32 * PW + lane], pw + d * pc);
+            fetch_words<GW>(&to.value[1][warp * 32 * GW + lane], gw + d * gc);
+            if constexpr (EIGHT) {
+                copy_async<8>((uint2*)to.state[0] + threadIdx.x, m + d * step);
+                copy_async<8>((uint2*)to.state[1] + threadIdx.x, v + d * step);
+                if (lane < 2) copy_async<4>(&to.scale[lane][warp], (lane ? vs : ms) + d * sc);
+            } else {
+                fetch_words<2>(&to.state[0][warp * 64 + lane], (const uint4*)(m + d * step) - lane);
+                fetch_words<2>(&to.state[1][warp * 64 + lane], (const uint4*)(v + d * step) - lane);
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");       // (an empty group keeps the count)
     };
@@ -400,34 +450,38 @@ __device__ __forceinline__ void whole_chunks8(const Entry& e, long long at, int 
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             __syncwarp();                            // the other lanes' copies
             Values x;
-            Raw8<P> rp;
-            Raw8<G> rg;
-#pragma unroll
-            for (int k = 0; k < PW; ++k) rp.u[k] = from.value[0][threadIdx.x * PW + k];
-#pragma unroll
-            for (int k = 0; k < GW; ++k) rg.u[k] = from.value[1][threadIdx.x * GW + k];
-            unpack8(rp, x.p);
-            unpack8(rg, x.g);
-            const uint2 mb = from.state[0][threadIdx.x], rb = from.state[1][threadIdx.x];
-            float s0 = from.scale[0][warp], s1 = from.scale[1][warp];
+            read_words<P>(from.value[0] + threadIdx.x * PW, x.p);
+            read_words<G>(from.value[1] + threadIdx.x * GW, x.g);
+            uint2 mb, rb;
+            float s0, s1;
+            if constexpr (EIGHT) {
+                mb = ((const uint2*)from.state[0])[threadIdx.x], rb = ((const uint2*)from.state[1])[threadIdx.x];
+                s0 = from.scale[0][warp], s1 = from.scale[1][warp];
+            } else {
+                read_words<float>(from.state[0] + threadIdx.x * 2, x.m);
+                read_words<float>(from.state[1] + threadIdx.x * 2, x.v);
+            }
             __syncwarp();                            // all lanes have read theirs
             fetch(from, kAhead);
-            uint32_t mw[2], rw[2];
-            step8(x, mb, rb, s0, s1, c, f, rate, keep, Dither(at, key), mw, rw);
-            pack8(rp, x.p);
-#pragma unroll
-            for (int k = 0; k < PW; ++k) reinterpret_cast<uint4*>(p)[k] = rp.u[k];
-            if (sizeof(P) == 4 && copy) {
-                Raw8<bf16> rc;
-                pack8(rc, x.p);
-                *reinterpret_cast<uint4*>(copy) = rc.u[0];
-                copy += step;
+            if constexpr (EIGHT) {
+                uint32_t mw[2], rw[2];
+                step8(x, mb, rb, s0, s1, c, f, rate, keep, Dither(at, key), mw, rw);
+                store_values(p, true, 8, x.p);
+                *reinterpret_cast<uint2*>(m) = make_uint2(mw[0], mw[1]);
+                *reinterpret_cast<uint2*>(v) = make_uint2(rw[0], rw[1]);
+                if (lane == 0) {
+                    *ms = s0;
+                    *vs = s1;
+                }
+            } else {
+                step32(x, c, f, rate, keep);
+                store_values(p, true, 8, x.p, true);
+                store_values(m, true, 8, x.m, true);
+                store_values(v, true, 8, x.v, true);
             }
-            *reinterpret_cast<uint2*>(m) = make_uint2(mw[0], mw[1]);
-            *reinterpret_cast<uint2*>(v) = make_uint2(rw[0], rw[1]);
-            if (lane == 0) {
-                *ms = s0;
-                *vs = s1;
+            if (sizeof(P) == 4 && copy) {
+                store_values(copy, true, 8, x.p);
+                copy += step;
             }
             at += step;
             p += step;
@@ -443,12 +497,15 @@ __device__ __forceinline__ void whole_chunks8(const Entry& e, long long at, int 
 }
 
 constexpr int kStepCtas = 3;                         // an SM
+constexpr int kStepShared = kAhead * sizeof(Stage);
+static_assert(kStepCtas * (kStepShared + 1024) <= 228 * 1024, "shared memory of an SM");
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kStepCtas)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const Constants given, const Constants* dev, const float* scale)
 {
-    __shared__ Stage stages[kAhead];
+    extern __shared__ __align__(16) uint8_t smem[];
+    Stage* stages = reinterpret_cast<Stage*>(smem);
     wait_previous();
     allow_next();
     const float f = scale ? *scale : 1.f;
@@ -464,17 +521,20 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
         const bool wide = flags & kWide;
         const float rate = c.rate * e.lr_factor, keep = 1.f - c.decay * e.lr_factor * e.decay_factor;
         const uint32_t key = mix(c.key ^ e.index);
-        if ((flags & (kState8 | kWide)) == (kState8 | kWide)) {
+        if ((flags & (kState8 | kWide)) == (kState8 | kWide) || (flags & (kState8 | kWhole)) == kWhole) {
             const uint32_t full = (uint32_t)(e.n / kChunk), own = chunk - first;
             const int whole = own < full ? (int)((full - own + step - 1) / step) : 0;      // chunks of this CTA
             if (whole > 0) {
                 const long long at = (long long)own * kChunk + threadIdx.x * kPer, by = (long long)step * kChunk;
-                if (flags & kParamBf16) {
-                    if (flags & kGradBf16) whole_chunks8<bf16, bf16>(e, at, whole, by, c, f, rate, keep, key, stages);
-                    else whole_chunks8<bf16, float>(e, at, whole, by, c, f, rate, keep, key, stages);
-                } else {
-                    if (flags & kGradBf16) whole_chunks8<float, bf16>(e, at, whole, by, c, f, rate, keep, key, stages);
-                    else whole_chunks8<float, float>(e, at, whole, by, c, f, rate, keep, key, stages);
+                switch (flags & (kParamBf16 | kGradBf16 | kState8)) {
+                case 0: whole_chunks<float, float, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                case kParamBf16: whole_chunks<bf16, float, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                case kGradBf16: whole_chunks<float, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                case kParamBf16 | kGradBf16: whole_chunks<bf16, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                case kState8: whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                case kState8 | kParamBf16: whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                case kState8 | kGradBf16: whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages); break;
+                default: whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
                 }
                 chunk += whole * step;
             }
@@ -504,16 +564,9 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
                 store_bytes((uint8_t*)e.m + at, wide, k, mw);
                 store_bytes((uint8_t*)e.v + at, wide, k, rw);
             } else {
-                float2 r[4];
                 load_values((const float*)e.m + at, wide, k, x.m);
                 load_values((const float*)e.v + at, wide, k, x.v);
-                moments(x, c, f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
-                    asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
-                }
-                parameters(x, r, c, rate, keep);
+                step32(x, c, f, rate, keep);
                 store_values((float*)e.m + at, wide, k, x.m);
                 store_values((float*)e.v + at, wide, k, x.v);
             }
@@ -791,6 +844,7 @@ int fill(Table<CAP>& t, int i, int count, const dion_adamw_tensor* tensors, bool
             all |= (uintptr_t)s.p | (uintptr_t)s.copy | ((uintptr_t)s.m | (uintptr_t)s.v) << (s.m_scale ? 1 : 0);
         }
         if (all % 16 == 0) e.flags |= kWide;
+        if (all % 32 == 0) e.flags |= kWhole;
         t.first[t.count++] = t.chunks;
         t.chunks += chunks;
     }
@@ -804,11 +858,14 @@ cudaError_t step_some(int& i, int count, const dion_adamw_tensor* tensors, const
     Table<CAP> t;
     i = fill(t, i, count, tensors, true);
     if (t.chunks == 0) return cudaSuccess;
+    static std::atomic<unsigned long long> attr{0};
+    const cudaError_t e = smem_attr_once((const void*)adamw_kernel<CAP>, kStepShared, attr);
+    if (e != cudaSuccess) return e;
     // Eight times what runs at once, taking chunks in turn: the CTAs at work then read and write side by side, and none
     // ends much later than the others.  262 million bfloat16 values with 8-bit states: 501 us, 24 times 525, once 539;
     // with contiguous ranges for each CTA 575.
     const unsigned ctas = (unsigned)std::min<long long>(t.chunks, 8ll * kStepCtas * num_sms());
-    return launch_overlapped("adamw", adamw_kernel<CAP>, dim3(ctas), dim3(kThreads), 0, st, t, c, dev, scale);
+    return launch_overlapped("adamw", adamw_kernel<CAP>, dim3(ctas), dim3(kThreads), kStepShared, st, t, c, dev, scale);
 }
 
 dion_status step_all(int count, const dion_adamw_tensor* tensors, const Constants& c, const Constants* dev,
