@@ -380,9 +380,11 @@ __device__ __forceinline__ void step32(Values& x, const Constants& c, float f, f
 // types are fixed and addresses are kept.
 constexpr int kAhead = 2;
 struct Stage {
-    uint4 value[2][2 * kThreads];                    // [p | g] in the memory's order, a warp's 1 KB (512 bytes) together
-    uint4 state[2][2 * kThreads];                    // [m | v] likewise (8-bit: 256 bytes a warp)
-    float scale[2][kThreads / 32];                   // [m | r][warp]
+    // a warp's values in the memory's order, from the start of its 1 KB whatever their type: warps go on to the next
+    // tensor, whose types may be others, without waiting for each other
+    uint4 value[2][kThreads / 32][64];               // [p | g]
+    uint4 state[2][kThreads / 32][64];               // [m | v]
+    float scale[2][kThreads / 32];                   // [m | r]
 };
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from)
@@ -426,15 +428,15 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int c
     const long long pc = step * PW / 8, gc = step * GW / 8, sc = step / DION_ADAMW_BLOCK;          // words, scales of a step
     auto fetch = [&](Stage& to, int d) {             // chunk d from there
         if (d < left) {
-            fetch_words<PW>(&to.value[0][warp * 32 * PW + lane], pw + d * pc);
-            fetch_words<GW>(&to.value[1][warp * 32 * GW + lane], gw + d * gc);
+            fetch_words<PW>(&to.value[0][warp][lane], pw + d * pc);
+            fetch_words<GW>(&to.value[1][warp][lane], gw + d * gc);
             if constexpr (EIGHT) {
-                copy_async<8>((uint2*)to.state[0] + threadIdx.x, m + d * step);
-                copy_async<8>((uint2*)to.state[1] + threadIdx.x, v + d * step);
+                copy_async<8>((uint2*)to.state[0][warp] + lane, m + d * step);
+                copy_async<8>((uint2*)to.state[1][warp] + lane, v + d * step);
                 if (lane < 2) copy_async<4>(&to.scale[lane][warp], (lane ? vs : ms) + d * sc);
             } else {
-                fetch_words<2>(&to.state[0][warp * 64 + lane], (const uint4*)(m + d * step) - lane);
-                fetch_words<2>(&to.state[1][warp * 64 + lane], (const uint4*)(v + d * step) - lane);
+                fetch_words<2>(&to.state[0][warp][lane], (const uint4*)(m + d * step) - lane);
+                fetch_words<2>(&to.state[1][warp][lane], (const uint4*)(v + d * step) - lane);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");       // (an empty group keeps the count)
@@ -450,16 +452,16 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int c
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             __syncwarp();                            // the other lanes' copies
             Values x;
-            read_words<P>(from.value[0] + threadIdx.x * PW, x.p);
-            read_words<G>(from.value[1] + threadIdx.x * GW, x.g);
+            read_words<P>(&from.value[0][warp][lane * PW], x.p);
+            read_words<G>(&from.value[1][warp][lane * GW], x.g);
             uint2 mb, rb;
             float s0, s1;
             if constexpr (EIGHT) {
-                mb = ((const uint2*)from.state[0])[threadIdx.x], rb = ((const uint2*)from.state[1])[threadIdx.x];
+                mb = ((const uint2*)from.state[0][warp])[lane], rb = ((const uint2*)from.state[1][warp])[lane];
                 s0 = from.scale[0][warp], s1 = from.scale[1][warp];
             } else {
-                read_words<float>(from.state[0] + threadIdx.x * 2, x.m);
-                read_words<float>(from.state[1] + threadIdx.x * 2, x.v);
+                read_words<float>(&from.state[0][warp][lane * 2], x.m);
+                read_words<float>(&from.state[1][warp][lane * 2], x.v);
             }
             __syncwarp();                            // all lanes have read theirs
             fetch(from, kAhead);
@@ -500,7 +502,10 @@ constexpr int kStepCtas = 3;                         // an SM
 constexpr int kStepShared = kAhead * sizeof(Stage);
 static_assert(kStepCtas * (kStepShared + 1024) <= 228 * 1024, "shared memory of an SM");
 
-template <int CAP>
+// Which states the tensors of a list have.
+enum : int { kAll32 = 1, kAll8 = 2, kMixed = 3 };
+
+template <int CAP, int KIND>
 __global__ void __launch_bounds__(kThreads, kStepCtas)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const Constants given, const Constants* dev, const float* scale)
 {
@@ -521,20 +526,29 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
         const bool wide = flags & kWide;
         const float rate = c.rate * e.lr_factor, keep = 1.f - c.decay * e.lr_factor * e.decay_factor;
         const uint32_t key = mix(c.key ^ e.index);
-        if ((flags & (kState8 | kWide)) == (kState8 | kWide) || (flags & (kState8 | kWhole)) == kWhole) {
+        const bool eight = KIND == kMixed ? flags & kState8 : KIND == kAll8;
+        if (flags & (eight ? kWide : kWhole)) {
             const uint32_t full = (uint32_t)(e.n / kChunk), own = chunk - first;
             const int whole = own < full ? (int)((full - own + step - 1) / step) : 0;      // chunks of this CTA
             if (whole > 0) {
                 const long long at = (long long)own * kChunk + threadIdx.x * kPer, by = (long long)step * kChunk;
-                switch (flags & (kParamBf16 | kGradBf16 | kState8)) {
-                case 0: whole_chunks<float, float, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                case kParamBf16: whole_chunks<bf16, float, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                case kGradBf16: whole_chunks<float, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                case kParamBf16 | kGradBf16: whole_chunks<bf16, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                case kState8: whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                case kState8 | kParamBf16: whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                case kState8 | kGradBf16: whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages); break;
-                default: whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                if (KIND != kAll8 && !eight) {
+                    if (flags & kParamBf16) {
+                        if (flags & kGradBf16) whole_chunks<bf16, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        else whole_chunks<bf16, float, false>(e, at, whole, by, c, f, rate, keep, key, stages);
+                    } else {
+                        if (flags & kGradBf16) whole_chunks<float, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        else whole_chunks<float, float, false>(e, at, whole, by, c, f, rate, keep, key, stages);
+                    }
+                }
+                if (KIND != kAll32 && eight) {
+                    if (flags & kParamBf16) {
+                        if (flags & kGradBf16) whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        else whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                    } else {
+                        if (flags & kGradBf16) whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        else whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                    }
                 }
                 chunk += whole * step;
             }
@@ -550,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
             else load_values((const float*)e.p + at, wide, k, x.p);
             if (flags & kGradBf16) load_values((const bf16*)e.g + at, wide, k, x.g);
             else load_values((const float*)e.g + at, wide, k, x.g);
-            if (flags & kState8) {
+            if (eight) {
                 const long long block = at / DION_ADAMW_BLOCK;
                 const uint2 mb = load_bytes((const uint8_t*)e.m + at, wide, k), rb = load_bytes((const uint8_t*)e.v + at, wide, k);
                 float ms = e.ms[block], rs = e.vs[block];
@@ -851,6 +865,19 @@ int fill(Table<CAP>& t, int i, int count, const dion_adamw_tensor* tensors, bool
     return i;
 }
 
+template <int CAP, int KIND>
+cudaError_t step_table(const Table<CAP>& t, const Constants& c, const Constants* dev, const float* scale, cudaStream_t st)
+{
+    static std::atomic<unsigned long long> attr{0};
+    const cudaError_t e = smem_attr_once((const void*)adamw_kernel<CAP, KIND>, kStepShared, attr);
+    if (e != cudaSuccess) return e;
+    // Eight times what runs at once, taking chunks in turn: the CTAs at work then read and write side by side, and none
+    // ends much later than the others.  262 million bfloat16 values with 8-bit states, before other steps: 501 us, 24 times 525, once 539;
+    // with contiguous ranges for each CTA 575.
+    const unsigned ctas = (unsigned)std::min<long long>(t.chunks, 8ll * kStepCtas * num_sms());
+    return launch_overlapped("adamw", adamw_kernel<CAP, KIND>, dim3(ctas), dim3(kThreads), kStepShared, st, t, c, dev, scale);
+}
+
 template <int CAP>
 cudaError_t step_some(int& i, int count, const dion_adamw_tensor* tensors, const Constants& c, const Constants* dev,
                       const float* scale, cudaStream_t st)
@@ -858,14 +885,12 @@ cudaError_t step_some(int& i, int count, const dion_adamw_tensor* tensors, const
     Table<CAP> t;
     i = fill(t, i, count, tensors, true);
     if (t.chunks == 0) return cudaSuccess;
-    static std::atomic<unsigned long long> attr{0};
-    const cudaError_t e = smem_attr_once((const void*)adamw_kernel<CAP>, kStepShared, attr);
-    if (e != cudaSuccess) return e;
-    // Eight times what runs at once, taking chunks in turn: the CTAs at work then read and write side by side, and none
-    // ends much later than the others.  262 million bfloat16 values with 8-bit states: 501 us, 24 times 525, once 539;
-    // with contiguous ranges for each CTA 575.
-    const unsigned ctas = (unsigned)std::min<long long>(t.chunks, 8ll * kStepCtas * num_sms());
-    return launch_overlapped("adamw", adamw_kernel<CAP>, dim3(ctas), dim3(kThreads), kStepShared, st, t, c, dev, scale);
+    int kind = 0;
+    for (int k = 0; k < t.count; ++k) kind |= t.e[k].flags & kState8 ? kAll8 : kAll32;
+    // A kernel of one kind of states has the registers for it: 262 million bfloat16 values with 8-bit states 472 us, in the mixed
+    // one, which spills, 486.
+    return kind == kAll32 ? step_table<CAP, kAll32>(t, c, dev, scale, st) : kind == kAll8 ? step_table<CAP, kAll8>(t, c, dev, scale, st)
+                                                                                          : step_table<CAP, kMixed>(t, c, dev, scale, st);
 }
 
 dion_status step_all(int count, const dion_adamw_tensor* tensors, const Constants& c, const Constants* dev,

@@ -85,6 +85,46 @@ def test_step(bits, p, g, offset):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p,g", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
+def test_several_chunks_a_cta(bits, p, g):
+    """More chunks of 2048 than CTAs of a launch, so that each takes several through its copies in flight."""
+    parts = make([9_000_003], p, g, bits, copies=p is F32)
+    before = [copy_of(x) for x in parts[0]], [copy_of(x) for x in parts[2]], [copy_of(x) for x in parts[3]]
+    od.dion_adamw_step(od.dion_adamw_plan(*parts[:4], copies=parts[4]), step=3, lr=1e-3)
+    check(parts, before, 3)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_lists_of_all_types_have_the_same_bits_as_single_tensors(bits):
+    """A CTA's warps go from tensor to tensor by themselves: what one copies for the next tensor must not meet what
+    another still reads of the last one, whatever the types."""
+    types = [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)] * 3
+    kinds = [make([2_000_000 + 2048 * i], p, g, bits, seed=i) for i, (p, g) in enumerate(types)]
+    joined = [[copy_of(t) for k in kinds for t in k[i]] for i in range(4)]
+    od.dion_adamw_step(od.dion_adamw_plan(*joined), step=3, lr=1e-3)
+    for i in range(len(kinds)):
+        # (the dither goes by the place in the list)
+        empty = [[x[:0] if not isinstance(x, od.State8) else od.State8(x.data[:0], x.scale[:0]) for x in kinds[i][j]] * i for j in range(4)]
+        alone = [empty[j] + kinds[i][j] for j in range(4)]
+        od.dion_adamw_step(od.dion_adamw_plan(*alone), step=3, lr=1e-3)
+        for j in (0, 2, 3):
+            a, b = joined[j][i], alone[j][i]
+            for s, t in zip(a, b) if isinstance(a, od.State8) else [(a, b)]:
+                assert torch.equal(s.view(torch.uint8), t.view(torch.uint8))
+
+
+@pytest.mark.parametrize("offset", [0, 4, 12])
+def test_lists_of_both_kinds_of_states(offset):
+    """Float32 and 8-bit states in turn; 4 and 12 float32 values are 16-byte boundaries but not 32-byte ones."""
+    kinds = [make([n], p, g, bits, seed=n, offset=offset) for n, p, g, bits in
+             [(4_000_000, BF16, BF16, 8), (70_001, F32, F32, 32), (6_000_001, F32, BF16, 32), (2048, BF16, F32, 8), (2_000_000, F32, F32, 8)]]
+    parts = [[t for k in kinds for t in k[i]] for i in range(4)] + [None]
+    before = [copy_of(x) for x in parts[0]], [copy_of(x) for x in parts[2]], [copy_of(x) for x in parts[3]]
+    od.dion_adamw_step(od.dion_adamw_plan(*parts[:4]), step=3, lr=1e-3)
+    check(parts, before, 3)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_steps_in_a_row_from_nothing(bits):
     """From zeroed states, with gradients that are zero in places (rows of an embedding that no token used)."""
     parts = make([3000, 513], BF16, BF16, bits)
@@ -172,6 +212,18 @@ def test_roots_of_subnormal_second_moments():
     od.dion_adamw_step(od.dion_adamw_plan(p, [g], first, second), step=1, lr=1e-3)
     want = math.sqrt(1e-3) * g.double()
     assert torch.all((ref.values(second[0], g.numel()) - want).abs() <= (2.0 ** -3 + 2.0 ** -10) * want)
+
+
+def test_roots_of_large_second_moments():
+    """Second moments on both sides of 2^63, where roots are taken in another way, and up to float32's largest: each
+    block's values are within 1.3 of each other, and a value is off by less than a step, 2^-3 of it (and 2^-20)."""
+    g = torch.logspace(9, 19.2, 1 << 14, device="cuda")
+    p = [torch.zeros_like(g)]
+    first, second = od.dion_adamw_state(p, bits=8)
+    od.dion_adamw_step(od.dion_adamw_plan(p, [g], first, second), step=1, lr=1e-3)
+    want = math.sqrt(1e-3) * g.double()
+    assert torch.all((ref.values(second[0], g.numel()) - want).abs() <= (2.0 ** -3 + 2.0 ** -20) * want)
+    assert torch.all((p[0].double() + 1e-3).abs() <= 1e-3 * 20 * EPS32)
 
 
 def test_roots_follow_a_change_that_is_smaller_than_a_step():
