@@ -7,6 +7,13 @@
 // CTA finds its first chunk's tensor by bisection over the first chunk of each.
 // A warp's 256 values are one block of an 8-bit state, so a block's largest
 // magnitude is one reduction over the warp.
+//
+// Memory bounds the step with float32 states: 67 million values take 217 us with
+// bfloat16 parameters and gradients, 274 with float32 ones, 0.99 to 1.01 of the
+// time of a copy of as many bytes.  With 8-bit states and bfloat16 the arithmetic
+// of a value (decoding, roots, dither, encoding) fills three quarters of the issue
+// slots: 126 us for 67 million, 0.79 of the copy's rate (float32 parameters 0.97).
+// The norm of 436 MB takes 69 us (0.92).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* 
 // that a call is one launch and has no workspace.  Lists of few values have many
 // small tensors, so 256 threads take single chunks, four of them together, whose
 // tensors are told by a table.
-constexpr int kCluster = 8, kFewThreads = 1024, kFewChunks = 512, kMedium = 256;
+constexpr int kFewThreads = 1024, kFewChunks = 512, kMedium = 256;
 struct TensorOf {
     uint16_t chunk[kFewChunks];
 };
@@ -720,13 +727,14 @@ template <int CAP>
 __global__ void __launch_bounds__(kFewThreads)
     grad_norm_small_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ TensorOf of, const double max_norm, float* out)
 {
-    constexpr uint32_t GROUPS = kCluster * kFewThreads / kThreads, N = 4;
+    constexpr uint32_t N = 4;
+    const uint32_t groups = gridDim.x * (kFewThreads / kThreads);      // (the grid is the cluster)
     __shared__ double sums[kFewThreads / 32];
     __shared__ double mine;
     wait_previous();
     allow_next();
     double sum = 0;
-    for (uint32_t c = blockIdx.x * (kFewThreads / kThreads) + threadIdx.x / kThreads; c < t.chunks; c += N * GROUPS) {
+    for (uint32_t c = blockIdx.x * (kFewThreads / kThreads) + threadIdx.x / kThreads; c < t.chunks; c += N * groups) {
         // 16-byte words first, as they are (anything done to one would wait for it before the next is asked for);
         // of a chunk without them, its squares
         uint4 raw[N][2];
@@ -734,7 +742,7 @@ __global__ void __launch_bounds__(kFewThreads)
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (uint32_t u = 0; u < N; ++u) {
-            const uint32_t chunk = c + u * GROUPS;
+            const uint32_t chunk = c + u * groups;
             const int i = of.chunk[min(chunk, (uint32_t)kFewChunks - 1)];
             const Entry& e = t.e[i];
             const long long at = ((long long)chunk - t.first[i]) * kChunk + threadIdx.x % kThreads * kPer;
@@ -783,7 +791,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        for (int r = 1; r < kCluster; ++r) {
+        for (int r = 1; r < (int)gridDim.x; ++r) {
             uint32_t a;
             double v;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(&mine)), "r"(r));
@@ -922,14 +930,44 @@ int norm_ctas() { return 6 * num_sms(); }
 long long norm_launches(int count) { return cdiv(count, kLarge) + cdiv(count, 15); }
 
 // Lists whose norm is one launch without a workspace: 867000 float32 values in 63
-// tensors take 11 us on the GPU so and 7 in two launches, but a call, host
-// included, takes 11 against 16.
+// tensors take 9 us on the GPU so and 7 in two launches, but a call, host
+// included, takes 9 against 16.
 bool few_values(int count, const dion_adamw_tensor* tensors)
 {
     if (count > kMedium) return false;
     long long chunks = 0;
     for (int i = 0; i < count && chunks <= kFewChunks; ++i) chunks += cdiv(tensors[i].n, kChunk);
     return chunks <= kFewChunks;
+}
+// CTAs of that launch's cluster: 16 where the device has room for such a cluster (asked once a device; beyond eight is
+// not portable), else 8, which take 11 us for the 867000 values.
+template <int CAP>
+int norm_cluster()
+{
+    static std::atomic<unsigned long long> known{0}, wide{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev > 63) return 8;
+    const unsigned long long bit = 1ull << dev;
+    if (!(known.load(std::memory_order_acquire) & bit)) {
+        const auto kernel = grad_norm_small_kernel<CAP>;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 16;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kFewThreads);
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&clusters, (const void*)kernel, &cfg) == cudaSuccess && clusters > 0)
+            wide.fetch_or(bit, std::memory_order_acq_rel);
+        else
+            cudaGetLastError();
+        known.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return wide.load(std::memory_order_acquire) & bit ? 16 : 8;
 }
 template <int CAP>
 cudaError_t norm_few(int count, const dion_adamw_tensor* tensors, double max_norm, float* out, cudaStream_t st)
@@ -944,7 +982,8 @@ cudaError_t norm_few(int count, const dion_adamw_tensor* tensors, double max_nor
         t.first[0] = 0;
         t.e[0] = Entry{};
     }
-    return launch_cluster("grad_norm_small", grad_norm_small_kernel<CAP>, dim3(kCluster), dim3(kFewThreads), kCluster, 0, st, t, of,
+    const int cluster = norm_cluster<CAP>();
+    return launch_cluster("grad_norm_small", grad_norm_small_kernel<CAP>, dim3((unsigned)cluster), dim3(kFewThreads), cluster, 0, st, t, of,
                           max_norm, out);
 }
 

@@ -3,6 +3,9 @@
 // Half a warp takes one 128-column chunk of a row: lane l its columns 8 l ..
 // 8 l + 7, which are one 32-bit word of the held chunk, so the reads and the
 // 64-byte write of a chunk are contiguous and a group is 4, 8 or 16 lanes.
+//
+// 14336 x 4096 bfloat16 values take 34 us (147 MB move, 22 us at a copy's rate:
+// 15 instructions a value fill 73 % of the issue slots) and 23 to 25 us back.
 #include "q4.cuh"
 
 namespace dion {
