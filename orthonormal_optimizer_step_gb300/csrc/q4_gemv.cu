@@ -31,7 +31,7 @@
 // Measured: 1 x 53248 x 16384 in 77 us, 5.8 TB/s (0.86 of a copy's rate); 1 x 4096
 // x 4096 in 4.9, of which its weights' time is 1.3 and a launch's start, x and a
 // tile's latency the rest; 16 x 4096 x 14336 of 8-bit rows in 17.5 (weights 4.7):
-// each CTA of 16 rows converts its 230 KB of x, and joins.
+// each CTA converts its 57000 values of x, and joins.
 #include <algorithm>
 
 #include "q4.cuh"
