@@ -36,13 +36,28 @@ extern "C" {
  *
  * 8-bit states: blocks of 256 values, the last one short.  m holds E4M3 values
  * that stand for value * scale, scale = max(amax / 448, 2^-100); v holds
- * r = sqrt(second moment) in the same format.  m is rounded to nearest even.
+ * r = sqrt(second moment) in the same format.
  * r is rounded up with the probability of its place between two values, by a
  * hash of seed, step, the tensor's place in the list and the value's place in
  * the tensor (with beta2 = 0.999 a step changes r by less than half the
  * distance of two values, so rounding to nearest would never let it fall), and
- * an r above zero does not become zero.  Infinities and NaN become the format's
- * NaN and do not count for amax.
+ * an r above zero does not become zero.
+ * m is rounded to nearest even where that holds no value in its place: with
+ * 1 - beta1 >= 3/32, except values that nearest rounding takes below 2^-6 (of the
+ * scale) while the gradient's part, (1 - beta1) g', is at most 2^-9.  Those, and
+ * with a smaller 1 - beta1 all values, are rounded by the same hash, the magnitude
+ * up with the probability of its place, so that an m whose gradient has stopped
+ * reaches zero and its parameter comes to rest.
+ * Infinities and NaN become the format's NaN and do not count for amax.
+ *
+ * What 8 bits cost, with Gaussian gradients: a held r has a standard deviation of
+ * 16.5 % of its value with beta2 = 0.999 (1 % to 99 % of them: 0.71 to 1.43 of it),
+ * 15.6 % with 0.99, 12 % with 0.95, since each step's rounding stays in it for
+ * 1 / (1 - beta2) steps; r is without bias a step, but its square, which the next
+ * step takes, is not: second moments are 5.4, 4.6 and 3.3 % too large in the mean.
+ * An m that is rounded to nearest, under a gradient that does not change at all,
+ * stays between a half and three times of it; a gradient's noise does what the
+ * dither would.
  */
 typedef struct {
     long long n;

@@ -31,6 +31,8 @@ using namespace q8;
 
 constexpr int kThreads = 256, kPer = 8, kChunk = kThreads * kPer;
 static_assert(32 * kPer == DION_ADAMW_BLOCK, "a warp holds one block of an 8-bit state");
+constexpr int kBlockLog = 8;
+static_assert(1 << kBlockLog == DION_ADAMW_BLOCK, "blocks by shifts");
 
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kWide = 8, kWhole = 16 };   // 16-byte accesses; float32 values in 32 bytes
 
@@ -198,9 +200,9 @@ __device__ __forceinline__ void block_scales(float2 amax, float2& scale, float2&
     inverse = fma2(fma2(make_float2(-scale.x, -scale.y), y, make_float2(1.f, 1.f)), y, y);
 }
 
-// Each element's dither, 20 bits, is the top of mix((at + j) ^ key) with at a
-// multiple of eight, so that (at + j) ^ key = x ^ j and mix's first shift is
-// the same for all eight.
+// Each element's dither is mix((at + j) ^ key) with at a multiple of eight, so
+// that (at + j) ^ key = x ^ j and mix's first shift is the same for all eight:
+// the upper 20 bits for the root, the lower 12 and a half for the first moment.
 struct Dither {
     uint32_t y;
     __device__ __forceinline__ Dither(long long at, uint32_t key)
@@ -208,12 +210,14 @@ struct Dither {
         const uint32_t x = (uint32_t)at ^ key ^ (uint32_t)(at >> 32);
         y = x ^ (x >> 16);
     }
-    __device__ __forceinline__ uint32_t operator()(int j) const
+    __device__ __forceinline__ uint32_t hash(int j) const
     {
         uint32_t w = (y ^ (uint32_t)j) * 0x9E3779B1u;
         w = (w ^ (w >> 15)) * 0x85EBCA6Bu;
-        return (w ^ (w >> 16)) >> 12;
+        return w ^ (w >> 16);
     }
+    __device__ __forceinline__ uint32_t operator()(int j) const { return hash(j) >> 12; }
+    __device__ __forceinline__ uint32_t first(int j) const { return (hash(j) & 0xfffu) << 8 | 0x80u; }
 };
 
 // E4M3 bytes of x = r / scale >= 0 (finite), rounded up where the dither
@@ -228,6 +232,16 @@ __device__ __forceinline__ uint32_t dithered4(float2 a, float2 b, const Dither& 
     const uint32_t lo = __byte_perm(__float_as_uint(a.x) + dither(j), __float_as_uint(a.y) + dither(j + 1), 0x7632);
     const uint32_t hi = __byte_perm(__float_as_uint(b.x) + dither(j + 2), __float_as_uint(b.y) + dither(j + 3), 0x7632);
     return __byte_perm(__vminu2(lo, 0x07ef07efu) >> 4, __vminu2(hi, 0x07ef07efu) >> 4, 0x6420);
+}
+
+// The same with signs: the bytes' upper bits are those of the halves.
+__device__ __forceinline__ uint32_t dithered4_signed(float2 a, float2 b, const Dither& dither, int j)
+{
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x) + dither.first(j), __float_as_uint(a.y) + dither.first(j + 1), 0x7632);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x) + dither.first(j + 2), __float_as_uint(b.y) + dither.first(j + 3), 0x7632);
+    const uint32_t l = (__vminu2(lo & 0x7fff7fffu, 0x07ef07efu) >> 4 & 0x007f007fu) | (lo >> 8 & 0x00800080u);
+    const uint32_t h = (__vminu2(hi & 0x7fff7fffu, 0x07ef07efu) >> 4 & 0x007f007fu) | (hi >> 8 & 0x00800080u);
+    return __byte_perm(l, h, 0x6420);
 }
 
 // What a thread holds of a chunk: eight values of each, of which k exist (the
@@ -292,16 +306,69 @@ __device__ __forceinline__ float2 roots(float2 v)
     return fma2(residual, mul2(y, make_float2(0.5f, 0.5f)), s);
 }
 
-// The roots of second moments v, times kRootScale, and the 8-bit states of a warp's block of 256.
-__device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4], float2 (&r)[4], const Dither& dither, float& ms,
-                                       float& rs, uint32_t (&mw)[2], uint32_t (&rw)[2])
+// Where a first moment is rounded by its dither.  Rounded to nearest, a value that a
+// step changes by less than half the format's distance there stays what it was, in
+// every step: one whose gradient has stopped would never reach zero, while its root
+// goes on falling to the least code, and the parameter would move for ever.  A
+// distance is a ninth to a sixteenth of a value, so
+//  - with 1 - beta1 >= 3/32 the decay alone takes every value from 2^-6 on to
+//    another one.  Below, all distances are 2^-9, and a value is dithered where the
+//    gradient's part is at most that (with a larger part nearest rounding does move
+//    it).  Nearest rounding elsewhere has half the error.
+//  - with less all values are dithered (ALL).
+constexpr float kNearest = 3.f / 32.f;               // least 1 - beta1
+
+// Of a thread's eight bytes of first moments, those below 2^-6 (0x08) of values that are not zero, one bit each.  (In a
+// block of zeros, a row of an embedding that no token used, mi is zero.)
+__device__ __forceinline__ uint32_t small_codes(const uint32_t (&w)[2], const float2 (&m)[4], float mi)
 {
-    // infinities reach the maxima, and a v that is NaN; a NaN of m does not, and has its own byte in the conversion
+    uint32_t mask = 0;
+    if ((((w[0] & 0x78787878u) + 0x78787878u) & ((w[1] & 0x78787878u) + 0x78787878u) & 0x80808080u) != 0x80808080u && mi != 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (!(w[j >> 2] >> (8 * (j & 3)) & 0x78u) && (j & 1 ? m[j >> 1].y : m[j >> 1].x) != 0.f) mask |= 1u << j;
+    }
+    return mask;
+}
+// Their dithered codes.  Few threads come here and the others' registers are scarce, so what the moments were made of
+// is read again (262 million bfloat16 values 485 us; kept in registers, 490 to 497): g, the old bytes m and scale (none is
+// overwritten yet); mi: the new scale's reciprocal.
+template <typename G>
+__device__ __forceinline__ void dither_small(uint32_t mask, const G* g, const uint8_t* m, const float* scale, const Constants& c, float f,
+                                             float mi, const Dither& dither, uint32_t (&mw)[2])
+{
+    do {
+        const int j = __ffs(mask) - 1, at = 8 * (j & 3);
+        mask &= mask - 1;
+        const float part = __fmul_rn(__fmul_rn(to_f(g[j]), f), c.c1);
+        const float v = __fadd_rn(__fmul_rn(__fmul_rn(e4m3_pair(m[j]).x, *scale), c.b1), part);
+        if (fabsf(part * mi) <= 0x1p-9f) {
+            const uint32_t code = (__float_as_uint(fabsf(v * mi) * 0x1p-120f) + dither.first(j)) >> 20;
+            const uint32_t w = ((j < 4 ? mw[0] : mw[1]) & ~(0x7fu << at)) | code << at;
+            if (j < 4) mw[0] = w;
+            else mw[1] = w;
+        }
+    } while (mask);
+}
+
+// The roots of second moments v, times kRootScale, and the 8-bit states of a warp's block of 256; mi: the reciprocal of
+// the first moments' scale.
+template <bool ALL>
+__device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4], float2 (&r)[4], const Dither& dither, float& ms,
+                                       float& mi, float& rs, uint32_t (&mw)[2], uint32_t (&rw)[2])
+{
+    // infinities reach the maxima, and a v that is NaN; a NaN of m does not, and has its own byte in the conversion (a
+    // dithered one has none, so it counts there)
     float mmax = 0.f;
     uint32_t vmax = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        mmax = fmaxf(mmax, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
+        if (ALL) {
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(mmax) : "f"(fabsf(m[j].x)));
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(mmax) : "f"(fabsf(m[j].y)));
+        } else {
+            mmax = fmaxf(mmax, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
+        }
         vmax = max3(vmax, __float_as_uint(v[j].x), __float_as_uint(v[j].y));
     }
     uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(mmax));
@@ -327,16 +394,25 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4
     block_scales(make_float2(__uint_as_float(mbits), rmax * (1.f / kRootScale)), scale, inverse);
     ms = scale.x;
     rs = scale.y;
-    const float mi = inverse.x, ri = inverse.y * (1.f / kRootScale);
+    mi = mbits ? inverse.x : 0.f;
+    const float ri = inverse.y * (1.f / kRootScale);
     uint32_t least = 0xffffffffu;
-    float2 x[4];
+    float2 x[4], y[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 y = mul2(m[j], make_float2(mi, mi));
-        const uint32_t w = plain ? cvt2<DION_E4M3>(y.x, y.y) : cvt2<DION_E4M3>(inf_to_nan(y.x), inf_to_nan(y.y));
-        mw[j >> 1] = j & 1 ? mw[j >> 1] | (w << 16) : w;
+        y[j] = mul2(m[j], make_float2(mi, mi));
+        if (ALL) {
+            y[j] = mul2(y[j], make_float2(0x1p-120f, 0x1p-120f));
+        } else {
+            const uint32_t w = plain ? cvt2<DION_E4M3>(y[j].x, y[j].y) : cvt2<DION_E4M3>(inf_to_nan(y[j].x), inf_to_nan(y[j].y));
+            mw[j >> 1] = j & 1 ? mw[j >> 1] | (w << 16) : w;
+        }
         x[j] = mul2(mul2(r[j], make_float2(ri, ri)), make_float2(0x1p-120f, 0x1p-120f));
         least = min(min(least, __float_as_uint(x[j].x)), __float_as_uint(x[j].y));
+    }
+    if (ALL) {
+        mw[0] = dithered4_signed(y[0], y[1], dither, 0);
+        mw[1] = dithered4_signed(y[2], y[3], dither, 4);
     }
     rw[0] = dithered4(x[0], x[1], dither, 0);
     rw[1] = dithered4(x[2], x[3], dither, 4);
@@ -347,14 +423,17 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4
     }
     if (!plain) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j) {
             if (mag_bits(j & 1 ? r[j >> 1].y : r[j >> 1].x) >= kInfBits) rw[j >> 2] |= 0x7fu << (8 * (j & 3));
+            if (ALL && mag_bits(j & 1 ? m[j >> 1].y : m[j >> 1].x) >= kInfBits) mw[j >> 2] |= 0x7fu << (8 * (j & 3));
+        }
     }
 }
 
 // A step with 8-bit states on what a thread holds; encodes them into mw and rw, with the block's new scales in ms and rs.
-__device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, float& rs, const Constants& c, float f, float rate,
-                                      float keep, const Dither& dither, uint32_t (&mw)[2], uint32_t (&rw)[2])
+template <bool ALL>
+__device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, float& mi, float& rs, const Constants& c, float f,
+                                          float rate, float keep, const Dither& dither, uint32_t (&mw)[2], uint32_t (&rw)[2])
 {
     float2 r[4];
     e4m3_values(mb, ms, x.m);
@@ -362,7 +441,7 @@ __device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
     moments(x, c, f);
-    encode(x.m, x.v, r, dither, ms, rs, mw, rw);
+    encode<ALL>(x.m, x.v, r, dither, ms, mi, rs, mw, rw);
     parameters(x, r, c.root * (1.f / kRootScale), c.eps, rate, keep);
 }
 
@@ -415,35 +494,31 @@ __device__ __forceinline__ void read_words(const uint4* from, float2 (&f)[4])
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = from[i];
     unpack8(r, f);
 }
-template <typename P, typename G, bool EIGHT>
-__device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int chunks, long long step, const Constants& c, float f, float rate,
+template <typename P, typename G, bool EIGHT, bool ALL = false>
+__device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int left, uint32_t step, const Constants& c, float f, float rate,
                                              float keep, uint32_t key, Stage* stages)
 {
     using S = typename std::conditional<EIGHT, uint8_t, float>::type;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // (of all these addresses only what changes is kept: registers decide about spills here)
     P* p = (P*)e.p + at;
     const G* g = (const G*)e.g + at;                 // (this thread's eight values; as are the next)
     S* m = (S*)e.m + at;
     S* v = (S*)e.v + at;
-    float* ms = e.ms + at / DION_ADAMW_BLOCK;
-    float* vs = e.vs + at / DION_ADAMW_BLOCK;
     bf16* copy = sizeof(P) == 4 && e.copy ? e.copy + at : nullptr;
-    int left = chunks;                               // of them from p, g, m and v on
     constexpr int PW = sizeof(P) / 2, GW = sizeof(G) / 2;          // words of a thread
-    const uint4* pw = (const uint4*)p - (PW - 1) * lane;
-    const uint4* gw = (const uint4*)g - (GW - 1) * lane;
-    const long long pc = step * PW / 8, gc = step * GW / 8, sc = step / DION_ADAMW_BLOCK;          // words, scales of a step
     auto fetch = [&](Stage& to, int d) {             // chunk d from there
         if (d < left) {
-            fetch_words<PW>(&to.value[0][warp][lane], pw + d * pc);
-            fetch_words<GW>(&to.value[1][warp][lane], gw + d * gc);
+            const long long ahead = (long long)d * step;
+            fetch_words<PW>(&to.value[0][warp][lane], (const uint4*)(p + ahead) - (PW - 1) * lane);
+            fetch_words<GW>(&to.value[1][warp][lane], (const uint4*)(g + ahead) - (GW - 1) * lane);
             if constexpr (EIGHT) {
-                copy_async<8>((uint2*)to.state[0][warp] + lane, m + d * step);
-                copy_async<8>((uint2*)to.state[1][warp] + lane, v + d * step);
-                if (lane < 2) copy_async<4>(&to.scale[lane][warp], (lane ? vs : ms) + d * sc);
+                copy_async<8>((uint2*)to.state[0][warp] + lane, m + ahead);
+                copy_async<8>((uint2*)to.state[1][warp] + lane, v + ahead);
+                if (lane < 2) copy_async<4>(&to.scale[lane][warp], (lane ? e.vs : e.ms) + ((at + ahead) >> kBlockLog));
             } else {
-                fetch_words<2>(&to.state[0][warp][lane], (const uint4*)(m + d * step) - lane);
-                fetch_words<2>(&to.state[1][warp][lane], (const uint4*)(v + d * step) - lane);
+                fetch_words<2>(&to.state[0][warp][lane], (const uint4*)(m + ahead) - lane);
+                fetch_words<2>(&to.state[1][warp][lane], (const uint4*)(v + ahead) - lane);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");       // (an empty group keeps the count)
@@ -451,10 +526,10 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int c
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(stages[i], i);
 #pragma unroll 1
-    for (int n = 0; n < chunks; n += kAhead) {
+    while (left > 0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (n + i >= chunks) break;
+            if (left <= 0) break;
             Stage& from = stages[i];
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             __syncwarp();                            // the other lanes' copies
@@ -474,13 +549,19 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int c
             fetch(from, kAhead);
             if constexpr (EIGHT) {
                 uint32_t mw[2], rw[2];
-                step8(x, mb, rb, s0, s1, c, f, rate, keep, Dither(at, key), mw, rw);
+                float mi;
+                const Dither dither(at, key);
+                step8<ALL>(x, mb, rb, s0, mi, s1, c, f, rate, keep, dither, mw, rw);
                 store_values(p, true, 8, x.p);
-                *reinterpret_cast<uint2*>(m) = make_uint2(mw[0], mw[1]);
                 *reinterpret_cast<uint2*>(v) = make_uint2(rw[0], rw[1]);
+                if (!ALL) {
+                    if (const uint32_t mask = small_codes(mw, x.m, mi)) dither_small(mask, g, m, e.ms + (at >> kBlockLog), c, f, mi, dither, mw);
+                    __syncwarp();                    // all lanes have read the old scale
+                }
+                *reinterpret_cast<uint2*>(m) = make_uint2(mw[0], mw[1]);
                 if (lane == 0) {
-                    *ms = s0;
-                    *vs = s1;
+                    e.ms[at >> kBlockLog] = s0;
+                    e.vs[at >> kBlockLog] = s1;
                 }
             } else {
                 step32(x, c, f, rate, keep);
@@ -494,12 +575,9 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int c
             }
             at += step;
             p += step;
-            pw += pc;
-            gw += gc;
+            g += step;
             m += step;
             v += step;
-            ms += sc;
-            vs += sc;
             --left;
         }
     }
@@ -512,9 +590,10 @@ static_assert(kStepCtas * (kStepShared + 1024) <= 228 * 1024, "shared memory of 
 // Which states the tensors of a list have.
 enum : int { kAll32 = 1, kAll8 = 2, kMixed = 3 };
 
-template <int CAP, int KIND>
+// (with DEV the constants are read from memory; as parameters they take no registers)
+template <int CAP, int KIND, bool DEV>
 __global__ void __launch_bounds__(kThreads, kStepCtas)
-    adamw_kernel(const __grid_constant__ Table<CAP> t, const Constants given, const Constants* dev, const float* scale)
+    adamw_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ Constants given, const Constants* dev, const float* scale)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     Stage* stages = reinterpret_cast<Stage*>(smem);
@@ -522,7 +601,9 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
     allow_next();
     const float f = scale ? *scale : 1.f;
     if (f != f) return;
-    const Constants c = dev ? *dev : given;
+    Constants read;
+    if (DEV) read = *dev;
+    const Constants& c = DEV ? read : given;
     const int lane = threadIdx.x & 31;
     const uint32_t step = gridDim.x;
     for (uint32_t chunk = blockIdx.x; chunk < t.chunks;) {
@@ -538,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
             const uint32_t full = (uint32_t)(e.n / kChunk), own = chunk - first;
             const int whole = own < full ? (int)((full - own + step - 1) / step) : 0;      // chunks of this CTA
             if (whole > 0) {
-                const long long at = (long long)own * kChunk + threadIdx.x * kPer, by = (long long)step * kChunk;
+                const long long at = (long long)own * kChunk + threadIdx.x * kPer;
+                const uint32_t by = step * kChunk;     // (the grid is some thousand CTAs)
                 if (KIND != kAll8 && !eight) {
                     if (flags & kParamBf16) {
                         if (flags & kGradBf16) whole_chunks<bf16, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages);
@@ -549,12 +631,17 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
                     }
                 }
                 if (KIND != kAll32 && eight) {
+                    const bool all = c.c1 < kNearest;
                     if (flags & kParamBf16) {
-                        if (flags & kGradBf16) whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
-                        else whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        if (flags & kGradBf16) all ? whole_chunks<bf16, bf16, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
+                                                   : whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        else all ? whole_chunks<bf16, float, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
+                                 : whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
                     } else {
-                        if (flags & kGradBf16) whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
-                        else whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        if (flags & kGradBf16) all ? whole_chunks<float, bf16, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
+                                                   : whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        else all ? whole_chunks<float, float, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
+                                 : whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
                     }
                 }
                 chunk += whole * step;
@@ -576,7 +663,17 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
                 const uint2 mb = load_bytes((const uint8_t*)e.m + at, wide, k), rb = load_bytes((const uint8_t*)e.v + at, wide, k);
                 float ms = e.ms[block], rs = e.vs[block];
                 uint32_t mw[2], rw[2];
-                step8(x, mb, rb, ms, rs, c, f, rate, keep, Dither(at, key), mw, rw);
+                float mi;
+                const Dither dither(at, key);
+                const uint8_t* bytes = (const uint8_t*)e.m + at;
+                if (c.c1 < kNearest) {
+                    step8<true>(x, mb, rb, ms, mi, rs, c, f, rate, keep, dither, mw, rw);
+                } else {
+                    step8<false>(x, mb, rb, ms, mi, rs, c, f, rate, keep, dither, mw, rw);
+                    const uint32_t mask = small_codes(mw, x.m, mi);
+                    if (mask && flags & kGradBf16) dither_small(mask, (const bf16*)e.g + at, bytes, e.ms + block, c, f, mi, dither, mw);
+                    else if (mask) dither_small(mask, (const float*)e.g + at, bytes, e.ms + block, c, f, mi, dither, mw);
+                }
                 __syncwarp();                        // all lanes have read the block's scales
                 if (lane == 0) {
                     e.ms[block] = ms;
@@ -873,17 +970,23 @@ int fill(Table<CAP>& t, int i, int count, const dion_adamw_tensor* tensors, bool
     return i;
 }
 
-template <int CAP, int KIND>
-cudaError_t step_table(const Table<CAP>& t, const Constants& c, const Constants* dev, const float* scale, cudaStream_t st)
+template <int CAP, int KIND, bool DEV>
+cudaError_t step_table_as(const Table<CAP>& t, const Constants& c, const Constants* dev, const float* scale, cudaStream_t st)
 {
     static std::atomic<unsigned long long> attr{0};
-    const cudaError_t e = smem_attr_once((const void*)adamw_kernel<CAP, KIND>, kStepShared, attr);
+    const cudaError_t e = smem_attr_once((const void*)adamw_kernel<CAP, KIND, DEV>, kStepShared, attr);
     if (e != cudaSuccess) return e;
     // Eight times what runs at once, taking chunks in turn: the CTAs at work then read and write side by side, and none
     // ends much later than the others.  262 million bfloat16 values with 8-bit states, before other steps: 501 us, 24 times 525, once 539;
     // with contiguous ranges for each CTA 575.
     const unsigned ctas = (unsigned)std::min<long long>(t.chunks, 8ll * kStepCtas * num_sms());
-    return launch_overlapped("adamw", adamw_kernel<CAP, KIND>, dim3(ctas), dim3(kThreads), kStepShared, st, t, c, dev, scale);
+    return launch_overlapped("adamw", adamw_kernel<CAP, KIND, DEV>, dim3(ctas), dim3(kThreads), kStepShared, st, t, c, dev, scale);
+}
+
+template <int CAP, int KIND>
+cudaError_t step_table(const Table<CAP>& t, const Constants& c, const Constants* dev, const float* scale, cudaStream_t st)
+{
+    return dev ? step_table_as<CAP, KIND, true>(t, c, dev, scale, st) : step_table_as<CAP, KIND, false>(t, c, dev, scale, st);
 }
 
 template <int CAP>
