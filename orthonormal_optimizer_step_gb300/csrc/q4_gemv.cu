@@ -13,7 +13,7 @@
 // inside one group, whose scale then multiplies the accumulated sum.
 //
 // x enters as float16 times a power of two for each row and 128 columns, its
-// largest value there in [2^14, 2^15): bfloat16 exactly (down to 2^-32 of that
+// largest value there in [2^14, 2^15): bfloat16 exactly (down to 2^-31 of that
 // largest value, within 2^-39 of it below), 8-bit rows exactly with the scale that
 // they have, and float32 as two terms (within 2^-24, and 2^-39 of the largest) in
 // columns of their own.  Products of such operands are exact in the float32
@@ -214,8 +214,8 @@ __device__ __forceinline__ float convert_x(uint8_t* at, int pitch)
     const uint32_t half = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = max(amax, __shfl_xor_sync(half, amax, o));
-    // 2^-e takes amax into [2^14, 2^15); for amax below 2^-98 it stays 2^112
-    const uint32_t e = max(amax >> 23, 29u);                       // biased: e - 14 + 127 is e's
+    // 2^-e takes amax into [2^14, 2^15); below 2^-112 it stays 2^126, which takes float32's least numbers to 2^-23
+    const uint32_t e = max(amax >> 23, 15u);                       // biased: e - 14 + 127 is e's
     const float down = __uint_as_float((268u - e) << 23), up = __uint_as_float((e - 14u) << 23);
     uint32_t h[4], l[4];
 #pragma unroll
