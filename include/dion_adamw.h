@@ -77,7 +77,8 @@ typedef struct {
  *   g' = f g                         f = *grad_scale (device; NULL: 1)
  *   m <- beta1 m + (1 - beta1) g'    v <- beta2 v + (1 - beta2) g'^2
  *   p <- (1 - lr wd) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * p is rounded once to its type; 8-bit states are rounded after p has used them.
+ * p is rounded once to its type (float32: p + (u - lr wd p), u the update, so that
+ * a decay below 2^-24 counts, too); 8-bit states are rounded after p has used them.
  * A factor f that is NaN skips the step: nothing is written.
  */
 dion_status dion_adamw_step(int count, const dion_adamw_tensor* tensors, double lr, double beta1, double beta2,

@@ -269,10 +269,20 @@ __device__ __forceinline__ void moments(Values& x, const Constants& c, float f)
 }
 
 // The parameters after the step, for r = sqrt(v) times a power of two and root
-// divided by it.  The quotient is within two
-// units of the last place: an update is a thousandth of the parameter or less.
-__device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], float root, float eps, float rate, float keep)
+// divided by it.  The update carries the errors of an approximate root and
+// reciprocal, 2^-23 of it each.  exact (float32 parameters):
+// the decay is subtracted with the update, p + (u - decay p), since beside one it
+// would be rounded to a multiple of 2^-24 (lr * weight_decay of 1e-7 decays by
+// 1.2e-7 then, 2e-8 not at all, every value in every step); in bfloat16 that is lost
+// in the parameter's own rounding.  An infinite parameter stays.
+__device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], float root, float eps, float rate, float decay, bool exact)
 {
+    const float keep = 1.f - decay;
+    float most = 0.f;
+    if (exact)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = fmaxf(most, fmaxf(fabsf(x.p[j].x), fabsf(x.p[j].y)));
+    const bool finite = most < __uint_as_float(kInfBits);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 d = fma2(r[j], make_float2(root, root), make_float2(eps, eps));
@@ -280,7 +290,16 @@ __device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], floa
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.x) : "f"(d.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.y) : "f"(d.y));
         const float2 u = mul2(mul2(x.m[j], make_float2(-rate, -rate)), i);
-        x.p[j] = fma2(x.p[j], make_float2(keep, keep), u);
+        if (!exact) {
+            x.p[j] = fma2(x.p[j], make_float2(keep, keep), u);
+            continue;
+        }
+        float2 p = add2(x.p[j], fma2(x.p[j], make_float2(-decay, -decay), u));
+        if (!finite) {
+            if (mag_bits(x.p[j].x) == kInfBits) p.x = fmaf(x.p[j].x, keep, u.x);
+            if (mag_bits(x.p[j].y) == kInfBits) p.y = fmaf(x.p[j].y, keep, u.y);
+        }
+        x.p[j] = p;
     }
 }
 
@@ -433,7 +452,8 @@ __device__ __forceinline__ void encode(const float2 (&m)[4], const float2 (&v)[4
 // A step with 8-bit states on what a thread holds; encodes them into mw and rw, with the block's new scales in ms and rs.
 template <bool ALL>
 __device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, float& mi, float& rs, const Constants& c, float f,
-                                          float rate, float keep, const Dither& dither, uint32_t (&mw)[2], uint32_t (&rw)[2])
+                                          float rate, float decay, bool exact, const Dither& dither, uint32_t (&mw)[2],
+                                          uint32_t (&rw)[2])
 {
     float2 r[4];
     e4m3_values(mb, ms, x.m);
@@ -442,11 +462,11 @@ __device__ __forceinline__ void step8(Values& x, uint2 mb, uint2 rb, float& ms, 
     for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], x.v[j]);
     moments(x, c, f);
     encode<ALL>(x.m, x.v, r, dither, ms, mi, rs, mw, rw);
-    parameters(x, r, c.root * (1.f / kRootScale), c.eps, rate, keep);
+    parameters(x, r, c.root * (1.f / kRootScale), c.eps, rate, decay, exact);
 }
 
 // A step with float32 states.
-__device__ __forceinline__ void step32(Values& x, const Constants& c, float f, float rate, float keep)
+__device__ __forceinline__ void step32(Values& x, const Constants& c, float f, float rate, float decay, bool exact)
 {
     float2 r[4];
     moments(x, c, f);
@@ -455,7 +475,7 @@ __device__ __forceinline__ void step32(Values& x, const Constants& c, float f, f
         asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].x) : "f"(x.v[j].x));
         asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j].y) : "f"(x.v[j].y));
     }
-    parameters(x, r, c.root, c.eps, rate, keep);
+    parameters(x, r, c.root, c.eps, rate, decay, exact);
 }
 
 // Whole chunks of a tensor with aligned addresses come through shared memory, each
@@ -496,7 +516,7 @@ __device__ __forceinline__ void read_words(const uint4* from, float2 (&f)[4])
 }
 template <typename P, typename G, bool EIGHT, bool ALL = false>
 __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int left, uint32_t step, const Constants& c, float f, float rate,
-                                             float keep, uint32_t key, Stage* stages)
+                                             float decay, uint32_t key, Stage* stages)
 {
     using S = typename std::conditional<EIGHT, uint8_t, float>::type;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -551,7 +571,7 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int l
                 uint32_t mw[2], rw[2];
                 float mi;
                 const Dither dither(at, key);
-                step8<ALL>(x, mb, rb, s0, mi, s1, c, f, rate, keep, dither, mw, rw);
+                step8<ALL>(x, mb, rb, s0, mi, s1, c, f, rate, decay, sizeof(P) == 4, dither, mw, rw);
                 store_values(p, true, 8, x.p);
                 *reinterpret_cast<uint2*>(v) = make_uint2(rw[0], rw[1]);
                 if (!ALL) {
@@ -564,7 +584,7 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int l
                     e.vs[at >> kBlockLog] = s1;
                 }
             } else {
-                step32(x, c, f, rate, keep);
+                step32(x, c, f, rate, decay, sizeof(P) == 4);
                 store_values(p, true, 8, x.p, true);
                 store_values(m, true, 8, x.m, true);
                 store_values(v, true, 8, x.v, true);
@@ -612,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
         const uint32_t first = t.first[i], stop = i + 1 < t.count ? t.first[i + 1] : t.chunks;
         const uint32_t flags = e.flags;
         const bool wide = flags & kWide;
-        const float rate = c.rate * e.lr_factor, keep = 1.f - c.decay * e.lr_factor * e.decay_factor;
+        const float rate = c.rate * e.lr_factor, decay = c.decay * e.lr_factor * e.decay_factor;
         const uint32_t key = mix(c.key ^ e.index);
         const bool eight = KIND == kMixed ? flags & kState8 : KIND == kAll8;
         if (flags & (eight ? kWide : kWhole)) {
@@ -623,25 +643,25 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
                 const uint32_t by = step * kChunk;     // (the grid is some thousand CTAs)
                 if (KIND != kAll8 && !eight) {
                     if (flags & kParamBf16) {
-                        if (flags & kGradBf16) whole_chunks<bf16, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages);
-                        else whole_chunks<bf16, float, false>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        if (flags & kGradBf16) whole_chunks<bf16, bf16, false>(e, at, whole, by, c, f, rate, decay, key, stages);
+                        else whole_chunks<bf16, float, false>(e, at, whole, by, c, f, rate, decay, key, stages);
                     } else {
-                        if (flags & kGradBf16) whole_chunks<float, bf16, false>(e, at, whole, by, c, f, rate, keep, key, stages);
-                        else whole_chunks<float, float, false>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        if (flags & kGradBf16) whole_chunks<float, bf16, false>(e, at, whole, by, c, f, rate, decay, key, stages);
+                        else whole_chunks<float, float, false>(e, at, whole, by, c, f, rate, decay, key, stages);
                     }
                 }
                 if (KIND != kAll32 && eight) {
                     const bool all = c.c1 < kNearest;
                     if (flags & kParamBf16) {
-                        if (flags & kGradBf16) all ? whole_chunks<bf16, bf16, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
-                                                   : whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
-                        else all ? whole_chunks<bf16, float, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
-                                 : whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        if (flags & kGradBf16) all ? whole_chunks<bf16, bf16, true, true>(e, at, whole, by, c, f, rate, decay, key, stages)
+                                                   : whole_chunks<bf16, bf16, true>(e, at, whole, by, c, f, rate, decay, key, stages);
+                        else all ? whole_chunks<bf16, float, true, true>(e, at, whole, by, c, f, rate, decay, key, stages)
+                                 : whole_chunks<bf16, float, true>(e, at, whole, by, c, f, rate, decay, key, stages);
                     } else {
-                        if (flags & kGradBf16) all ? whole_chunks<float, bf16, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
-                                                   : whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, keep, key, stages);
-                        else all ? whole_chunks<float, float, true, true>(e, at, whole, by, c, f, rate, keep, key, stages)
-                                 : whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, keep, key, stages);
+                        if (flags & kGradBf16) all ? whole_chunks<float, bf16, true, true>(e, at, whole, by, c, f, rate, decay, key, stages)
+                                                   : whole_chunks<float, bf16, true>(e, at, whole, by, c, f, rate, decay, key, stages);
+                        else all ? whole_chunks<float, float, true, true>(e, at, whole, by, c, f, rate, decay, key, stages)
+                                 : whole_chunks<float, float, true>(e, at, whole, by, c, f, rate, decay, key, stages);
                     }
                 }
                 chunk += whole * step;
@@ -667,9 +687,9 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
                 const Dither dither(at, key);
                 const uint8_t* bytes = (const uint8_t*)e.m + at;
                 if (c.c1 < kNearest) {
-                    step8<true>(x, mb, rb, ms, mi, rs, c, f, rate, keep, dither, mw, rw);
+                    step8<true>(x, mb, rb, ms, mi, rs, c, f, rate, decay, !(flags & kParamBf16), dither, mw, rw);
                 } else {
-                    step8<false>(x, mb, rb, ms, mi, rs, c, f, rate, keep, dither, mw, rw);
+                    step8<false>(x, mb, rb, ms, mi, rs, c, f, rate, decay, !(flags & kParamBf16), dither, mw, rw);
                     const uint32_t mask = small_codes(mw, x.m, mi);
                     if (mask && flags & kGradBf16) dither_small(mask, (const bf16*)e.g + at, bytes, e.ms + block, c, f, mi, dither, mw);
                     else if (mask) dither_small(mask, (const float*)e.g + at, bytes, e.ms + block, c, f, mi, dither, mw);
@@ -684,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas)
             } else {
                 load_values((const float*)e.m + at, wide, k, x.m);
                 load_values((const float*)e.v + at, wide, k, x.v);
-                step32(x, c, f, rate, keep);
+                step32(x, c, f, rate, decay, !(flags & kParamBf16));
                 store_values((float*)e.m + at, wide, k, x.m);
                 store_values((float*)e.v + at, wide, k, x.v);
             }
