@@ -79,6 +79,7 @@ typedef struct {
  *   p <- (1 - lr wd) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * p is rounded once to its type (float32: p + (u - lr wd p), u the update, so that
  * a decay below 2^-24 counts, too); 8-bit states are rounded after p has used them.
+ * An eps between zero and 2^-126 counts as 2^-126.
  * A factor f that is NaN skips the step: nothing is written.
  */
 dion_status dion_adamw_step(int count, const dion_adamw_tensor* tensors, double lr, double beta1, double beta2,

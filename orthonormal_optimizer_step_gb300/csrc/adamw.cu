@@ -85,7 +85,8 @@ __host__ __device__ inline Constants constants(double lr, double b1, double b2, 
     c.c2 = (float)(1.0 - b2);
     c.rate = (float)(lr / (1.0 - pow(b1, (double)step)));
     c.root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)step)));
-    c.eps = (float)eps;
+    // (reciprocals take subnormal numbers for zero, and nothing times their infinity is no number)
+    c.eps = eps > 0 ? fmaxf((float)eps, 0x1p-126f) : (float)eps;
     c.decay = (float)(lr * wd);
     c.key = mix(seed * 0x632BE5ABu + (uint32_t)step);
     c.one = 1.f;
