@@ -283,8 +283,10 @@ def dion_adamw_step(plan, *, step, lr=None, betas=(0.9, 0.999), eps=1e-8, weight
     table, dev = plan._use(), plan.device
     if not isinstance(plan, AdamWPlan):
         raise TypeError("expected a plan of dion_adamw_plan")
-    if not plan.count:
-        return
+    if dev is None:
+        if hyper is None:
+            return
+        dev = _current_device()                    # (a step of nothing counts all the same)
     scale = None
     if grad_scale is not None:
         if grad_scale.dtype is not _F32 or grad_scale.numel() != 1:
