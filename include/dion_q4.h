@@ -61,8 +61,9 @@ typedef enum {
  * 2^-39 of that one at most (float32: by 2^-24 of themselves too); products are
  * exact, summed in float32, a group at a time, in an order that depends on the
  * sizes alone, and rounded once.  Made for few rows: beyond 32 (16 of float32;
- * fewer from k = 12288 on) the weights are read again for each as many.  k = 0 writes
- * zeros, m = 0 or n = 0 nothing.  m up to 65535, k up to 131072.
+ * fewer for k beyond 16384, down to 4 and 2) the weights are read again for each
+ * as many.  k = 0 writes zeros, m = 0 or n = 0 nothing.  m up to 65535, k up to
+ * 131072.
  */
 dion_status dion_q4_matmul(int m, int n, int k, dion_x_type xt, const void* x, long long ldx, const void* sx,
                            long long ldsx, int group, const void* q, long long ldq, const void* s, long long lds,

@@ -563,6 +563,41 @@ int clusters_at_once(int shares)
 template <class C>
 int ctas_of(size_t bytes) { return std::min(C::CTAS, (int)(228 * 1024 / (bytes + 1024))); }
 
+// Chunks of a CTA's share of `chunks` where s CTAs share them; 0: one of them would have none.
+constexpr int share_of(int chunks, int s)
+{
+    const int per = ((chunks + s - 1) / s + kUnit - 1) / kUnit * kUnit;
+    return s > 1 && (chunks + per - 1) / per != s ? 0 : per;
+}
+// Bytes of a CTA's sums that wait for a join: a block's at least.
+template <int MB>
+constexpr size_t hold_bytes() { return std::max(16384, Cfg<MB>::WARPS * 8 * MB * 64); }
+// Shared memory of a CTA: the batches in flight, x, its powers of two, and the warps' sums.
+template <int MB, int GROUP>
+constexpr size_t shared_bytes(int cols, int per, int s)
+{
+    using C = Cfg<MB>;
+    return (size_t)C::WARPS * C::AHEAD * Batch<GROUP, C::BATCH>::BYTES + (size_t)cols * (256 * per + 64 + 128 * C::WARPS) + 32 * MB * per +
+           (s > 1 ? hold_bytes<MB>() : 0);
+}
+template <int MB, int GROUP>
+constexpr bool fits(int cols, int chunks)
+{
+    for (int s = 1; s <= 8; ++s)
+        if (const int per = share_of(chunks, s); per && shared_bytes<MB, GROUP>(cols, per, s) <= kMostShared) return true;
+    return false;
+}
+// What the header says of the weights' being read again.
+constexpr int kLongestOfAllColumns = 16384;
+template <int GROUP>
+constexpr bool all_columns_fit()
+{
+    for (int c = 1; c <= kLongestOfAllColumns / 128; ++c)
+        if (!fits<4, GROUP>(32, c)) return false;
+    return !fits<4, GROUP>(32, kLongestOfAllColumns / 128 + 1);
+}
+static_assert(all_columns_fit<32>() && all_columns_fit<64>() && all_columns_fit<128>(), "longest rows of which 32 columns are one pass");
+
 // How the work is cut, for p.tokens rows a pass: CTAs that share the contraction
 // (returned; 0: x does not fit), warps that share a tile, and a CTA's shared
 // memory.  The cut with the least estimate of an SM's time is taken, in the time
@@ -581,17 +616,14 @@ template <int MB, int GROUP>
 int cut(MatParams& p, size_t& smem)
 {
     using C = Cfg<MB>;
-    constexpr size_t ring = (size_t)C::WARPS * C::AHEAD * Batch<GROUP, C::BATCH>::BYTES;
-    constexpr size_t hold = std::max(16384, C::WARPS * 8 * MB * 64);         // sums that wait for a join: a block's at least
+    constexpr size_t hold = hold_bytes<MB>();
     const int tiles = (int)cdiv(p.n, 16), cols = p.tokens * p.terms;
     float least = 0.f;
     int best = 0;
     for (int s = 1; s <= 8 && (best == 0 || cdiv(p.chunks, s) >= C::BATCH); ++s) {
-        const int per = (int)(cdiv(cdiv(p.chunks, s), kUnit) * kUnit);
-        if (s > 1 && cdiv(p.chunks, per) != s) continue;           // (a share would be empty)
-        // the batches in flight, x, its powers of two, and the warps' sums
-        const size_t bytes = ring + (size_t)cols * (256 * per + 64 + 128 * C::WARPS) + 32 * MB * per + (s > 1 ? hold : 0);
-        if (bytes > kMostShared) continue;
+        const int per = share_of(p.chunks, s);
+        const size_t bytes = shared_bytes<MB, GROUP>(cols, per, s);
+        if (!per || bytes > kMostShared) continue;
         const int at_once = clusters_at_once(s), per_sm = ctas_of<C>(bytes);
         const float x = 0.55f * 16 / C::THREADS * p.tokens * per, join = s > 1 ? 7.f : 0.f;
         for (int split = C::WARPS; split; split /= 2) {
