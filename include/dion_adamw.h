@@ -104,8 +104,9 @@ dion_status dion_grad_norm_workspace_size(int count, size_t* bytes);
  * out[0] = sqrt(sum of g^2 over all tensors), out[1] = min(1, max_norm /
  * (out[0] + 1e-6)), or NaN where the norm is not finite (dion_adamw_step then
  * skips).  Of the list, n, g and g_type are read.  Squares are float32 (a
- * gradient beyond 1.8e19 makes the norm infinite), their sums float64 from a
- * few hundred values on, in a fixed order (the same bits every time).
+ * gradient beyond 1.8e19 makes the norm infinite; below 2^-63 = 1.1e-19 a square is
+ * off by up to 2^-150, and from 2^-75 = 2.6e-23 down it is nothing), their sums
+ * float64 from a few hundred values on, in a fixed order (the same bits every time).
  * max_norm > 0 may be infinite.  workspace: 8-byte aligned; none is used, and
  * it may be NULL, for up to 256 tensors of 2^20 values in all, each counted up to
  * a multiple of 2048.

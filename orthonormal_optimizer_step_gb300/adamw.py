@@ -233,8 +233,8 @@ def dion_grad_norm(grads, *, max_norm=math.inf, out=None, workspace=None, stream
     """(norm, factor) of all gradients of a list or plan, float32 on the device.
 
     factor = min(1, max_norm / (norm + 1e-6)); NaN where the norm is not finite,
-    with which dion_adamw_step does nothing.  Squares are float32, sums float64 in
-    a fixed order."""
+    with which dion_adamw_step does nothing.  Squares are float32 (gradients from 2e-23 to
+    1.8e19 count), sums float64 in a fixed order."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return dion_grad_norm(grads, max_norm=max_norm, out=out, workspace=workspace)
