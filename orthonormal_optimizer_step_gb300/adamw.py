@@ -4,8 +4,14 @@ For what the orthonormal step does not take: embeddings, output heads, norm
 weights, biases.  A plan holds the list of tensors, checked once, as the table
 that the library reads; a program makes it when it sets up its optimizer and
 keeps it.  `set_gradients` gives it new gradient tensors where a program does
-not keep theirs.  All tensors of a plan are on one device, which is the current
-one when a call uses it.
+not keep theirs (a step captured before that reads the old ones' memory, which the
+program has to keep then).  All tensors of a plan are on one device, which is the
+current one when a call uses it.
+
+These checks are host time: for 65 tensors a plan takes 0.6 to 1 ms, a gradient
+list 0.12 and `set_gradients` 0.2, beside calls of 6 to 9 us.  A program whose
+gradients are new tensors in each step pays the last one in each step; one that
+zeroes them in place does not.
 
     first, second = dion_adamw_state(params, bits=8)             # or 32
     plan = dion_adamw_plan(params, grads, first, second)
@@ -270,7 +276,7 @@ def dion_adamw_step(plan, *, step, lr=None, betas=(0.9, 0.999), eps=1e-8, weight
 
     step: the number of this step, from 1.  grad_scale: a float32 CUDA tensor whose
     one value multiplies the gradients (NaN: nothing is done), as dion_grad_norm
-    leaves it.  seed: of the rounding of 8-bit second moments.
+    leaves it.  seed: of the rounding of 8-bit states.
 
     With `hyper`, a float64 CUDA tensor of (lr, beta1, beta2, eps, weight_decay),
     these are read on the device when the step runs, and `step` is an int64 CUDA

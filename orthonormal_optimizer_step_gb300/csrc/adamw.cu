@@ -12,7 +12,9 @@
 // bfloat16 parameters and gradients, 274 with float32 ones, 0.99 to 1.01 of the
 // time of a copy of as many bytes.  With 8-bit states and bfloat16 the arithmetic
 // of a value (decoding, roots, dither, encoding) fills three quarters of the issue
-// slots: 126 us for 67 million, 0.79 of the copy's rate (float32 parameters 0.97).
+// slots: 133 us for 67 million, 0.75 of the copy's rate (float32 parameters 0.99).
+// Where all first moments are dithered (1 - beta1 below 3/32), 262 million take 510
+// us instead of 485.
 // The norm of 436 MB takes 69 us (0.92).
 #include <algorithm>
 #include <cmath>
@@ -521,7 +523,8 @@ __device__ __forceinline__ void whole_chunks(const Entry& e, long long at, int l
 {
     using S = typename std::conditional<EIGHT, uint8_t, float>::type;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // (of all these addresses only what changes is kept: registers decide about spills here)
+    // (scales' and words' addresses are formed anew: kept, they spill, 262 million bfloat16 values with 8-bit states 491 us
+    // and 67 million float32 ones 172 instead of 485 and 160)
     P* p = (P*)e.p + at;
     const G* g = (const G*)e.g + at;                 // (this thread's eight values; as are the next)
     S* m = (S*)e.m + at;
@@ -611,7 +614,8 @@ static_assert(kStepCtas * (kStepShared + 1024) <= 228 * 1024, "shared memory of 
 // Which states the tensors of a list have.
 enum : int { kAll32 = 1, kAll8 = 2, kMixed = 3 };
 
-// (with DEV the constants are read from memory; as parameters they take no registers)
+// (with DEV the constants are read from memory; as parameters they take no registers: 262 million bfloat16 values with
+// 8-bit states 485 us instead of 491)
 template <int CAP, int KIND, bool DEV>
 __global__ void __launch_bounds__(kThreads, kStepCtas)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ Constants given, const Constants* dev, const float* scale)
@@ -1019,8 +1023,8 @@ cudaError_t step_some(int& i, int count, const dion_adamw_tensor* tensors, const
     if (t.chunks == 0) return cudaSuccess;
     int kind = 0;
     for (int k = 0; k < t.count; ++k) kind |= t.e[k].flags & kState8 ? kAll8 : kAll32;
-    // A kernel of one kind of states has the registers for it: 262 million bfloat16 values with 8-bit states 472 us, in the mixed
-    // one, which spills, 486.
+    // A kernel of one kind of states has the registers for it: 262 million bfloat16 values with 8-bit states 485 us, in the mixed
+    // one 495.
     return kind == kAll32 ? step_table<CAP, kAll32>(t, c, dev, scale, st) : kind == kAll8 ? step_table<CAP, kAll8>(t, c, dev, scale, st)
                                                                                           : step_table<CAP, kMixed>(t, c, dev, scale, st);
 }

@@ -164,3 +164,29 @@ def test_what_is_not_finite_has_its_own_code(beta1):
     bad = torch.zeros(n, dtype=torch.bool, device="cuda")
     bad[[3, 300, 400]] = True
     assert torch.equal(torch.isnan(first[0].data.float()), bad) and torch.isfinite(first[0].scale).all()
+
+
+@pytest.mark.parametrize("beta1", [0.9, 0.95])
+def test_mixed_lists_and_device_numbers_have_the_same_bits(beta1):
+    """8-bit states among float32 ones, and with hyperparameters on the device, against a list of their own with numbers."""
+    n, other = 2_000_003, 70_001
+    hyper = torch.tensor([1e-3, beta1, 0.999, 1e-8, 0.1], dtype=torch.float64, device="cuda")
+    runs = []
+    for mixed, device in ((False, False), (True, False), (False, True), (True, True)):
+        first, second, gen = states(n, 3)
+        g = torch.randn(n, generator=gen, device="cuda") * 1e-3
+        g[::3] *= 1e-5
+        p = torch.randn(n, generator=gen, device="cuda")
+        lists = [p], [g], [first], [second]
+        if mixed:
+            more = [torch.randn(other, generator=gen, device="cuda") for _ in range(3)]
+            for to, x in zip(lists, (*more, more[0].square())):
+                to.append(x)
+        plan = od.dion_adamw_plan(*lists)
+        if device:
+            od.dion_adamw_step(plan, step=torch.full((1,), 6, dtype=torch.int64, device="cuda"), hyper=hyper, seed=4)
+        else:
+            od.dion_adamw_step(plan, step=7, lr=1e-3, betas=(beta1, 0.999), weight_decay=0.1, seed=4)
+        runs.append([p, first.data.view(torch.uint8), first.scale, second.data.view(torch.uint8), second.scale])
+    for run in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], run))
