@@ -120,8 +120,8 @@ def dion_q4_dequantize(w, *, out=None, out_dtype=_BF16, stream=None):
 
 
 def dion_q4_matmul(x, w, *, out=None, out_dtype=_BF16, stream=None):
-    """x w^T [..., rows of w] for a few rows of x, [..., cols] in float32 or bfloat16, or a Q8 matrix
-    (what dion_rms_norm_q8 returns); w a Q4.  Sums are float32, rounded once to out_dtype
+    """x w^T [..., rows of w] for a few rows of x, [..., cols] of two dimensions or more in float32 or
+    bfloat16, or a Q8 matrix (what dion_rms_norm_q8 returns); w a Q4.  Sums are float32, rounded once to out_dtype
     (bfloat16 or float32; that of `out` if given)."""
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import threading
 from typing import NamedTuple
 
@@ -110,7 +111,7 @@ def _matrix(t, what):
         if t.dim() < 2:
             raise ValueError(f"{what} must have at least two dimensions")
         try:
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1])
+            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(math.prod(t.shape[:-1]), t.shape[-1])
         except RuntimeError:
             raise ValueError(f"{what} must be viewable as a matrix of rows") from None
     return t, _pitch(*t.shape, *t.stride(), what)
