@@ -56,17 +56,17 @@ typedef enum {
 
 /*
  * y (m x n, type ydt, pitch ldy) = x W^T, x (m x k, pitch ldx; sx, ldsx: the
- * scales of 8-bit rows, else ignored) and W a 4-bit matrix n x k.  x is exact
- * but for values far below the largest of a row's 128 columns, which are off by
- * 2^-39 of that one at most (float32: by 2^-24 of themselves too); products are
- * exact, summed in float32, a group at a time, in an order that depends on the
- * sizes alone, and rounded once.  A group's sum meets its scale before x's power
- * of two (the largest of 128 columns is raised to 2^14 .. 2^15): a scale below
- * 2^102, of weights below 3.5e31, cannot overflow there; a larger one may give an
- * infinity where x is small enough for a finite result.  Made for few rows: beyond 32 (16 of float32;
- * fewer for k beyond 16384, down to 4 and 2) the weights are read again for each
- * as many.  k = 0 writes zeros, m = 0 or n = 0 nothing.  m up to 65535, k up to
- * 131072.
+ * scales of 8-bit rows, else ignored) and W a 4-bit matrix n x k.  x is exact but
+ * for values far below the largest of a row's 128 columns, which are off by 2^-39
+ * of that one at most (float32: by 2^-24 of themselves too); products are exact,
+ * summed in float32, a group at a time, in an order that depends on the sizes
+ * alone, and rounded once.  A group's sum meets its scale before x's power of two
+ * (the largest of 128 columns is raised to between 2^14 and 2^15): a scale below 2^102, of
+ * weights below 3.5e31, cannot overflow there; a larger one may give an infinity
+ * where x is small enough for a finite result.  Made for few rows: beyond 32 (16
+ * of float32; fewer for k beyond 16384, down to 4 and 2) the weights are read
+ * again for each as many.  k = 0 writes zeros, m = 0 or n = 0 nothing.  m up to
+ * 65535, k up to 131072.
  */
 dion_status dion_q4_matmul(int m, int n, int k, dion_x_type xt, const void* x, long long ldx, const void* sx,
                            long long ldsx, int group, const void* q, long long ldq, const void* s, long long lds,

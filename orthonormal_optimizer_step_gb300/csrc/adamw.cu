@@ -273,11 +273,11 @@ __device__ __forceinline__ void moments(Values& x, const Constants& c, float f)
 
 // The parameters after the step, for r = sqrt(v) times a power of two and root
 // divided by it.  The update carries the errors of an approximate root and
-// reciprocal, 2^-23 of it each.  exact (float32 parameters):
-// the decay is subtracted with the update, p + (u - decay p), since beside one it
-// would be rounded to a multiple of 2^-24 (lr * weight_decay of 1e-7 decays by
-// 1.2e-7 then, 2e-8 not at all, every value in every step); in bfloat16 that is lost
-// in the parameter's own rounding.  An infinite parameter stays.
+// reciprocal, 2^-23 of it each.  exact (float32 parameters): the decay is subtracted
+// with the update, p + (u - decay p), since beside one it would be rounded to a
+// multiple of 2^-24 (lr * weight_decay of 1e-7 decays by 1.2e-7 then, 2e-8 not at
+// all, every value in every step); in bfloat16 that is lost in the parameter's own
+// rounding.  An infinite parameter stays.
 __device__ __forceinline__ void parameters(Values& x, const float2 (&r)[4], float root, float eps, float rate, float decay, bool exact)
 {
     const float keep = 1.f - decay;
@@ -331,8 +331,8 @@ __device__ __forceinline__ float2 roots(float2 v)
 // Where a first moment is rounded by its dither.  Rounded to nearest, a value that a
 // step changes by less than half the format's distance there stays what it was, in
 // every step: one whose gradient has stopped would never reach zero, while its root
-// goes on falling to the least code, and the parameter would move for ever.  A
-// distance is a ninth to a sixteenth of a value, so
+// goes on falling to the least code, and the parameter would move for ever.  The
+// next value down is a ninth to a sixteenth away, so
 //  - with 1 - beta1 >= 3/32 the decay alone takes every value from 2^-6 on to
 //    another one.  Below, all distances are 2^-9, and a value is dithered where the
 //    gradient's part is at most that (with a larger part nearest rounding does move
